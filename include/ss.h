@@ -386,6 +386,82 @@ ss_status ss_spgemm_tiled_block(int64_t M, int64_t N, int64_t Kc, const void* tv
                                 const void* dense, int64_t ldd, const float* sx, const float* sw, ss_dtype y_dt,
                                 void* Y, int64_t ldy, void* stream);
 
+/* ---- Between the products of a layer -----------------------------------------
+ * Rotary positions and attention on the outputs of the query/key/value product,
+ * in place of a trip out of the library between two products. The attention
+ * keeps both of its products dense; ss_spgemm_tiled_batched is the form with a
+ * pruned operand (deep reading of arXiv 2610.28947, introduction). Strides are
+ * in elements; the values of a head are adjacent. */
+
+typedef enum {
+  SS_ROPE_NONE = 0,   /* f_i = base^(-2i / rot_dim) */
+  SS_ROPE_LINEAR = 1, /* f_i / factor */
+  SS_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  SS_ROPE_SMOOTH = 3, /* by turns over the original context, t_i = original * f_i / 2 pi: f_i where t_i >= high,
+                         f_i / factor where t_i <= low, between them linear in t_i */
+  SS_ROPE_YARN = 4    /* by a linear ramp over i: f_i up to the pair that turns `high` times over the original
+                         context (rounded down), f_i / factor from the one that turns `low` times (rounded up);
+                         mscale = 0.1 ln(factor) + 1 */
+} ss_rope_scaling;
+typedef enum {
+  SS_ROPE_HALF = 0,       /* pair i = values (i, i + rot_dim / 2) */
+  SS_ROPE_INTERLEAVED = 1 /* pair i = values (2i, 2i + 1) */
+} ss_rope_layout;
+
+/* ss_rotary_steps -- the frequencies of ss_rotary, computed on the host (no
+ * launch, no device needed): steps[i] = round(f_i / 2 pi * 2^64) modulo 2^64,
+ * rot_dim / 2 values into HOST memory (the caller copies them to the device
+ * once), and *mscale (1 except for YARN). rot_dim even, >= 2; base, factor
+ * finite and > 0; SMOOTH and YARN need original > 0 and 0 < low < high, YARN
+ * base > 1 as well (SS_ERR_SHAPE otherwise). */
+ss_status ss_rotary_steps(int rot_dim, double base, ss_rope_scaling scaling, double factor, double original,
+                          double low, double high, uint64_t* steps, float* mscale);
+
+/* ss_rotary -- rotary positions: of each head's D values the first rot_dim are
+ * turned in pairs by the angle of their token, t = 2 pi pos * steps / 2^64:
+ *   (a, b) -> mscale (a cos t - b sin t, b cos t + a sin t),
+ * the others are copied. inverse != 0 turns by -t (the transpose, which is
+ * also the gradient). x [T][H][D], y likewise, x_dt BF16 or F32 (rounded once);
+ * token and head strides sxt, sxh / syt, syh >= 0. pos: T int32, any values.
+ * steps: rot_dim / 2 device words of ss_rotary_steps, 8-byte aligned;
+ * 2 <= rot_dim <= D, even. mscale finite. y may be x with the same strides (in
+ * place), else the two must not overlap. x and y need the alignment of their
+ * elements only; 16-byte vectors are used where pointers, strides and sizes
+ * allow. */
+ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t D, int64_t sxt, int64_t sxh,
+                    const int32_t* pos, const uint64_t* steps, int64_t rot_dim, ss_rope_layout layout, float mscale,
+                    int inverse, void* y, int64_t syt, int64_t syh, void* stream);
+
+/* ss_attn -- attention of packed sequences with grouped heads:
+ *   o[i][a] = sum_j p_j v[j][a / G], p = softmax over the seen keys j of
+ *   scale * q[i][a] . k[j][a / G], G = Hq / Hkv,
+ * q, o [Tq][Hq][D], k, v [Tk][Hkv][D], all BF16, float32 inside (the
+ * probabilities are rounded to bf16 for the second product).
+ *   Sequences: b = 0 .. B-1 has query rows cu_q[b] .. cu_q[b+1]-1 and key rows
+ * cu_k[b] .. cu_k[b+1]-1 (int32 device arrays of B+1 non-decreasing values;
+ * NULL with B = 1: all rows). k_len (NULL or B int32) keeps only the first
+ * k_len[b] key rows, for caches with room behind them. Values outside the
+ * tensors are clamped to them.
+ *   Mask: causal = 0 sees every key of the sequence; causal = 1 aligns the
+ * last query row with the last key: row i of lq sees keys 0 .. i + lk - lq. A
+ * row that sees no key gives zeros (and lse -inf). Query rows in no sequence
+ * leave o and lse untouched; key rows in no sequence or behind k_len are never
+ * part of a result, whatever they hold.
+ *   lse: NULL, or [Hq][Tq] floats that receive the natural logarithm of each
+ * row's sum of exp(scale * q . k).
+ *   8 <= D <= 128, D % 8 == 0 (SS_ERR_UNSUPPORTED otherwise), Hq % Hkv == 0, scale finite and
+ * > 0. Pointers and strides 16-byte aligned (strides >= 0, token strides of k and v below 2^24).
+ *   workspace: ss_attn_workspace_bytes bytes (16-byte aligned; NULL where that
+ * is 0), as for ss_spgemm_tiled_ws: no initialisation, undefined afterwards,
+ * calls that share one must be stream-ordered. It serves calls with few query
+ * rows per sequence (single tokens over a cache), which split the keys over
+ * workgroups and join the parts in a fixed order in a second kernel. */
+int64_t ss_attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                  int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
+                  int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
+                  const int32_t* k_len, float scale, int causal, void* workspace, int64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

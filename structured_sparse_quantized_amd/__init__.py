@@ -22,6 +22,10 @@ Functions keep the names of the C entry points:
         (takes a workspace from torch when ss_spgemm_tiled_workspace_bytes asks for one)
     spgemm_tiled_workspace_bytes(side, M, N, Kc, dtype) -> int
     spgemm_tiled_noalloc(side, M, N, Kc, tvals, tmeta, dense, sx, sw, y_dtype) -> Y  (static scratch, no workspace)
+    rotary_steps(rot_dim, base, scaling, ...)   -> (steps, mscale)
+    rotary(x, pos, steps, layout, mscale)       -> y [T, H, D]
+    attn(q, k, v, cu_q, cu_k, k_len, causal)    -> o [Tq, Hq, D]  (workspace from torch when ss_attn_workspace_bytes
+                                                   asks for one)
 """
 from __future__ import annotations
 
@@ -78,10 +82,18 @@ lib.ss_spgemm_tiled_batched.argtypes = [_int, _i64, _i64, _i64, _i64, _int, _vp,
                                         _i64, _fp, _i64, _int, _vp, _i64, _i64, _vp]
 lib.ss_quant_lift_spgemm_decode.argtypes = [_vp, _int, _i64, _i64, _i64, _int, _int, _vp, _vp, _fp, _i64, _int, _vp, _i64,
                                             _fp, _vp]
+lib.ss_rotary_steps.argtypes = [_int, ctypes.c_double, _int, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                ctypes.c_double, _vp, _vp]
+lib.ss_rotary.argtypes = [_vp, _int, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _int, ctypes.c_float, _int, _vp, _i64,
+                          _i64, _vp]
+lib.ss_attn_workspace_bytes.argtypes = [_i64] * 6
+lib.ss_attn_workspace_bytes.restype = _i64
+lib.ss_attn.argtypes = [_vp, _i64, _i64] * 4 + [_fp] + [_i64] * 6 + [_vp, _vp, _vp, ctypes.c_float, _int, _vp, _i64, _vp]
 for _f in ("ss_prune24", "ss_slide_decompose", "ss_quant_lift_act", "ss_prune24_act", "ss_spgemm", "ss_pack_sparse",
            "ss_prune24_act_tiled", "ss_slide_decompose_tiled", "ss_spgemm_tiled", "ss_spgemm_tiled_ws",
            "ss_spgemm_tiled_noalloc", "ss_prune24_block", "ss_quant_group_act", "ss_spgemm_tiled_block",
-           "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill"):
+           "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill", "ss_rotary_steps", "ss_rotary",
+           "ss_attn"):
     getattr(lib, _f).restype = _int
 
 EXPORTS = ("ss_lifted_k", "ss_lifted_k_logical", "ss_status_string", "ss_last_error", "ss_version",
@@ -89,7 +101,8 @@ EXPORTS = ("ss_lifted_k", "ss_lifted_k_logical", "ss_status_string", "ss_last_er
            "ss_tiled_vals_bytes", "ss_tiled_meta_bytes", "ss_pack_sparse", "ss_prune24_act_tiled",
            "ss_slide_decompose_tiled", "ss_spgemm_tiled", "ss_spgemm_tiled_workspace_bytes", "ss_spgemm_tiled_ws",
            "ss_spgemm_tiled_noalloc", "ss_prune24_block", "ss_quant_group_act", "ss_spgemm_tiled_block",
-           "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill")
+           "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill",
+           "ss_rotary_steps", "ss_rotary", "ss_attn_workspace_bytes", "ss_attn")
 
 
 class SSError(RuntimeError):
@@ -553,3 +566,136 @@ def spgemm_tiled_block(M: int, N: int, Kc: int, tvals: torch.Tensor, tmeta: torc
     _check(lib.ss_spgemm_tiled_block(M, N, Kc, _ptr(tvals), _ptr(tmeta), _ptr(dense), _ld(dense), _ptr(sx), _ptr(sw),
                                      y, _ptr(Y), _ld(Y), _stream(dense.device)))
     return Y
+
+
+# ---- between the products of a layer: rotary positions and attention -----------------------------------------
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "smooth": 3, "yarn": 4}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+
+
+def _need_heads(t, shape, name: str) -> None:
+    """A [tokens, heads, D] view of this shape whose heads are contiguous."""
+    if t.dim() != 3 or tuple(t.shape) != tuple(shape) or (t.numel() > 0 and shape[2] > 1 and t.stride(2) != 1):
+        raise SSError(SS_ERR_SHAPE, f"{name}: needs {list(shape)} with unit stride along the last dimension, has "
+                      f"{list(t.shape)} with strides {list(t.stride())}")
+
+
+def _need_ints(t, n: int, name: str, device) -> None:
+    if t is None:
+        return
+    _need_dtype(t, torch.int32, name)
+    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise SSError(SS_ERR_SHAPE, f"{name}: needs {n} contiguous int32 values, has {list(t.shape)}")
+    _same_device(device, **{name: t})
+
+
+def _same_device(device, **ts) -> None:
+    for name, t in ts.items():
+        if t is not None and t.device != device:
+            raise SSError(SS_ERR_UNSUPPORTED, f"{name} is on {t.device}, the call runs on {device}")
+
+
+class _on_device:
+    """Makes a tensor's GPU the current one for a call: kernels launch on the current GPU."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.index != self.back:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.index != self.back:
+            torch.cuda.set_device(self.back)
+
+
+def rotary_steps(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0,
+                 low: float = 1.0, high: float = 4.0, device="cuda"):
+    """The frequencies of `rotary` on `device` (int64 [rot_dim / 2], turns per position times 2^64) and the factor on
+    the turned values. scaling: "none", "linear", "ntk", "smooth" or "yarn" (ss.h, ss_rope_scaling)."""
+    if scaling not in ROPE_SCALING:
+        raise SSError(SS_ERR_UNSUPPORTED, f"scaling {scaling!r}: one of {', '.join(ROPE_SCALING)}")
+    n = max(rot_dim // 2, 1)
+    steps, mscale = (ctypes.c_int64 * n)(), ctypes.c_float()
+    _check(lib.ss_rotary_steps(rot_dim, base, ROPE_SCALING[scaling], factor, original, low, high, steps,
+                               ctypes.byref(mscale)))
+    return torch.tensor(list(steps), dtype=torch.int64, device=device), mscale.value
+
+
+def rotary(x: torch.Tensor, pos: torch.Tensor, steps: torch.Tensor, layout: str = "half", mscale: float = 1.0,
+           inverse: bool = False, out=None):
+    """Rotary positions on x [T, H, D] (bf16 or f32; any token and head strides), rot_dim = 2 * len(steps); pos: int32
+    [T]. out may be x (in place); else it must not overlap x. inverse turns back (the gradient's direction)."""
+    _need_heads(x, x.shape if x.dim() == 3 else (0, 0, 0), "x")
+    T, H, D = x.shape
+    if layout not in ROPE_LAYOUT:
+        raise SSError(SS_ERR_UNSUPPORTED, f"layout {layout!r}: one of {', '.join(ROPE_LAYOUT)}")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise SSError(SS_ERR_DTYPE, f"x: needs bf16 or f32, has {x.dtype}")
+    _need_dtype(steps, torch.int64, "steps")
+    if steps.dim() != 1 or not steps.is_contiguous():
+        raise SSError(SS_ERR_SHAPE, f"steps: needs a contiguous vector, has {list(steps.shape)}")
+    if out is not None:
+        _need_heads(out, (T, H, D), "out")
+        _need_dtype(out, x.dtype, "out")
+    _on_gpu(x, pos, steps, out)
+    _need_ints(pos, T, "pos", x.device)
+    _same_device(x.device, steps=steps, out=out)
+    y = out if out is not None else torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    with _on_device(x.device):
+        _check(lib.ss_rotary(_ptr(x), dtype_code(x.dtype), T, H, D, x.stride(0), x.stride(1), _ptr(pos), _ptr(steps),
+                             2 * steps.numel(), ROPE_LAYOUT[layout], mscale, int(inverse), _ptr(y), y.stride(0),
+                             y.stride(1), _stream(x.device)))
+    return y
+
+
+def attn_workspace_bytes(Tq: int, Tk: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib.ss_attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D))
+
+
+def attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k=None, k_len=None, causal: bool = True,
+         scale=None, out=None, lse=None, workspace=None):
+    """Attention of packed sequences: q [Tq, Hq, D], k and v [Tk, Hkv, D] bf16 (any 16-byte aligned token and head
+    strides), cu_q / cu_k int32 [B + 1] row bounds (None: one sequence), k_len int32 [B] keys in use (caches with
+    room). scale defaults to 1 / sqrt(D). lse: a float32 [Hq, Tq] tensor that receives the rows' log-sum-exp.
+    Calls with few query rows per sequence take a workspace from torch's allocator unless one is passed."""
+    _need_heads(q, q.shape if q.dim() == 3 else (0, 0, 0), "q")
+    _need_heads(k, k.shape if k.dim() == 3 else (0, 0, 0), "k")
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    _need_heads(k, (Tk, Hkv, D), "k")
+    _need_heads(v, (Tk, Hkv, D), "v")
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        _need_dtype(t, torch.bfloat16, name)
+    if out is not None:
+        _need_heads(out, (Tq, Hq, D), "out")
+    _need_dtype(lse, torch.float32, "lse")
+    if lse is not None and (tuple(lse.shape) != (Hq, Tq) or not lse.is_contiguous()):
+        raise SSError(SS_ERR_SHAPE, f"lse: needs contiguous [{Hq}, {Tq}], has {list(lse.shape)}")
+    B = cu_q.numel() - 1 if cu_q is not None else cu_k.numel() - 1 if cu_k is not None else 1
+    if B < 0:
+        raise SSError(SS_ERR_SHAPE, "cu_q and cu_k hold one value more than there are sequences")
+    _on_gpu(q, k, v, cu_q, cu_k, k_len, out, lse, workspace)
+    dev = q.device
+    _need_ints(cu_q, B + 1, "cu_q", dev)
+    _need_ints(cu_k, B + 1, "cu_k", dev)
+    _need_ints(k_len, B, "k_len", dev)
+    _same_device(dev, k=k, v=v, out=out, lse=lse, workspace=workspace)
+    o = out if out is not None else torch.empty((Tq, Hq, D), dtype=q.dtype, device=dev)
+    ws, nbytes = workspace, 0
+    if ws is None:
+        need = attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    elif not ws.is_contiguous():
+        raise SSError(SS_ERR_SHAPE, "workspace is not contiguous")
+    if ws is not None:
+        nbytes = ws.numel() * ws.element_size()
+    with _on_device(dev):
+        _check(lib.ss_attn(_ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+                           v.stride(1), _ptr(o), o.stride(0), o.stride(1), _ptr(lse), Tq, Tk, B, Hq, Hkv, D, _ptr(cu_q),
+                           _ptr(cu_k), _ptr(k_len), D ** -0.5 if scale is None else scale, int(causal), _ptr(ws), nbytes,
+                           _stream(dev)))
+    return o

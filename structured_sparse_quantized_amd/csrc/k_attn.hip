@@ -1,0 +1,335 @@
+// Attention over packed sequences (gfx950): o = softmax(scale q k^T + mask) v, grouped heads, causal or not.
+//
+// Mathematics. One pass over the keys with a running maximum and sum: for a query row, after keys 0..j,
+//   m = max_i s_i, l = sum_i 2^(c s_i - m), O = sum_i 2^(c s_i - m) v_i  (s = q.k, c = scale * log2 e),
+// and o = O / l. A new maximum m' multiplies l and O by 2^(m - m'). m only has to keep the powers in range,
+// so it is raised only when a row's maximum passes it by more than kSlack (the powers then stay below 2^kSlack;
+// their relative precision is the same), which leaves O untouched on almost every tile. Scores, m, l and O are
+// float32; the powers are rounded to bf16 (nearest even) for the second product, because the matrix
+// instructions take bf16 there: with q, k, v in bf16 that adds one rounding of relative size 2^-9 per key,
+// independent over the keys. l sums the powers before that rounding.
+//
+// Rows. The query heads that share a key head read the same keys, so the rows of one (sequence, key head) are
+// all its (token, head) pairs, r = token * G + head-in-group: a tile of rows covers fewer tokens than rows,
+// which also wastes less at the causal edge.
+//
+// Matrix instructions (32x32x16 bf16, operands A: row l%32, positions 8(l/32)..+7; result: column l%32, rows
+// 8(i/4) + 4(l/32) + i%4). Both products are taken transposed: S^T = K Q^T, so a lane holds 16 of 32 scores
+// of one query row (its column) and the row's maximum needs one exchange with lane l^32; and O^T = V^T P^T,
+// whose B operand takes the lane's own powers unmoved, because the order of the reduction is free: position
+// 8h + j of a 16-key step stands for key 4h + j (j < 4) or 8 + 4h + j - 4 (j >= 4) of the step. V^T
+// fragments come out of the row-major V tile in LDS by the transposing LDS read (64 bits per lane: 16 lanes
+// read 4 rows of 16 values and each receives one column).
+#include <math.h>
+
+#include <algorithm>
+
+#include "ss_device.h"
+#include "ss_kernels.h"
+
+namespace ss {
+namespace attn {
+
+#define SS_LDS __attribute__((address_space(3)))
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+constexpr float kSlack = 8.0f;     // in powers of two
+constexpr float kLow = -1.0e30f;   // below every finite score's exponent; 2^(kLow - m) = 0
+constexpr int NW = 4;              // waves per workgroup
+constexpr int BK = 64;             // keys per tile
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uni64(int64_t x) {
+  return ((int64_t)(uint32_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x);
+}
+
+// the value of this lane and of lane l ^ 32, combined
+__device__ __forceinline__ float pair_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// One sequence's share of the call, all uniform. Bounds taken from device memory are clamped to the tensors,
+// so whatever cu_q, cu_k and k_len hold, no access leaves q, k, v or o.
+struct Seq {
+  int64_t q0, k0;  // first query and key row
+  int lq, lk;      // rows
+};
+__device__ __forceinline__ int64_t bound(const int32_t* cu, int i, int64_t n) {  // NULL: one sequence of all rows
+  return cu ? min(max((int64_t)cu[i], (int64_t)0), n) : i == 0 ? 0 : n;
+}
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  Seq s;
+  const int64_t q0 = bound(a.cu_q, b, a.Tq), q1 = max(bound(a.cu_q, b + 1, a.Tq), q0);
+  const int64_t k0 = bound(a.cu_k, b, a.Tk), k1 = max(bound(a.cu_k, b + 1, a.Tk), k0);
+  s.q0 = q0;
+  s.k0 = k0;
+  s.lq = (int)(q1 - q0);
+  s.lk = (int)(k1 - k0);
+  if (a.k_len) s.lk = min(max(a.k_len[b], 0), s.lk);
+  return s;
+}
+
+// Row tiles: sequence b's tiles of BM rows start at slot floor(cu_q[b] G / BM) + b. The slots between two
+// starts are at least the tiles of the sequence (floor(x + n) - floor(x) + 1 >= ceil(n)), so a grid of
+// floor(Tq G / BM) + B slots serves every split of Tq rows into B sequences without the host knowing it; a
+// slot past its sequence's rows has nothing to do. Each wave finds its slot's sequence with one load of cu_q per lane
+// and a ballot per factor of 64 in B. Returns false where there is no tile.
+template <int BM> __device__ __forceinline__ bool find_tile(const AttnArgs& a, int slot, int& b, int& tile) {
+  const int lane = threadIdx.x & 63;
+  auto start = [&](int i) { return bound(a.cu_q, i, a.Tq) * a.G / BM + i; };
+  int lo = 0, n = a.B;
+  while (true) {
+    const int step = (n + 63) / 64;
+    const int i = lane * step;
+    const bool in = i < n && start(lo + min(i, n - 1)) <= slot;
+    const int cnt = __popcll(__ballot(in));
+    if (cnt == 0) return false;
+    lo += (cnt - 1) * step;
+    n = min(step, n - (cnt - 1) * step);
+    if (step == 1) break;
+  }
+  b = uni(lo);
+  tile = uni((int)(slot - start(b)));
+  return tile >= 0;
+}
+
+// LDS tiles are row-major (DP values a row, in 16-byte chunks) with the chunks of a row permuted by an XOR, so
+// that the fragment reads below spread over the banks: a K fragment reads one chunk column of 32 rows, a V
+// fragment 4 chunks of 4 rows.
+template <int DP> struct Lds {
+  static constexpr int CH = DP / 8;  // chunks a row
+  __device__ static int swk(int row) { return row & (CH - 1); }
+  __device__ static int swv(int row) { return DP >= 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
+};
+
+// ---- many rows: tiles of 4 waves x NQ x 32 rows ---------------------------------------------------------------
+template <int DP, int NQ>
+__global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(AttnArgs a, int slots) {
+  constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;  // chunks a row, 16-value steps, 32-value blocks
+  constexpr int BM = NW * NQ * 32;
+  constexpr int KB = BK * DP * 2, TILE = 2 * KB;           // bytes of a K tile; of K and V
+  constexpr int LPW = KB / 1024 / NW;                      // 1 KB loads per wave and operand
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+
+  // Workgroups go to the 8 XCDs round-robin: with the key head as the fast index, the tiles of a head meet in
+  // one L2 (for 8 key heads; in few for other counts). The last rows, which see the most keys under a causal
+  // mask, start first.
+  const int kvh = blockIdx.x % a.Hkv, slot = slots - 1 - blockIdx.x / a.Hkv;
+  int b, tile;
+  if (!find_tile<BM>(a, slot, b, tile)) return;
+  const Seq s = load_seq(a, b);
+  const int nr = s.lq * a.G;  // rows of this sequence and key head
+  if (tile * BM >= nr) return;
+
+  // the keys row r sees: 0 .. lim(r) - 1
+  auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
+  const int r0 = tile * BM + wave * NQ * 32;
+  int row_lim[NQ];
+  bool row_ok[NQ];
+  int64_t row_tok[NQ];
+  int row_head[NQ];
+  v8bf qf[NQ][KST];
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    const int r = min(r0 + u * 32 + l32, nr - 1);
+    row_ok[u] = r0 + u * 32 + l32 < nr;
+    row_lim[u] = lim(r);
+    row_tok[u] = s.q0 + r / a.G;
+    row_head[u] = kvh * a.G + r % a.G;
+    const uint16_t* p = a.q + row_tok[u] * a.sqt + row_head[u] * a.sqh;
+#pragma unroll
+    for (int i = 0; i < KST; ++i) {
+      const int c = 2 * i + h;
+      v4u x = {0, 0, 0, 0};
+      if (DP == a.D || c * 8 < a.D) x = *reinterpret_cast<const v4u*>(p + c * 8);
+      qf[u][i] = __builtin_bit_cast(v8bf, x);
+    }
+  }
+  const int kend = uni(lim(min(tile * BM + BM, nr) - 1));  // keys of the workgroup
+  const int wmin = uni(r0 < nr ? lim(r0) : 0), wmax = uni(r0 < nr ? lim(min(r0 + NQ * 32, nr) - 1) : 0);
+  const int nt = (kend + BK - 1) / BK;
+
+  // DMA of a tile: instruction q of this wave fills bytes 1024 (wave LPW + q) + 16 lane. The buffer resource
+  // starts at the tile and ends behind the sequence's last key: what is read past it is zero, so keys behind a
+  // sequence, whatever they hold, meet the product as zeros. The resource moves with the tile in 64 bits;
+  // lane offsets stay within one tile.
+  uint32_t ofk[4], ofv[4];  // LPW of them
+  static_assert(LPW <= 4, "loads per wave");
+#pragma unroll
+  for (int i = 0; i < LPW; ++i) {
+    const int x = (wave * LPW + i) * 64 + lane, row = x / CH, ck = (x % CH) ^ Lds<DP>::swk(row),
+              cv = (x % CH) ^ Lds<DP>::swv(row);
+    ofk[i] = ck * 8 < a.D ? (uint32_t)row * (uint32_t)a.skt * 2u + ck * 16 : 0xFFFFFF00u;
+    ofv[i] = cv * 8 < a.D ? (uint32_t)row * (uint32_t)a.svt * 2u + cv * 16 : 0xFFFFFF00u;
+  }
+  const uint16_t* kp = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
+  const uint16_t* vp = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
+  auto issue = [&](int t, int slot_bytes) {
+    const int rows = min(s.lk - t * BK, BK);  // >= 1
+    const uint32_t nk = (uint32_t)(rows - 1) * (uint32_t)a.skt * 2u + a.D * 2,
+                   nv = (uint32_t)(rows - 1) * (uint32_t)a.svt * 2u + a.D * 2;
+    const __amdgpu_buffer_rsrc_t rk = rsrc(kp + (int64_t)t * BK * a.skt, nk), rv = rsrc(vp + (int64_t)t * BK * a.svt, nv);
+    SS_LDS uint8_t* dst = (SS_LDS uint8_t*)smem + slot_bytes + wave * LPW * 1024;
+#pragma unroll
+    for (int i = 0; i < LPW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (SS_LDS void*)(dst + i * 1024), 16, ofk[i], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < LPW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (SS_LDS void*)(dst + KB + i * 1024), 16, ofv[i], 0, 0, 0);
+  };
+
+  v16f O[NQ][DB];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    m[u] = kLow;
+    l[u] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) O[u][d] = v16f{};
+  }
+  // this lane's places in a tile: K row l32 (chunk 2 i + h), V row 4 h + (lane % 16) / 4 of a 16-key step
+  const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
+
+  if (nt > 0) issue(0, 0);
+  for (int t = 0; t < nt; ++t) {
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's loads of tile t, and its LDS reads of tile t - 1
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    const int cur = (t & 1) * TILE;
+    if (t + 1 < nt) issue(t + 1, TILE - cur);
+    if (t * BK >= wmax) continue;  // no row of this wave sees this tile
+    const SS_LDS uint8_t* kt = (const SS_LDS uint8_t*)smem + cur;
+    const SS_LDS uint8_t* vt = kt + KB;
+    v16f S[NQ][2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) S[u][kb] = v16f{};
+#pragma unroll
+      for (int i = 0; i < KST; ++i) {
+        const int row = kb * 32 + l32;
+        const v8bf kf = *reinterpret_cast<const SS_LDS v8bf*>(kt + row * DP * 2 + ((2 * i + h) ^ Lds<DP>::swk(row)) * 16);
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) S[u][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u][i], S[u][kb], 0, 0, 0);
+      }
+    }
+    if (t * BK + BK > wmin) {  // some row of this wave does not see the whole tile
+#pragma unroll
+      for (int u = 0; u < NQ; ++u) {
+        const int left = row_lim[u] - t * BK - 4 * h;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (kb * 32 + 8 * (i / 4) + i % 4 >= left) S[u][kb][i] = -INFINITY;
+      }
+    }
+    v8bf P[NQ][4];
+#pragma unroll
+    for (int u = 0; u < NQ; ++u) {
+      float mt = S[u][0][0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) mt = fmaxf(mt, S[u][i / 16][i % 16]);
+      mt = pair_max(mt) * a.c;
+      if (__any(mt > m[u] + kSlack)) {
+        const float mn = fmaxf(m[u], mt), f = __builtin_amdgcn_exp2f(m[u] - mn);
+        m[u] = mn;
+        l[u] *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) O[u][d][i] *= f;
+      }
+      float sum = 0.0f;
+      v4u pk[4];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[u][i / 16][i % 16], a.c, -m[u]));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(S[u][i / 16][i % 16 + 1], a.c, -m[u]));
+        sum += x + y;
+        pk[i / 8][(i % 8) / 2] = pack_bf16x2(x, y);
+      }
+      l[u] += sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) P[u][i] = __builtin_bit_cast(v8bf, pk[i]);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {  // 16 keys each
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        v8bf vf;
+        {
+          const int ra = kk * 16 + vrow, rb = ra + 8, c = d * 4 + vcol;
+          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (SS_LDS v4s*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
+          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (SS_LDS v4s*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
+          vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) O[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, P[u][kk], O[u][d], 0, 0, 0);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int u = 0; u < NQ; ++u) {
+    const float lt = pair_sum(l[u]);
+    const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;  // a row that sees no key: zeros
+    if (a.lse && row_ok[u] && h == 0)
+      a.lse[row_head[u] * a.Tq + row_tok[u]] = lt > 0.0f ? (m[u] + __builtin_amdgcn_logf(lt)) * 0.69314718056f : -INFINITY;
+    uint16_t* op = a.o + row_tok[u] * a.sot + row_head[u] * a.soh;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+#pragma unroll
+      for (int g = 0; g < 4; g += 2) {
+        // lane l holds values 8g + 4h .. +3 and 8(g+1) + 4h .. +3 of its row; exchanged with lane l ^ 32, the
+        // lower lane has 8g .. 8g+7 and the upper 8(g+1) .. 8(g+1)+7
+        uint32_t x[2], y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[e] = pack_bf16x2(O[u][d][4 * g + 2 * e] * inv, O[u][d][4 * g + 2 * e + 1] * inv);
+          y[e] = pack_bf16x2(O[u][d][4 * g + 4 + 2 * e] * inv, O[u][d][4 * g + 5 + 2 * e] * inv);
+        }
+        const auto r0_ = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+        const auto r1_ = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+        const int col = d * 32 + 8 * (g + h);
+        if (row_ok[u] && (DP == a.D || col < a.D))
+          *reinterpret_cast<v4u*>(op + col) = v4u{r0_[0], r1_[0], r0_[1], r1_[1]};
+      }
+    }
+  }
+}
+
+template <int DP, int NQ> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
+  auto kern = prompt_kernel<DP, NQ>;
+  constexpr int lds = 2 * 2 * BK * DP * 2, BM = NW * NQ * 32;
+  const hipError_t e = lds_limit((const void*)kern, lds);
+  if (e != hipSuccess) return e;
+  const int64_t slots = a.Tq * a.G / BM + a.B;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * a.Hkv)), dim3(64 * NW), lds, st, a, (int)slots);
+  return hipGetLastError();
+}
+
+}  // namespace attn
+
+int64_t attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t launch_attn(const AttnArgs& a, void*, hipStream_t st) {
+  return a.D <= 64 ? attn::launch_prompt<64, 2>(a, st) : attn::launch_prompt<128, 2>(a, st);
+}
+
+}  // namespace ss

@@ -4,6 +4,7 @@
 #include <stdarg.h>
 
 #include <atomic>
+#include <cmath>
 #include <stdio.h>
 #include <string.h>
 
@@ -527,6 +528,141 @@ ss_status ss_quant_lift_spgemm_decode(const void* X, ss_dtype x_dt, int64_t M, i
                                                  static_cast<const uint8_t*>(tvals), tmeta, sw, Y, ldy, sx_out,
                                                  (hipStream_t)stream),
                     "ss_quant_lift_spgemm_decode launch");
+}
+
+ss_status ss_rotary_steps(int rot_dim, double base, ss_rope_scaling scaling, double factor, double original,
+                          double low, double high, uint64_t* steps, float* mscale) {
+  if (rot_dim < 2 || rot_dim % 2 != 0) return fail(SS_ERR_SHAPE, "rot_dim=%d must be even and at least 2", rot_dim);
+  if (scaling < SS_ROPE_NONE || scaling > SS_ROPE_YARN) return fail(SS_ERR_UNSUPPORTED, "unknown scaling %d", (int)scaling);
+  if (!(base > 0) || !std::isfinite(base) || !(factor > 0) || !std::isfinite(factor))
+    return fail(SS_ERR_SHAPE, "base and factor must be positive and finite");
+  const bool ctx = scaling == SS_ROPE_SMOOTH || scaling == SS_ROPE_YARN;
+  if (ctx && (!(original > 0) || !std::isfinite(original) || !(low > 0) || !(high > low) || !std::isfinite(high)))
+    return fail(SS_ERR_SHAPE, "this scaling needs original > 0 and 0 < low < high");
+  if (scaling == SS_ROPE_YARN && !(base > 1)) return fail(SS_ERR_SHAPE, "this scaling needs base > 1");
+  if (!steps || !mscale) return fail(SS_ERR_NULL, "steps or mscale is NULL");
+  const long double two_pi = 6.283185307179586476925286766559005768L;
+  const int n = rot_dim / 2;
+  long double bs = base;
+  if (scaling == SS_ROPE_NTK && rot_dim > 2) bs *= powl((long double)factor, (long double)rot_dim / (rot_dim - 2));
+  long double first = 0, last = 0;
+  if (scaling == SS_ROPE_YARN) {
+    auto pair_of = [&](double turns) {  // the (fractional) pair that turns so often over the original context
+      return rot_dim * logl((long double)original / (two_pi * turns)) / (2 * logl((long double)base));
+    };
+    first = fmaxl(0, floorl(pair_of(high)));
+    last = fminl(rot_dim - 1, ceill(pair_of(low)));
+  }
+  for (int i = 0; i < n; ++i) {
+    long double f = powl(bs, -2.0L * i / rot_dim);
+    if (scaling == SS_ROPE_LINEAR) f /= factor;
+    if (ctx) {
+      long double keep;
+      if (scaling == SS_ROPE_SMOOTH) keep = ((long double)original * f / two_pi - low) / ((long double)high - low);
+      else keep = 1 - (i - first) / fmaxl(last - first, 0.001L);
+      keep = fminl(1, fmaxl(0, keep));
+      f = f / factor * (1 - keep) + f * keep;
+    }
+    const long double turns = f / two_pi;
+    const long double frac = turns - floorl(turns);
+    const long double units = rintl(frac * 0x1p64L);
+    steps[i] = units >= 0x1p64L ? 0 : (uint64_t)units;
+  }
+  *mscale = scaling == SS_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  return ok();
+}
+
+ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t D, int64_t sxt, int64_t sxh,
+                    const int32_t* pos, const uint64_t* steps, int64_t rot_dim, ss_rope_layout layout, float mscale,
+                    int inverse, void* y, int64_t syt, int64_t syh, void* stream) {
+  if (x_dt != SS_F32 && x_dt != SS_BF16) return fail(SS_ERR_DTYPE, "x must be F32 or BF16");
+  if (T < 0 || H < 0 || D < 0) return fail(SS_ERR_SHAPE, "negative size");
+  if (layout != SS_ROPE_HALF && layout != SS_ROPE_INTERLEAVED) return fail(SS_ERR_UNSUPPORTED, "unknown layout %d", (int)layout);
+  if (T == 0 || H == 0 || D == 0) return ok();
+  if (rot_dim < 2 || rot_dim > D || rot_dim % 2 != 0)
+    return fail(SS_ERR_SHAPE, "rot_dim=%lld must be even and within 2..%lld", (long long)rot_dim, (long long)D);
+  if (T > 0x7FFFFFFF || H * D > 0x7FFFFFF || H > 0x7FFFFFF || D > 0x7FFFFFF) return fail(SS_ERR_SHAPE, "too large");
+  // the stride of a single token or head is never taken
+  if (T == 1) sxt = syt = D;
+  if (H == 1) sxh = syh = D;
+  if (sxt < 0 || sxh < 0 || syt < 0 || syh < 0) return fail(SS_ERR_SHAPE, "negative stride");
+  if (syh < D || syt < D) return fail(SS_ERR_SHAPE, "y: strides below D=%lld", (long long)D);
+  if (!x || !y || !pos || !steps) return fail(SS_ERR_NULL, "x, y, pos and steps are required");
+  if (x == y && (sxt != syt || sxh != syh)) return fail(SS_ERR_SHAPE, "in place needs equal strides");
+  if (!std::isfinite(mscale)) return fail(SS_ERR_SHAPE, "mscale must be finite");
+  const int es = esize(x_dt);
+  if ((uintptr_t)x % es || (uintptr_t)y % es || (uintptr_t)pos % 4 || (uintptr_t)steps % 8)
+    return fail(SS_ERR_ALIGN, "a pointer is not aligned to its elements");
+  ss::RotaryArgs a{x, y, pos, steps, T, sxt, sxh, syt, syh, (int)H, (int)D, (int)rot_dim, layout == SS_ROPE_HALF,
+                   mscale, inverse ? -mscale : mscale};
+  return hip_status(ss::launch_rotary(x_dt == SS_BF16, a, (hipStream_t)stream), "ss_rotary launch");
+}
+
+int64_t ss_attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  if (Tq < 0 || Tk < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || (Hkv > 0 && Hq % Hkv != 0)) return -1;
+  if (Tq == 0 || Tk == 0 || B == 0 || Hq == 0 || Hkv == 0 || D == 0) return 0;
+  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || B > 0x7FFFFFFF || Hq > 0xFFFF || D > 128 || Tq * (Hq / Hkv) > 0x7FFFFF00LL)
+    return -1;
+  return ss::attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
+}
+
+ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                  int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
+                  int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
+                  const int32_t* k_len, float scale, int causal, void* workspace, int64_t ws_bytes, void* stream) {
+  if (Tq < 0 || Tk < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ws_bytes < 0) return fail(SS_ERR_SHAPE, "negative size");
+  if (Tq == 0 || B == 0 || Hq == 0) return ok();
+  if (Hkv == 0 || Hq % Hkv != 0)
+    return fail(SS_ERR_SHAPE, "%lld query heads do not divide into %lld key heads", (long long)Hq, (long long)Hkv);
+  if (D < 8 || D > 128 || D % 8 != 0) return fail(SS_ERR_UNSUPPORTED, "D=%lld must be a multiple of 8 within 8..128", (long long)D);
+  if (!(scale > 0) || !std::isfinite(scale * 1.5f)) return fail(SS_ERR_SHAPE, "scale must be positive and finite");
+  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL)
+    return fail(SS_ERR_SHAPE, "too large");
+  if ((!cu_q || !cu_k) && B != 1) return fail(SS_ERR_NULL, "cu_q and cu_k are required with %lld sequences", (long long)B);
+  // the stride of a single token or head is never taken
+  if (Tq <= 1) sqt = sot = D;
+  if (Tk <= 1) skt = svt = D;
+  if (Hq <= 1) sqh = soh = D;
+  if (Hkv <= 1) skh = svh = D;
+  struct Op { const char* name; const void* p; int64_t st, sh; bool used; };
+  for (const Op& t : {Op{"q", q, sqt, sqh, true}, Op{"k", k, skt, skh, Tk > 0}, Op{"v", v, svt, svh, Tk > 0},
+                      Op{"o", o, sot, soh, true}}) {
+    if (!t.used) continue;
+    if (!t.p) return fail(SS_ERR_NULL, "%s is NULL", t.name);
+    if (t.st < 0 || t.sh < 0) return fail(SS_ERR_SHAPE, "%s: negative stride", t.name);
+    if (!aligned16(t.p) || t.st % 8 || t.sh % 8)
+      return fail(SS_ERR_ALIGN, "%s: pointer and strides must be 16-byte aligned", t.name);
+  }
+  if (sot < D || soh < D) return fail(SS_ERR_SHAPE, "o: strides below D=%lld", (long long)D);
+  // a tile's lane offsets are 32-bit
+  if (Tk > 0 && (skt >= (1 << 24) || svt >= (1 << 24))) return fail(SS_ERR_UNSUPPORTED, "token strides of k and v must be below 2^24");
+  if ((uintptr_t)cu_q % 4 || (uintptr_t)cu_k % 4 || (uintptr_t)k_len % 4 || (uintptr_t)lse % 4)
+    return fail(SS_ERR_ALIGN, "a pointer is not aligned to its elements");
+  const int64_t need = ss::attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
+  if (need > 0) {
+    if (!workspace) return fail(SS_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+    if (!aligned16(workspace)) return fail(SS_ERR_ALIGN, "workspace is not 16-byte aligned");
+    if (ws_bytes < need) return fail(SS_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  }
+  ss::AttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.k_len = k_len;
+  a.sqt = sqt; a.sqh = sqh; a.skt = skt; a.skh = skh; a.svt = svt; a.svh = svh; a.sot = sot; a.soh = soh;
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.B = (int)B;
+  a.Hkv = (int)Hkv;
+  a.G = (int)(Hq / Hkv);
+  a.D = (int)D;
+  a.c = scale * 1.44269504088896340736f;
+  a.causal = causal != 0;
+  return hip_status(ss::launch_attn(a, need > 0 ? workspace : nullptr, (hipStream_t)stream), "ss_attn launch");
 }
 
 }  // extern "C"

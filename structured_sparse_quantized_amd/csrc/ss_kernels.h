@@ -88,4 +88,32 @@ hipError_t launch_spgemm_tiled_block(int yt, int64_t R, int64_t C, int64_t Kc, c
                                      const void* bd, int64_t ldb_bytes, const float* sx, const float* sw, void* Y,
                                      int64_t ldy, hipStream_t st);
 
+// Attention over packed sequences. Strides in elements (t: token, h: head); q, k, v, o are bf16.
+struct AttnArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  float* lse;  // [Hq][Tq] or NULL
+  const int32_t *cu_q, *cu_k, *k_len;
+  int64_t sqt, sqh, skt, skh, svt, svh, sot, soh;
+  int64_t Tq, Tk;
+  int B, Hkv, G, D;  // G = query heads per key head
+  float c;           // scale * log2 e
+  int causal;
+};
+int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st);
+
+// Rotary positions on [T][H][D] views (strides in elements, t: token, h: head); y may be x (same strides).
+struct RotaryArgs {
+  const void* x;
+  void* y;
+  const int32_t* pos;     // [T]
+  const uint64_t* steps;  // [rot / 2] turns per position * 2^64
+  int64_t T, sxt, sxh, syt, syh;
+  int H, D, rot;
+  int half;  // pairs (i, i + rot / 2), else (2 i, 2 i + 1)
+  float cscale, sscale;
+};
+hipError_t launch_rotary(bool bf16, const RotaryArgs& a, hipStream_t st);
+
 }  // namespace ss
