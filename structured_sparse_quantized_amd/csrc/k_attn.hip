@@ -324,11 +324,282 @@ template <int DP, int NQ> hipError_t launch_prompt(const AttnArgs& a, hipStream_
   return hipGetLastError();
 }
 
+// ---- few rows per sequence: the keys split over waves and workgroups ---------------------------------------------
+// Single tokens over a cache read every key and value once for a handful of rows (HBM bound), so the work is cut
+// along the keys: a tile has 32 rows, each wave takes every FW-th unit of 32 keys of its workgroup's share with a
+// ring of its own in LDS (whole 1 KB DMA loads, no barrier in the loop: a wave waits for its own loads only),
+// and gridDim.y workgroups share a tile's keys. The waves of a workgroup join through LDS, the workgroups through
+// float32 parts (each normalised, with its row's log2 of the sum) that join_kernel adds in order.
+constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
+
+template <int DP, bool SPLIT>
+__global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, float* __restrict__ part) {
+  constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;
+  constexpr int KB = 32 * DP * 2, UNIT = 2 * KB, RING = FR * UNIT;
+  constexpr int LPU = KB / 1024;            // 1 KB loads per unit and operand
+  constexpr int OST = DP * 4 + 16;          // bytes of a joined row, padded
+  static_assert(FM * OST <= RING, "a wave's results fit its ring");
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[FW][2][FM];
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int kvh = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv;
+  int b, tile;
+  if (!find_tile<FM>(a, slot, b, tile)) return;
+  const Seq s = load_seq(a, b);
+  const int nr = s.lq * a.G;
+  if (tile * FM >= nr) return;
+  auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
+  const int r0 = tile * FM, rows = min(nr - r0, FM);
+  const int r = min(r0 + l32, nr - 1);
+  const int row_lim = lim(r);
+  const int kend = uni(lim(r0 + rows - 1)), kmin = uni(lim(r0));
+  const int units = (kend + 31) / 32;
+  const int ulo = (int)((int64_t)units * blockIdx.y / gridDim.y), uhi = (int)((int64_t)units * (blockIdx.y + 1) / gridDim.y);
+
+  uint32_t ofk[8], ofv[8];  // LPU of them
+  static_assert(LPU <= 8, "loads per unit");
+#pragma unroll
+  for (int i = 0; i < LPU; ++i) {
+    const int x = i * 64 + lane, row = x / CH, ck = (x % CH) ^ Lds<DP>::swk(row), cv = (x % CH) ^ Lds<DP>::swv(row);
+    ofk[i] = ck * 8 < a.D ? (uint32_t)row * (uint32_t)a.skt * 2u + ck * 16 : 0xFFFFFF00u;
+    ofv[i] = cv * 8 < a.D ? (uint32_t)row * (uint32_t)a.svt * 2u + cv * 16 : 0xFFFFFF00u;
+  }
+  const uint16_t* kp = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
+  const uint16_t* vp = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
+  SS_LDS uint8_t* ring = (SS_LDS uint8_t*)smem + wave * RING;
+  auto issue = [&](int u, int at) {
+    const int n = min(s.lk - u * 32, 32);  // >= 1
+    const __amdgpu_buffer_rsrc_t rk = rsrc(kp + (int64_t)u * 32 * a.skt, (uint32_t)(n - 1) * (uint32_t)a.skt * 2u + a.D * 2),
+                                 rv = rsrc(vp + (int64_t)u * 32 * a.svt, (uint32_t)(n - 1) * (uint32_t)a.svt * 2u + a.D * 2);
+#pragma unroll
+    for (int i = 0; i < LPU; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (SS_LDS void*)(ring + at + i * 1024), 16, ofk[i], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < LPU; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (SS_LDS void*)(ring + at + KB + i * 1024), 16, ofv[i], 0, 0, 0);
+  };
+
+  if (ulo + wave < uhi) issue(ulo + wave, 0);
+  v8bf qf[KST];
+  {
+    const uint16_t* p = a.q + (s.q0 + r / a.G) * a.sqt + (int64_t)(kvh * a.G + r % a.G) * a.sqh;
+#pragma unroll
+    for (int i = 0; i < KST; ++i) {
+      const int c = 2 * i + h;
+      v4u x = {0, 0, 0, 0};
+      if (DP == a.D || c * 8 < a.D) x = *reinterpret_cast<const v4u*>(p + c * 8);
+      qf[i] = __builtin_bit_cast(v8bf, x);
+    }
+  }
+  v16f O[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) O[d] = v16f{};
+  float m = kLow, l = 0.0f;
+  const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
+
+  int at = 0;
+  for (int u = ulo + wave; u < uhi; u += FW) {
+    if (u + FW < uhi) {
+      issue(u + FW, RING / FR - at);
+      // unit u has landed when only the loads just issued are outstanding (loads complete in order)
+      __builtin_amdgcn_s_waitcnt(((2 * LPU) & 0xF) | (((2 * LPU) >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+    } else {
+      __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xF << 8));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const SS_LDS uint8_t* kt = ring + at;
+    const SS_LDS uint8_t* vt = kt + KB;
+    at = RING / FR - at;
+    v16f S = v16f{};
+#pragma unroll
+    for (int i = 0; i < KST; ++i) {
+      const v8bf kf = *reinterpret_cast<const SS_LDS v8bf*>(kt + l32 * DP * 2 + ((2 * i + h) ^ Lds<DP>::swk(l32)) * 16);
+      S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], S, 0, 0, 0);
+    }
+    if (u * 32 + 32 > kmin) {
+      const int left = row_lim - u * 32 - 4 * h;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * (i / 4) + i % 4 >= left) S[i] = -INFINITY;
+    }
+    float mt = S[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, S[i]);
+    mt = pair_max(mt) * a.c;
+    if (__any(mt > m + kSlack)) {
+      const float mn = fmaxf(m, mt), f = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[d][i] *= f;
+    }
+    v8bf P[2];
+    {
+      v4u pk[2];
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i], a.c, -m));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i + 1], a.c, -m));
+        sum += x + y;
+        pk[i / 8][(i % 8) / 2] = pack_bf16x2(x, y);
+      }
+      l += sum;
+      P[0] = __builtin_bit_cast(v8bf, pk[0]);
+      P[1] = __builtin_bit_cast(v8bf, pk[1]);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const int ra = kk * 16 + vrow, rb = ra + 8, c = d * 4 + vcol;
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (SS_LDS v4s*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (SS_LDS v4s*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
+        const v8bf vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, P[kk], O[d], 0, 0, 0);
+      }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this unit's LDS reads are done before its slot is filled again
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // join the waves: a wave's O goes through its own ring, scaled to the workgroup's maximum
+  if (h == 0) red[wave][0][l32] = m;
+  const float lt = pair_sum(l);
+  if (h == 0) red[wave][1][l32] = lt;
+  __syncthreads();
+  float M = red[0][0][l32];
+#pragma unroll
+  for (int w = 1; w < FW; ++w) M = fmaxf(M, red[w][0][l32]);
+  if (l32 < rows) {
+    const float f = __builtin_amdgcn_exp2f(m - M);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        typedef float v4f __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<SS_LDS v4f*>(ring + l32 * OST + (d * 32 + 8 * g + 4 * h) * 4) =
+            v4f{O[d][4 * g] * f, O[d][4 * g + 1] * f, O[d][4 * g + 2] * f, O[d][4 * g + 3] * f};
+      }
+  }
+  __syncthreads();
+  const int quads = a.D / 4;
+  for (int i = threadIdx.x; i < rows * quads; i += 64 * FW) {
+    const int row = i / quads, c = (i - row * quads) * 4;
+    float M2 = red[0][0][row], L = 0.0f;
+#pragma unroll
+    for (int w = 1; w < FW; ++w) M2 = fmaxf(M2, red[w][0][row]);
+#pragma unroll
+    for (int w = 0; w < FW; ++w) L += red[w][1][row] * __builtin_amdgcn_exp2f(red[w][0][row] - M2);
+    float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < FW; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(smem + w * RING + row * OST + c * 4);
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int rr = r0 + row, head = kvh * a.G + rr % a.G;
+    const int64_t tok = s.q0 + rr / a.G;
+    const float lg = L > 0.0f ? M2 + __builtin_amdgcn_logf(L) : -INFINITY;  // log2 of the row's sum
+    if constexpr (SPLIT) {
+      const int64_t Hq = (int64_t)a.Hkv * a.G, at_row = (blockIdx.y * a.Tq + tok) * Hq + head;
+      *reinterpret_cast<float4*>(part + at_row * a.D + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      if (c == 0) part[(int64_t)gridDim.y * a.Tq * Hq * a.D + at_row] = lg;
+    } else {
+      *reinterpret_cast<uint2*>(a.o + tok * a.sot + head * a.soh + c) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (a.lse && c == 0) a.lse[head * a.Tq + tok] = lg * 0.69314718056f;
+    }
+  }
+}
+
+// o = sum_s w_s part_s, w_s = 2^(lg_s - max) / sum of them: one workgroup per (token, head), 16 bytes a thread,
+// the parts dealt over groups of threads and joined in LDS in a fixed order.
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __restrict__ part, int splits) {
+  __shared__ float4 acc[256];
+  const int Hq = a.Hkv * a.G;
+  const int64_t row = blockIdx.x, tok = row / Hq, n = a.Tq * Hq;
+  const int head = (int)(row - tok * Hq);
+  // rows of no sequence have no parts
+  if (tok < bound(a.cu_q, 0, a.Tq) || tok >= bound(a.cu_q, a.B, a.Tq)) return;
+  const float* lg = part + (int64_t)splits * n * a.D + row;
+  const int lane = threadIdx.x & 63;
+  float M = -INFINITY;
+  for (int s = lane; s < splits; s += 64) M = fmaxf(M, lg[s * n]);
+  M = wave_max(M);
+  float sum = 0.0f;
+  for (int s = lane; s < splits; s += 64) sum += M > -INFINITY ? __builtin_amdgcn_exp2f(lg[s * n] - M) : 0.0f;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const int quads = a.D / 4, groups = 256 / quads, g = threadIdx.x / quads, c = threadIdx.x % quads;
+  float4 o = make_float4(0, 0, 0, 0);
+  if (g < groups && M > -INFINITY) {
+    for (int s = g; s < splits; s += groups) {
+      const float w = __builtin_amdgcn_exp2f(lg[s * n] - M) * inv;
+      const float4 x = *reinterpret_cast<const float4*>(part + (s * n + row) * a.D + c * 4);
+      o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
+    }
+  }
+  acc[threadIdx.x] = o;
+  __syncthreads();
+  if (threadIdx.x < quads) {
+    for (int k = 1; k < groups; ++k) {
+      const float4 x = acc[k * quads + threadIdx.x];
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(a.o + tok * a.sot + head * a.soh + threadIdx.x * 4) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  }
+  if (a.lse && threadIdx.x == 0)
+    a.lse[head * a.Tq + tok] = sum > 0.0f ? (M + __builtin_amdgcn_logf(sum)) * 0.69314718056f : -INFINITY;
+}
+
+// Calls whose sequences have 32 rows or fewer on average go to few_kernel.
+inline bool few_rows(int64_t Tq, int64_t B, int64_t G) { return Tq * G <= FM * B; }
+inline int64_t few_slots(int64_t Tq, int64_t B, int64_t G) { return Tq * G / FM + B; }
+// Workgroups per tile: enough for kFill workgroups a CU, with at least two units of 32 keys for every wave if the
+// keys were spread evenly over the sequences.
+constexpr int kFill = 8;
+inline int splits(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv) {
+  const int64_t wgs = few_slots(Tq, B, G) * Hkv, want = (kFill * (int64_t)num_cus_p() + wgs - 1) / wgs;
+  const int64_t most = Tk / B / (FW * 2 * 32);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 256));
+}
+
+template <int DP> hipError_t launch_few(const AttnArgs& a, void* ws, hipStream_t st) {
+  const int n = splits(a.Tq, a.Tk, a.B, a.G, a.Hkv);
+  const int64_t slots = few_slots(a.Tq, a.B, a.G);
+  constexpr int lds = FW * FR * 2 * 32 * DP * 2;
+  const dim3 grid((unsigned)(slots * a.Hkv), (unsigned)n);
+  auto go = [&](auto kern) -> hipError_t {
+    const hipError_t e = lds_limit((const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, grid, dim3(64 * FW), lds, st, a, (int)slots, static_cast<float*>(ws));
+    return hipGetLastError();
+  };
+  if (n == 1) return go(few_kernel<DP, false>);
+  const hipError_t e = go(few_kernel<DP, true>);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(join_kernel, dim3((unsigned)(a.Tq * a.Hkv * a.G)), dim3(256), 0, st, a, static_cast<const float*>(ws), n);
+  return hipGetLastError();
+}
+
 }  // namespace attn
 
-int64_t attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  const int64_t G = Hq / Hkv;
+  if (Tk == 0 || !attn::few_rows(Tq, B, G)) return 0;
+  const int64_t n = attn::splits(Tq, Tk, B, G, Hkv);
+  return n == 1 ? 0 : n * Tq * Hq * (D + 1) * 4;
+}
 
-hipError_t launch_attn(const AttnArgs& a, void*, hipStream_t st) {
+hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {
+  if (a.Tk > 0 && attn::few_rows(a.Tq, a.B, a.G)) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
   return a.D <= 64 ? attn::launch_prompt<64, 2>(a, st) : attn::launch_prompt<128, 2>(a, st);
 }
 

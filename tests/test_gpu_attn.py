@@ -38,17 +38,17 @@ def _compare(o, lse, ref, norm=True):
     e = np.nan_to_num(size).T[:, :, None] * 8e-5 + 6e-5
     tol = np.nan_to_num(mass) * (2.0 ** -8 + e)
     tol = tol + 2.0 ** -8 * (np.abs(np.nan_to_num(eo)) + tol)
-    err = np.abs(g - eo)
+    err = np.abs(g - np.where(inside, eo, g))
     assert (err <= tol)[inside].all(), f"worst {np.nanmax(err / (tol + 1e-30)):.3g}"
     n = np.linalg.norm(np.nan_to_num(eo))
     if norm and n > 0:
-        assert np.linalg.norm(np.where(inside, g - eo, 0)) <= 2.0 ** -8 * n
+        assert np.linalg.norm(np.where(inside, g - np.nan_to_num(eo), 0)) <= 2.0 ** -8 * n
     if lse is not None:
         gl = lse.double().cpu().numpy()
         lin = ~np.isnan(el)
         assert np.array_equal(np.isneginf(gl[lin]), np.isneginf(el[lin]))
         fin = np.isfinite(el)
-        assert (np.abs(gl - el)[fin] <= (np.nan_to_num(size) * 4e-5 + 2e-5 + np.abs(np.where(fin, el, 0)) * 2.0 ** -22)[fin]).all()
+        assert (np.abs(gl[fin] - el[fin]) <= (np.nan_to_num(size) * 4e-5 + 2e-5 + np.abs(np.where(fin, el, 0)) * 2.0 ** -22)[fin]).all()
 
 
 def _run(ss, lq, lk, Hq, Hkv, D, causal, seed=0, scale=None, amp=1.0):
@@ -89,6 +89,26 @@ def test_grouped_heads(ss, Hq, Hkv):
 @pytest.mark.parametrize("Hq,Hkv,lq,lk", [(8, 1, [500, 37], [500, 90]), (2, 2, [400], [700]), (16, 2, [150, 1, 299], [150, 40, 310])])
 def test_many_tiles(ss, Hq, Hkv, lq, lk):
     _run(ss, lq, lk, Hq, Hkv, 128, True, seed=3)
+
+
+@pytest.mark.parametrize("D", [8, 64, 72, 128])
+@pytest.mark.parametrize("lq,lk", [([1], [5000]), ([1, 1, 1], [3000, 1, 0]), ([4], [4097]), ([3, 1], [33, 6001]), ([2], [1])])
+def test_few_rows_split_over_workgroups(ss, lq, lk, D):
+    _run(ss, lq, lk, 7, 1, D, True, seed=D)
+    _run(ss, lq, lk, 4, 4, D, False, seed=D + 1)
+
+
+def test_own_workspace(ss):
+    """A workspace of the stated size serves; its contents before do not matter."""
+    q = torch.randn((2, 8, 64), device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn((9000, 2, 64), device="cuda").to(torch.bfloat16) for _ in range(2))
+    need = ss.attn_workspace_bytes(2, 9000, 1, 8, 2, 64)
+    assert need > 0
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    o = ss.attn(q, k, v, workspace=ws[:need])
+    assert torch.equal(o, ss.attn(q, k, v)) and (ws[need:] == 255).all()
+    with pytest.raises(ss.SSError):
+        ss.attn(q, k, v, workspace=ws[: need - 1])
 
 
 def test_large_scores(ss):

@@ -129,9 +129,11 @@ def test_attention_refusals():
     assert call(skt=1 << 24) == ss.SS_ERR_UNSUPPORTED
     assert call(B=2, cq=None) == call(B=2, ck=None) == ss.SS_ERR_NULL
     assert call(Tq=0, q=None) == call(B=0) == call(Hq=0, Hkv=0) == ss.SS_OK
-    need = ss.attn_workspace_bytes(8, 8, 1, 4, 2, 16)
-    if need > 0:
-        assert call(ws=None) == ss.SS_ERR_NULL and call(n=need - 1) == ss.SS_ERR_SHAPE and call(ws=odd) == ss.SS_ERR_ALIGN
+    need = ss.attn_workspace_bytes(8, 10000, 1, 4, 2, 16)  # few rows, many keys: split over workgroups
+    few = dict(Tk=10000)
+    assert need > 0 and need % (8 * 4 * 17 * 4) == 0
+    assert call(ws=None, **few) == ss.SS_ERR_NULL and call(n=need - 1, **few) == ss.SS_ERR_SHAPE and call(ws=odd, **few) == ss.SS_ERR_ALIGN
+    assert ss.attn_workspace_bytes(8000, 8000, 1, 4, 2, 16) == 0
     assert ss.lib.ss_attn_workspace_bytes(8, 8, 1, 3, 2, 16) == -1 and ss.attn_workspace_bytes(0, 8, 1, 4, 2, 16) == 0
     t = torch.zeros((4, 2, 16), dtype=torch.bfloat16)
     for bad in (lambda: ss.attn(t, t, t), lambda: ss.attn(t.float(), t, t), lambda: ss.attn(t[0], t, t),
