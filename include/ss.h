@@ -265,6 +265,33 @@ ss_status ss_spgemm_tiled_ws(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_
                              const uint8_t* tmeta, const void* dense, int64_t ldd, const float* sx, const float* sw,
                              ss_dtype y_dt, void* Y, int64_t ldy, void* workspace, int64_t ws_bytes, void* stream);
 
+/* ss_spgemm_tiled_epilogue -- ss_spgemm_tiled_ws with what follows a linear
+ * layer done in its epilogue, so that it costs no pass of its own:
+ *   z[m][n] = fl32(fl32(fl32(float(acc)) * sx[m]) * sw[n]) + bias[n]
+ *   v[m][n] = act(z[m][n]);  gated: v[m][j] = act(z[m][2j]) * z[m][2j + 1]
+ *   Y[m][j] = v[m][j] + residual[m][j], rounded once to y_dt (BF16 or F32),
+ * all in float32. bias: N floats or NULL. residual: [M][columns of Y] of type
+ * y_dt (ldr elements, 16-byte aligned pointer; rows need not be) or NULL; it
+ * may be Y itself with ldr = ldy, and must not overlap Y otherwise. gated != 0
+ * makes Y [M][N / 2] (N even): weight rows 2j and 2j + 1 hold the gate and the
+ * value of column j (a caller interleaves the two matrices before the weight
+ * preparation). Exponentials, where y_dt is BF16, are the chip's own (relative
+ * error below 2^-19 for |z| < 16).
+ * Sides, operands, scales (both for I8 and FP8E4M3), workspace and errors as
+ * ss_spgemm_tiled_ws; the workspace query is the same. */
+typedef enum {
+  SS_ACT_NONE = 0,
+  SS_ACT_RELU = 1,      /* max(z, 0) */
+  SS_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) */
+  SS_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+  SS_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} ss_act;
+ss_status ss_spgemm_tiled_epilogue(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_dtype ab_dt, const void* tvals,
+                                   const uint8_t* tmeta, const void* dense, int64_t ldd, const float* sx,
+                                   const float* sw, const float* bias, ss_act act, int gated, const void* residual,
+                                   int64_t ldr, ss_dtype y_dt, void* Y, int64_t ldy, void* workspace,
+                                   int64_t ws_bytes, void* stream);
+
 /* ss_spgemm_tiled_noalloc -- ss_spgemm_tiled_ws for callers that cannot
  * allocate device memory (code under HIP graph capture, tight serving loops,
  * harnesses that forbid hipMalloc): the split-K partial tiles go to the

@@ -22,6 +22,8 @@ Functions keep the names of the C entry points:
         (takes a workspace from torch when ss_spgemm_tiled_workspace_bytes asks for one)
     spgemm_tiled_workspace_bytes(side, M, N, Kc, dtype) -> int
     spgemm_tiled_noalloc(side, M, N, Kc, tvals, tmeta, dense, sx, sw, y_dtype) -> Y  (static scratch, no workspace)
+    spgemm_tiled_epilogue(side, M, N, Kc, tvals, tmeta, dense, sx, sw, bias, act, gated, residual, y_dtype) -> Y
+        (the product with bias, activation, gate and residual; workspace as spgemm_tiled)
     rotary_steps(rot_dim, base, scaling, ...)   -> (steps, mscale)
     rotary(x, pos, steps, layout, mscale)       -> y [T, H, D]
     attn(q, k, v, cu_q, cu_k, k_len, causal)    -> o [Tq, Hq, D]  (workspace from torch when ss_attn_workspace_bytes
@@ -71,6 +73,8 @@ lib.ss_spgemm_tiled_workspace_bytes.argtypes = [_int, _i64, _i64, _i64, _int]
 lib.ss_spgemm_tiled_workspace_bytes.restype = _i64
 lib.ss_spgemm_tiled_ws.argtypes = [_int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _i64, _fp, _fp, _int, _vp, _i64, _vp,
                                    _i64, _vp]
+lib.ss_spgemm_tiled_epilogue.argtypes = [_int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _i64, _fp, _fp, _fp, _int, _int,
+                                         _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp]
 lib.ss_spgemm_tiled_noalloc.argtypes = [_int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _i64, _fp, _fp, _int, _vp, _i64,
                                         _vp]
 lib.ss_quant_spgemm_prefill.argtypes = [_vp, _int, _i64, _i64, _i64, _int, _vp, _vp, _fp, _i64, _int, _vp, _i64, _fp,
@@ -92,8 +96,8 @@ lib.ss_attn.argtypes = [_vp, _i64, _i64] * 4 + [_fp] + [_i64] * 6 + [_vp, _vp, _
 for _f in ("ss_prune24", "ss_slide_decompose", "ss_quant_lift_act", "ss_prune24_act", "ss_spgemm", "ss_pack_sparse",
            "ss_prune24_act_tiled", "ss_slide_decompose_tiled", "ss_spgemm_tiled", "ss_spgemm_tiled_ws",
            "ss_spgemm_tiled_noalloc", "ss_prune24_block", "ss_quant_group_act", "ss_spgemm_tiled_block",
-           "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill", "ss_rotary_steps", "ss_rotary",
-           "ss_attn"):
+           "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill", "ss_spgemm_tiled_epilogue",
+           "ss_rotary_steps", "ss_rotary", "ss_attn"):
     getattr(lib, _f).restype = _int
 
 EXPORTS = ("ss_lifted_k", "ss_lifted_k_logical", "ss_status_string", "ss_last_error", "ss_version",
@@ -102,7 +106,7 @@ EXPORTS = ("ss_lifted_k", "ss_lifted_k_logical", "ss_status_string", "ss_last_er
            "ss_slide_decompose_tiled", "ss_spgemm_tiled", "ss_spgemm_tiled_workspace_bytes", "ss_spgemm_tiled_ws",
            "ss_spgemm_tiled_noalloc", "ss_prune24_block", "ss_quant_group_act", "ss_spgemm_tiled_block",
            "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill",
-           "ss_rotary_steps", "ss_rotary", "ss_attn_workspace_bytes", "ss_attn")
+           "ss_spgemm_tiled_epilogue", "ss_rotary_steps", "ss_rotary", "ss_attn_workspace_bytes", "ss_attn")
 
 
 class SSError(RuntimeError):
@@ -377,6 +381,49 @@ def spgemm_tiled_noalloc(side: int, M: int, N: int, Kc: int, tvals: torch.Tensor
     Y = out if out is not None else torch.empty((M, N), dtype=_TORCH[y], device=dense.device)
     _check(lib.ss_spgemm_tiled_noalloc(side, M, N, Kc, dtype_code(dense.dtype), _ptr(tvals), _ptr(tmeta), _ptr(dense),
                                        _ld(dense), _ptr(sx), _ptr(sw), y, _ptr(Y), _ld(Y), _stream(dense.device)))
+    return Y
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def spgemm_tiled_epilogue(side: int, M: int, N: int, Kc: int, tvals: torch.Tensor, tmeta: torch.Tensor,
+                          dense: torch.Tensor, sx=None, sw=None, bias=None, act: str = "none", gated: bool = False,
+                          residual=None, y_dtype="bf16", out=None, workspace=None):
+    """spgemm_tiled followed by + bias [N] (f32), the activation ("none", "relu", "gelu", "gelu_tanh", "silu") and
+    + residual, all in the product's epilogue and rounded once. gated: weight rows 2j and 2j + 1 are the gate and
+    the value of column j, y[:, j] = act(z[:, 2j]) * z[:, 2j + 1], so Y and residual are [M, N / 2]. residual has
+    the type of Y (bf16 or f32) and may be `out` itself. workspace: as spgemm_tiled (None takes one where needed)."""
+    y = dtype_code(y_dtype)
+    ab = dtype_code(dense.dtype)
+    if act not in ACTIVATIONS:
+        raise SSError(SS_ERR_UNSUPPORTED, f"act {act!r}: one of {', '.join(ACTIVATIONS)}")
+    if y not in (SS_BF16, SS_F32):
+        raise SSError(SS_ERR_DTYPE, "the output must be bf16 or f32")
+    cols = N // 2 if gated else N
+    _check_tiled_product(side, M, N, Kc, ab, tvals, tmeta, dense, sx, sw, None, y)
+    for t, name in ((out, "out"), (residual, "residual")):
+        _need_dtype(t, _TORCH[y], name)
+        _need_mat(t, M, cols, name)
+    _need_dtype(bias, torch.float32, "bias")
+    _need_vec(bias, N, "bias")
+    _on_gpu(bias, residual, out)
+    dev = dense.device
+    _same_device(dev, tvals=tvals, tmeta=tmeta, sx=sx, sw=sw, bias=bias, residual=residual, out=out)
+    Y = out if out is not None else torch.empty((M, cols), dtype=_TORCH[y], device=dev)
+    need = int(lib.ss_spgemm_tiled_workspace_bytes(side, M, N, Kc, ab))
+    if workspace is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    else:
+        ws = workspace
+        _need_bytes(ws, need, "workspace")
+        _on_gpu(ws)
+        _same_device(dev, workspace=ws)
+    with _on_device(dev):
+        _check(lib.ss_spgemm_tiled_epilogue(side, M, N, Kc, ab, _ptr(tvals), _ptr(tmeta), _ptr(dense), _ld(dense),
+                                            _ptr(sx), _ptr(sw), _ptr(bias), ACTIVATIONS[act], int(gated),
+                                            _ptr(residual), 0 if residual is None else _ld(residual), y, _ptr(Y),
+                                            _ld(Y), _ptr(ws), 0 if ws is None else _bytes(ws), _stream(dev)))
     return Y
 
 

@@ -110,7 +110,8 @@ template <int AB, int YT, bool SIDE_X, bool BS>
 __device__ __forceinline__ void spgemm_body(int R, int C, int KS, const uint8_t* __restrict__ tv,
                                             const uint8_t* __restrict__ tm, const uint8_t* __restrict__ bd, int ldb,
                                             const float* __restrict__ sx, const float* __restrict__ sw,
-                                            void* __restrict__ Y, int ldy, int tiles_r, int tiles_c) {
+                                            void* __restrict__ Y, int ldy, int tiles_r, int tiles_c,
+                                            const EpilogueOf<YT>& ep = EpilogueOf<YT>{}) {
   using Acc = typename Mma<AB>::Acc;
   using MT = Meta<AB>;
   using MV = typename MT::V;
@@ -450,7 +451,8 @@ __device__ __forceinline__ void spgemm_body(int R, int C, int KS, const uint8_t*
           y[q] = __fmul_rn(__fmul_rn((float)acc[t][u][q], s1), s2);
         }
       }
-      store_out<YT, SIDE_X>(Y, ldy, ar, bc, R, y, yi);
+      if constexpr (YT == 3) store_epilogue<SIDE_X>(Y, ldy, ar, bc, R, y, ep);
+      else store_out<YT, SIDE_X>(Y, ldy, ar, bc, R, y, yi);
     }
   }
 }
@@ -460,8 +462,8 @@ __global__ __launch_bounds__(64 * NW, 1) void spgemm_kernel(int R, int C, int KS
                                                             const uint8_t* __restrict__ tm, const uint8_t* __restrict__ bd,
                                                             int ldb, const float* __restrict__ sx,
                                                             const float* __restrict__ sw, void* __restrict__ Y, int ldy,
-                                                            int tiles_r, int tiles_c) {
-  spgemm_body<AB, YT, SIDE_X, BS>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, tiles_r, tiles_c);
+                                                            int tiles_r, int tiles_c, EpilogueOf<YT> ep) {
+  spgemm_body<AB, YT, SIDE_X, BS>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, tiles_r, tiles_c, ep);
 }
 
 // A batch of independent products of one shape (e.g. one per attention head): blockIdx.y selects the
@@ -494,13 +496,13 @@ hipError_t launch_batched(int batch, int R, int C, int KS, const uint8_t* tv, in
 
 template <int AB, int YT, bool SIDE_X, bool BS = false>
 hipError_t launch(int R, int C, int KS, const uint8_t* tv, const uint8_t* tm, const uint8_t* bd, int ldb,
-                  const float* sx, const float* sw, void* Y, int ldy, hipStream_t st) {
+                  const float* sx, const float* sw, void* Y, int ldy, const EpilogueOf<YT>& ep, hipStream_t st) {
   auto kern = spgemm_kernel<AB, YT, SIDE_X, BS>;
   constexpr int lds = BS ? LDS_BS : LDS_SC;
   const hipError_t e = lds_limit((const void*)kern, lds);
   if (e != hipSuccess) return e;
   const int tr = (R + BM - 1) / BM, tc = (C + BN - 1) / BN;
-  hipLaunchKernelGGL(kern, dim3(tr * tc), dim3(64 * NW), lds, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, tr, tc);
+  hipLaunchKernelGGL(kern, dim3(tr * tc), dim3(64 * NW), lds, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, tr, tc, ep);
   return hipGetLastError();
 }
 
@@ -518,7 +520,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
                                                             const uint8_t* __restrict__ bd, int ldb,
                                                             const float* __restrict__ sx,
                                                             const float* __restrict__ sw, void* __restrict__ Y,
-                                                            int ldy) {
+                                                            int ldy, EpilogueOf<YT> ep) {
   using Acc = typename tiled::Mma<AB>::Acc;
   using MT = tiled::Meta<AB>;
   using MV = typename MT::V;
@@ -594,24 +596,25 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
           y[q] = f;
         }
       }
-      store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
+      if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, ep);
+      else store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
     }
   }
 }
 
 template <int AB, int YT>
 hipError_t launch(int R, int C, int KS, const uint8_t* tv, const uint8_t* tm, const uint8_t* bd, int ldb,
-                  const float* sx, const float* sw, void* Y, int ldy, hipStream_t st) {
+                  const float* sx, const float* sw, void* Y, int ldy, const EpilogueOf<YT>& ep, hipStream_t st) {
   const int nrb = (R + 15) / 16;
   if (C <= 16)
     hipLaunchKernelGGL((decode_kernel<AB, YT, 1>), dim3(nrb), dim3(64 * NW), 0, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y,
-                       ldy);
+                       ldy, ep);
   else if (C <= 32)
     hipLaunchKernelGGL((decode_kernel<AB, YT, 2>), dim3(nrb), dim3(64 * NW), 0, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y,
-                       ldy);
+                       ldy, ep);
   else
     hipLaunchKernelGGL((decode_kernel<AB, YT, 4>), dim3(nrb), dim3(64 * NW), 0, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y,
-                       ldy);
+                       ldy, ep);
   return hipGetLastError();
 }
 
@@ -997,7 +1000,7 @@ template <int AB, int YT>
 __global__ __launch_bounds__(256) void splitk_reduce_kernel(int R, int C, int RP, int splits,
                                                             const void* __restrict__ ws, const float* __restrict__ sx,
                                                             const float* __restrict__ sw, void* __restrict__ Y,
-                                                            int ldy) {
+                                                            int ldy, EpilogueOf<YT> ep) {
   const int quads = RP / 4;
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int bc = (int)(idx / quads), ar = (int)(idx % quads) * 4;
@@ -1028,7 +1031,8 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(int R, int C, int RP
       y[q] = f;
     }
   }
-  store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
+  if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, ep);
+  else store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
 }
 
 struct Plan {
@@ -1052,7 +1056,7 @@ inline Plan plan(int64_t R, int64_t C, int64_t KS) {
 
 template <int AB, int YT>
 hipError_t launch(int R, int C, int KS, const uint8_t* tv, const uint8_t* tm, const uint8_t* bd, int ldb,
-                  const float* sx, const float* sw, void* Y, int ldy, void* ws, hipStream_t st) {
+                  const float* sx, const float* sw, void* Y, int ldy, void* ws, const EpilogueOf<YT>& ep, hipStream_t st) {
   const Plan p = plan(R, C, KS);
   const int nrg = ((R + 15) / 16 + NW - 1) / NW;
   const dim3 grid((unsigned)nrg, (unsigned)p.splits);
@@ -1066,7 +1070,7 @@ hipError_t launch(int R, int C, int KS, const uint8_t* tv, const uint8_t* tm, co
   if (e != hipSuccess) return e;
   const int64_t threads = (int64_t)C * (p.rp / 4);
   hipLaunchKernelGGL((splitk_reduce_kernel<AB, YT>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, R, C, p.rp,
-                     p.splits, (const void*)ws, sx, sw, Y, ldy);
+                     p.splits, (const void*)ws, sx, sw, Y, ldy, ep);
   return hipGetLastError();
 }
 
@@ -1159,8 +1163,8 @@ hipError_t launch_spgemm_tiled_block(int yt, int64_t R, int64_t C, int64_t Kc, c
                                      int64_t ldy, hipStream_t st) {
   const uint8_t* b = static_cast<const uint8_t*>(bd);
   const int r = (int)R, c = (int)C, ks = (int)(Kc / 128), lb = (int)ldb_bytes, ly = (int)ldy;
-  if (yt == 0) return tiled::launch<1, 0, false, true>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, st);
-  return tiled::launch<1, 1, false, true>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, st);
+  if (yt == 0) return tiled::launch<1, 0, false, true>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, {}, st);
+  return tiled::launch<1, 1, false, true>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, {}, st);
 }
 
 bool quant_lift_spgemm_fits(bool x_bf16, int64_t M, int64_t K, int64_t Kc) {
@@ -1207,30 +1211,33 @@ int64_t spgemm_tiled_workspace_bytes(bool side_x, int ab, int64_t R, int64_t C, 
 
 hipError_t launch_spgemm_tiled(bool side_x, int ab, int yt, int64_t R, int64_t C, int64_t Kc, const uint8_t* tv,
                                const uint8_t* tm, const void* bd, int64_t ldb_bytes, const float* sx, const float* sw,
-                               void* Y, int64_t ldy, void* ws, hipStream_t st) {
+                               void* Y, int64_t ldy, void* ws, const Epilogue& ep, hipStream_t st) {
   const uint8_t* b = static_cast<const uint8_t*>(bd);
   const int r = (int)R, c = (int)C, ks = (int)(Kc * (ab == 2 ? 2 : 1) / 128), lb = (int)ldb_bytes, ly = (int)ldy;
   // few tokens: split-K when a workspace is given and the problem uses one, else the row-block decode kernel
   const bool dec = few_tokens(side_x, R, C);
   const bool spk = ws != nullptr && use_splitk(side_x, R, C);
   const int bn = spk || dec ? 0 : wide_bn(side_x, R, C, ks, ldb_bytes);
-  if (bn) return launch_spgemm_wide(bn, side_x, ab, yt, r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, st);
-#define SS_TL(AB_, YT_)                                                                                   \
-  return spk      ? splitk::launch<AB_, YT_>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, ws, st)               \
-         : dec    ? decode::launch<AB_, YT_>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, st)                   \
-         : side_x ? tiled::launch<AB_, YT_, true>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, st)               \
-                  : tiled::launch<AB_, YT_, false>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, st)
+  if (bn) return launch_spgemm_wide(bn, side_x, ab, yt, r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, ep, st);
+#define SS_TL(AB_, YT_, EP_)                                                                                    \
+  return spk      ? splitk::launch<AB_, YT_>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, ws, EP_, st)                \
+         : dec    ? decode::launch<AB_, YT_>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, EP_, st)                    \
+         : side_x ? tiled::launch<AB_, YT_, true>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, EP_, st)               \
+                  : tiled::launch<AB_, YT_, false>(r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, EP_, st)
   if (ab == 0) {
-    if (yt == 0) SS_TL(0, 0);
-    if (yt == 1) SS_TL(0, 1);
-    SS_TL(0, 2);
+    if (yt == 0) SS_TL(0, 0, {});
+    if (yt == 1) SS_TL(0, 1, {});
+    if (yt == 3) SS_TL(0, 3, ep);
+    SS_TL(0, 2, {});
   }
   if (ab == 1) {
-    if (yt == 0) SS_TL(1, 0);
-    SS_TL(1, 1);
+    if (yt == 0) SS_TL(1, 0, {});
+    if (yt == 3) SS_TL(1, 3, ep);
+    SS_TL(1, 1, {});
   }
-  if (yt == 0) SS_TL(2, 0);
-  SS_TL(2, 1);
+  if (yt == 0) SS_TL(2, 0, {});
+  if (yt == 3) SS_TL(2, 3, ep);
+  SS_TL(2, 1, {});
 #undef SS_TL
 }
 

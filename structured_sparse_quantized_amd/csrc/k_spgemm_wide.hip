@@ -90,7 +90,7 @@ template <int BN, int W, int AB, int YT, bool SX, int GR>
 __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
     int R, int C, int KS, const uint8_t* __restrict__ tv, const uint8_t* __restrict__ tm, const uint8_t* __restrict__ bd,
     int ldb, const float* __restrict__ sx, const float* __restrict__ sw, void* __restrict__ Y, int ldy, int tiles_r,
-    int tiles_c) {
+    int tiles_c, EpilogueOf<YT> ep) {
   using SH = Shape<BN, W>;
   constexpr int TJ = SH::TJ, PA = SH::PA, PB = SH::PB, LPW = SH::LPW, STAGE = SH::STAGE, S = SH::S, META = SH::META;
   constexpr int NW = SH::NW, WGN = SH::WGN;
@@ -410,6 +410,48 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
         }
       }
     };
+    if constexpr (YT == 3) {
+      // The general epilogue. The scaled sums go through the idle ring as float32 rows of tokens, and leave 8
+      // columns per lane and step: bias, activation and gate there, in one small loop (unrolled over a lane's
+      // accumulators the activations' code is too long to unroll, and the accumulators would go to memory), and
+      // the residual on the unrounded value.
+      constexpr int LD = (SX ? 16 * TJ : 128) + 4;  // floats of a staged row, padded against bank conflicts
+      constexpr int UB = SX ? TI : TJ;                                     // 16-token blocks of this wave
+      constexpr int UP = up_rows(UB, META / NW / (16 * LD * 4)), NP = UB / UP, RP = 16 * UP;  // per pass; passes
+      static_assert(NW * RP * LD * 4 <= META, "staging fits the stage ring");
+      SS_LDS float* stg = (SS_LDS float*)((SS_LDS uint8_t*)smem + wave * RP * LD * 4);
+      const int tok0 = SX ? r0 + wm * TI * 16 : c0 + wn * TJ * 16, ntok = SX ? R : C;
+      const int ch0 = SX ? c0 + wn * TJ * 16 : r0 + wm * TI * 16, nch = SX ? C : R;
+      const int cpr = (SX ? 2 * TJ : 16) >> ep.gated;  // 8-column pieces of a row of Y
+  #pragma unroll
+      for (int p = 0; p < NP; ++p) {
+  #pragma unroll
+        for (int uu = 0; uu < UP; ++uu) {
+  #pragma unroll
+          for (int x = 0; x < (SX ? TJ : TI); ++x) {
+            float y[4];
+            int32_t yi[4];
+            if constexpr (SX) {  // 4 tokens of one channel
+              result(p * UP + uu, x, y, yi);
+  #pragma unroll
+              for (int q = 0; q < 4; ++q) stg[(uu * 16 + 4 * jj + q) * LD + x * 16 + r16] = y[q];
+            } else {  // 4 channels of one token
+              result(x, p * UP + uu, y, yi);
+              *reinterpret_cast<SS_LDS v4i*>(stg + (uu * 16 + r16) * LD + x * 16 + 4 * jj) =
+                  v4i{__float_as_int(y[0]), __float_as_int(y[1]), __float_as_int(y[2]), __float_as_int(y[3])};
+            }
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+  #pragma unroll 1
+        for (int i = lane; i < RP * cpr; i += 64) {
+          const int row = i / cpr, piece = i % cpr, tok = tok0 + p * RP + row;
+          if (tok < ntok) leave8((const float*)(stg + row * LD), piece, Y, ldy, tok, ch0, nch, ep);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+      return;
+    }
     constexpr int EB = YT == 0 ? 2 : 4;  // output element bytes
     const bool vec = ((int64_t)ldy * EB) % 16 == 0;
     uint8_t* Yb = static_cast<uint8_t*>(Y);
@@ -551,30 +593,33 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
 
 template <int BN, int W, int AB, int YT, bool SX, int GR = 8>
 hipError_t launch(int R, int C, int KS, const uint8_t* tv, const uint8_t* tm, const uint8_t* bd, int ldb, const float* sx,
-                  const float* sw, void* Y, int ldy, hipStream_t st) {
+                  const float* sw, void* Y, int ldy, const EpilogueOf<YT>& ep, hipStream_t st) {
   auto kern = wide_kernel<BN, W, AB, YT, SX, GR>;
   constexpr int lds = lds_bytes<BN, W, AB>();
   const hipError_t e = lds_limit((const void*)kern, lds);
   if (e != hipSuccess) return e;
   const int tr = (R + BM - 1) / BM, tc = (C + BN - 1) / BN;
-  hipLaunchKernelGGL(kern, dim3(tr * tc), dim3(64 * W), lds, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, tr, tc);
+  hipLaunchKernelGGL(kern, dim3(tr * tc), dim3(64 * W), lds, st, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, tr, tc, ep);
   return hipGetLastError();
 }
 
 template <int BN, int W, bool SX>
 hipError_t launch_bn(int ab, int yt, int R, int C, int KS, const uint8_t* tv, const uint8_t* tm, const uint8_t* bd, int ldb,
-                     const float* sx, const float* sw, void* Y, int ldy, hipStream_t st) {
+                     const float* sx, const float* sw, void* Y, int ldy, const Epilogue& ep, hipStream_t st) {
   if (ab == 0) {
-    if (yt == 0) return launch<BN, W, 0, 0, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
-    if (yt == 1) return launch<BN, W, 0, 1, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
-    return launch<BN, W, 0, 2, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
+    if (yt == 0) return launch<BN, W, 0, 0, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
+    if (yt == 1) return launch<BN, W, 0, 1, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
+    if (yt == 3) return launch<BN, W, 0, 3, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st);
+    return launch<BN, W, 0, 2, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
   }
   if (ab == 1) {
-    if (yt == 0) return launch<BN, W, 1, 0, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
-    return launch<BN, W, 1, 1, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
+    if (yt == 0) return launch<BN, W, 1, 0, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
+    if (yt == 3) return launch<BN, W, 1, 3, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st);
+    return launch<BN, W, 1, 1, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
   }
-  if (yt == 0) return launch<BN, W, 2, 0, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
-  return launch<BN, W, 2, 1, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
+  if (yt == 0) return launch<BN, W, 2, 0, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
+  if (yt == 3) return launch<BN, W, 2, 3, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st);
+  return launch<BN, W, 2, 1, SX>(R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, {}, st);
 }
 
 }  // namespace wide
@@ -586,11 +631,11 @@ constexpr int kWide8MaxSteps = 64;
 
 hipError_t launch_spgemm_wide(int bn, bool side_x, int ab, int yt, int R, int C, int KS, const uint8_t* tv,
                               const uint8_t* tm, const uint8_t* bd, int ldb, const float* sx, const float* sw, void* Y,
-                              int ldy, hipStream_t st) {
-  if (side_x) return wide::launch_bn<128, 4, true>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
-  if (bn != 256) return wide::launch_bn<128, 4, false>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
-  return KS <= kWide8MaxSteps ? wide::launch_bn<256, 8, false>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st)
-                              : wide::launch_bn<256, 4, false>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, st);
+                              int ldy, const Epilogue& ep, hipStream_t st) {
+  if (side_x) return wide::launch_bn<128, 4, true>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st);
+  if (bn != 256) return wide::launch_bn<128, 4, false>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st);
+  return KS <= kWide8MaxSteps ? wide::launch_bn<256, 8, false>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st)
+                              : wide::launch_bn<256, 4, false>(ab, yt, R, C, KS, tv, tm, bd, ldb, sx, sw, Y, ldy, ep, st);
 }
 
 }  // namespace ss

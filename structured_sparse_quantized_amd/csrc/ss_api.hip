@@ -269,7 +269,8 @@ ss_status ss_slide_decompose_tiled(const void* W, ss_dtype w_dt, int64_t rows, i
 // Checks shared by ss_spgemm_tiled and ss_spgemm_tiled_ws; sets *run = false for an empty problem.
 static ss_status check_spgemm_tiled(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_dtype ab_dt, const void* tvals,
                                     const uint8_t* tmeta, const void* dense, int64_t ldd, const float* sx,
-                                    const float* sw, ss_dtype y_dt, void* Y, int64_t ldy, bool* run) {
+                                    const float* sw, ss_dtype y_dt, void* Y, int64_t ldy, bool* run,
+                                    bool half_width = false) {
   *run = false;
   if (side != SS_SPARSE_W && side != SS_SPARSE_X) return fail(SS_ERR_SHAPE, "bad side");
   if (ab_dt != SS_I8 && ab_dt != SS_FP8E4M3 && ab_dt != SS_BF16)
@@ -290,7 +291,7 @@ static ss_status check_spgemm_tiled(ss_side side, int64_t M, int64_t N, int64_t 
   // the kernel addresses the dense operand with 32-bit byte offsets
   if ((uint64_t)(C - 1) * (uint64_t)ldd * es + (uint64_t)Kc * es > 0xFFFFFFFFull)
     return fail(SS_ERR_UNSUPPORTED, "dense operand spans more than 4 GiB");
-  if ((s = check_mat("Y", Y, 1, N, ldy, esize(y_dt))) != SS_OK) return s;
+  if ((s = check_mat("Y", Y, 1, half_width ? N / 2 : N, ldy, esize(y_dt))) != SS_OK) return s;
   if (!tvals || !tmeta) return fail(SS_ERR_NULL, "tiled operand is NULL");
   if (!aligned16(tvals) || !aligned16(tmeta)) return fail(SS_ERR_ALIGN, "tiled operand is not 16-byte aligned");
   if (ab_dt != SS_BF16 && y_dt != SS_I32 && (!sx || !sw)) return fail(SS_ERR_NULL, "INT8/FP8 products need both scales");
@@ -300,14 +301,16 @@ static ss_status check_spgemm_tiled(ss_side side, int64_t M, int64_t N, int64_t 
 
 static ss_status run_spgemm_tiled(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_dtype ab_dt, const void* tvals,
                                   const uint8_t* tmeta, const void* dense, int64_t ldd, const float* sx,
-                                  const float* sw, ss_dtype y_dt, void* Y, int64_t ldy, void* ws, void* stream) {
+                                  const float* sw, ss_dtype y_dt, void* Y, int64_t ldy, void* ws, void* stream,
+                                  const ss::Epilogue* ep = nullptr) {
   const bool sx_side = (side == SS_SPARSE_X);
   const int64_t R = sx_side ? M : N, C = sx_side ? N : M;
   const int ab = ab_dt == SS_I8 ? 0 : ab_dt == SS_FP8E4M3 ? 1 : 2;
-  const int yt = y_dt == SS_BF16 ? 0 : y_dt == SS_F32 ? 1 : 2;
+  const int yt = ep ? 3 : y_dt == SS_BF16 ? 0 : y_dt == SS_F32 ? 1 : 2;
   return hip_status(ss::launch_spgemm_tiled(sx_side, ab, yt, R, C, Kc, static_cast<const uint8_t*>(tvals), tmeta, dense,
                                             ldd * esize(ab_dt), y_dt == SS_I32 ? nullptr : sx,
-                                            y_dt == SS_I32 ? nullptr : sw, Y, ldy, ws, (hipStream_t)stream),
+                                            y_dt == SS_I32 ? nullptr : sw, Y, ldy, ws, ep ? *ep : ss::Epilogue{},
+                                            (hipStream_t)stream),
                     "ss_spgemm_tiled launch");
 }
 
@@ -414,6 +417,36 @@ ss_status ss_spgemm_tiled_ws(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_
   }
   return run_spgemm_tiled(side, M, N, Kc, ab_dt, tvals, tmeta, dense, ldd, sx, sw, y_dt, Y, ldy,
                           need > 0 ? workspace : nullptr, stream);
+}
+
+ss_status ss_spgemm_tiled_epilogue(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_dtype ab_dt, const void* tvals,
+                                   const uint8_t* tmeta, const void* dense, int64_t ldd, const float* sx,
+                                   const float* sw, const float* bias, ss_act act, int gated, const void* residual,
+                                   int64_t ldr, ss_dtype y_dt, void* Y, int64_t ldy, void* workspace,
+                                   int64_t ws_bytes, void* stream) {
+  if (y_dt != SS_BF16 && y_dt != SS_F32) return fail(SS_ERR_DTYPE, "output must be BF16 or F32");
+  if (act < SS_ACT_NONE || act > SS_ACT_SILU) return fail(SS_ERR_UNSUPPORTED, "unknown activation %d", (int)act);
+  if (gated && N % 2 != 0) return fail(SS_ERR_SHAPE, "a gate needs an even N, has %lld", (long long)N);
+  bool run = false;
+  ss_status s = check_spgemm_tiled(side, M, N, Kc, ab_dt, tvals, tmeta, dense, ldd, sx, sw, y_dt, Y, ldy, &run, gated != 0);
+  if (s != SS_OK) return s;
+  if (ws_bytes < 0) return fail(SS_ERR_SHAPE, "negative workspace size");
+  if (!run) return ok();
+  if (residual) {
+    if ((s = check_mat("residual", residual, 1, gated ? N / 2 : N, ldr, esize(y_dt))) != SS_OK) return s;
+    if (residual == Y && ldr != ldy) return fail(SS_ERR_SHAPE, "a residual in place needs ldr = ldy");
+  }
+  if ((uintptr_t)bias % 4 != 0) return fail(SS_ERR_ALIGN, "bias is not aligned to its elements");
+  const int64_t need = ss_spgemm_tiled_workspace_bytes(side, M, N, Kc, ab_dt);
+  if (need > 0) {
+    if (!workspace) return fail(SS_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+    if (!aligned16(workspace)) return fail(SS_ERR_ALIGN, "workspace is not 16-byte aligned");
+    if (ws_bytes < need) return fail(SS_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)ws_bytes,
+                                     (long long)need);
+  }
+  const ss::Epilogue ep{bias, residual, residual ? ldr : 0, (int)act, gated ? 1 : 0, y_dt == SS_F32 ? 1 : 0};
+  return run_spgemm_tiled(side, M, N, Kc, ab_dt, tvals, tmeta, dense, ldd, sx, sw, y_dt, Y, ldy,
+                          need > 0 ? workspace : nullptr, stream, &ep);
 }
 
 ss_status ss_prune24_block(const void* W, ss_dtype w_dt, int64_t rows, int64_t K, int64_t ldw, void* tvals,

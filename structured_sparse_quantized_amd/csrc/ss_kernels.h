@@ -38,16 +38,27 @@ hipError_t launch_prune24_tiled(bool in_bf16, int out, const void* W, int64_t ld
 hipError_t launch_slide_tiled(bool in_bf16, int out, const void* W, int64_t ldw, int64_t rows, int64_t K, int n,
                               int64_t Kc, void* tv, uint8_t* tm, float* scale, hipStream_t st);
 
+// What the general epilogue of a product (yt = 3) does after the scales: z = scaled + bias[n]; act(z), or with
+// `gated` act(z[2j]) * z[2j + 1] as column j; + residual; rounded to f32 or bf16.
+struct Epilogue {
+  const float* bias;  // [N] or NULL
+  const void* res;    // type of Y, or NULL
+  int64_t ldr;
+  int act;    // ss_act
+  int gated;
+  int f32;    // Y and the residual are f32, else bf16
+};
+
 // Tiled sparse operand and the product that reads it. es = value bytes (1: int8/fp8, 2: bf16).
 int64_t tiled_vals_bytes(int64_t rows, int64_t Kc, int es);
 int64_t tiled_meta_bytes(int64_t rows, int64_t Kc, int es);
 hipError_t launch_pack_tiled(int es, const uint8_t* vals, int64_t ldv_bytes, const uint8_t* meta, int64_t ldm,
                              int64_t rows, int64_t Kc, uint8_t* tv, uint8_t* tm, hipStream_t st);
-// ab: 0 = int8, 1 = fp8, 2 = bf16; yt: 0 = bf16, 1 = f32, 2 = i32
+// ab: 0 = int8, 1 = fp8, 2 = bf16; yt: 0 = bf16, 1 = f32, 2 = i32, 3 = the general epilogue `ep`
 // ws: workspace of spgemm_tiled_workspace_bytes bytes, or NULL (no split-K path)
 hipError_t launch_spgemm_tiled(bool side_x, int ab, int yt, int64_t R, int64_t C, int64_t Kc, const uint8_t* tv,
                                const uint8_t* tm, const void* bd, int64_t ldb_bytes, const float* sx, const float* sw,
-                               void* Y, int64_t ldy, void* ws, hipStream_t st);
+                               void* Y, int64_t ldy, void* ws, const Epilogue& ep, hipStream_t st);
 int64_t spgemm_tiled_workspace_bytes(bool side_x, int ab, int64_t R, int64_t C, int64_t Kc);
 // The prefill kernel of k_spgemm_wide.hip with 256 x bn tiles (bn = 256: one workgroup per CU, weight-sparse
 // side only, eight waves for reductions of at most 64 steps and four beyond; bn = 128: two workgroups of four
@@ -55,7 +66,7 @@ int64_t spgemm_tiled_workspace_bytes(bool side_x, int ab, int64_t R, int64_t C, 
 // bytes; launch_spgemm_tiled routes the larger prefill problems to it.
 hipError_t launch_spgemm_wide(int bn, bool side_x, int ab, int yt, int R, int C, int KS, const uint8_t* tv,
                               const uint8_t* tm, const uint8_t* bd, int ldb, const float* sx, const float* sw, void* Y,
-                              int ldy, hipStream_t st);
+                              int ldy, const Epilogue& ep, hipStream_t st);
 
 // A batch of same-shaped tiled products (one launch; blockIdx.y = problem); strides in bytes for the tiled
 // operand and the dense operand, in elements for the scales and Y.

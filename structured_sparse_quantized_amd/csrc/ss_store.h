@@ -1,6 +1,9 @@
 // Epilogue store shared by the product kernels (internal to the library).
 #pragma once
+#include <type_traits>
+
 #include "ss_device.h"
+#include "ss_kernels.h"
 
 namespace ss {
 
@@ -26,6 +29,166 @@ __device__ __forceinline__ void store_out(void* Y, int64_t ldy, int64_t ar, int6
     if constexpr (YT == 0) static_cast<uint16_t*>(Y)[off] = f32_to_bf16(y[q]);
     else if constexpr (YT == 1) static_cast<float*>(Y)[off] = y[q];
     else static_cast<int32_t*>(Y)[off] = yi[q];
+  }
+}
+
+// ---- the general epilogue (YT == 3) ---------------------------------------------
+// The kernels take an Epilogue where YT is 3 and nothing otherwise.
+struct NoEpilogue {};
+template <int YT> using EpilogueOf = typename std::conditional<YT == 3, Epilogue, NoEpilogue>::type;
+
+// The activations in float32. 1 / (1 + exp(-z)) takes the chip's power and reciprocal instructions where the
+// result is rounded to bf16 (their error and that of the exponent, |z| 2^-23, vanish in its 2^-8), the exact
+// functions for float32 results. tanh(u) enters as 2 / (1 + exp(-2u)) - 1, which makes the tanh form of GELU
+// z / (1 + exp(-2u)).
+__device__ __forceinline__ float over_1p_exp(float num, float z, bool f32) {  // num / (1 + exp(-z))
+  if (f32) return num / (1.0f + expf(-z));
+  return num * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z));
+}
+template <int N> __device__ __forceinline__ void activate_n(float* z, int act, bool f32) {
+  if (act == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = fmaxf(z[i], 0.0f);
+  } else if (act == 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678118654752440f));
+  } else if (act >= 3) {  // z / (1 + exp(-u)): u = z, or the tanh form's sqrt(8 / pi) (z + 0.044715 z^3)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float u = act == 3 ? 1.59576912160573071176f * __builtin_fmaf(0.044715f * z[i] * z[i], z[i], z[i]) : z[i];
+      z[i] = over_1p_exp(z[i], u, f32);
+    }
+  }
+}
+__device__ __forceinline__ float load_res(const Epilogue& e, int64_t at) {
+  return e.f32 ? static_cast<const float*>(e.res)[at] : bf16_to_f32(static_cast<const uint16_t*>(e.res)[at]);
+}
+__device__ __forceinline__ void store_one(void* Y, int64_t at, float v, bool f32) {
+  if (f32) static_cast<float*>(Y)[at] = v;
+  else static_cast<uint16_t*>(Y)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
+}
+// a column's bias and activation for a lane's 4 scaled results (columns ar..ar+3 of side W, column bc of side X),
+// in place; gated: the results move to y[0], y[1] (side W) or stay in the even lanes (side X)
+template <bool SIDE_X>
+__device__ __forceinline__ void finish(float* y, int64_t ar, int64_t bc, int64_t R, const Epilogue& e) {
+  if (e.bias) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = y[q] + e.bias[SIDE_X ? bc : min(ar + q, R - 1)];
+  }
+  if constexpr (SIDE_X) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float up = e.gated ? __shfl_xor(y[q], 1, 64) : 1.0f;
+      activate_n<1>(y + q, e.act, e.f32);
+      if (e.gated) y[q] *= up;
+    }
+  } else if (e.gated) {
+    float g[2] = {y[0], y[2]};
+    activate_n<2>(g, e.act, e.f32);
+    y[0] = g[0] * y[1];
+    y[1] = g[1] * y[3];
+  } else {
+    activate_n<4>(y, e.act, e.f32);
+  }
+}
+
+// store_out with the general epilogue: all lanes of a wave whose bc is below the count of B rows call it together.
+template <bool SIDE_X>
+__device__ __forceinline__ void store_epilogue(void* Y, int64_t ldy, int64_t ar, int64_t bc, int64_t R, float* y,
+                                               const Epilogue& e) {
+  finish<SIDE_X>(y, ar, bc, R, e);
+  if constexpr (SIDE_X) {
+    if (e.gated && (bc & 1)) return;
+    const int64_t col = e.gated ? bc >> 1 : bc;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (ar + q >= R) break;
+      const float v = e.res ? y[q] + load_res(e, (ar + q) * e.ldr + col) : y[q];
+      store_one(Y, (ar + q) * ldy + col, v, e.f32);
+    }
+  } else {
+    const int n = e.gated ? 2 : 4;
+    const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
+    if (n == 4 && !e.f32 && (ldy & 3) == 0 && (e.ldr & 3) == 0 && col + 4 <= cols) {  // 8-byte vectors
+      if (e.res) {
+        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.res) + bc * e.ldr + col);
+        y[0] += __uint_as_float(r.x << 16);
+        y[1] += __uint_as_float(r.x & 0xFFFF0000u);
+        y[2] += __uint_as_float(r.y << 16);
+        y[3] += __uint_as_float(r.y & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + bc * ldy + col) =
+          make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q >= n || col + q >= cols) break;
+      const float v = e.res ? y[q] + load_res(e, bc * e.ldr + col + q) : y[q];
+      store_one(Y, bc * ldy + col + q, v, e.f32);
+    }
+  }
+}
+
+// Columns 8 piece .. +7 of one row of Y from a staged row of scaled sums (channels ch0, ch0 + 1, ..; `nch` of
+// them in all): 8 channels, or with a gate the 16 channels of 8 pairs.
+__device__ __forceinline__ void leave8(const float* row, int piece, void* Y, int64_t ldy, int64_t tok, int ch0, int nch,
+                                       const Epilogue& e) {
+  float f[16];
+  const int n = e.gated ? 16 : 8, first = ch0 + piece * n;
+  if (first >= nch) return;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    if (i >= n) break;
+    const float4 x = *reinterpret_cast<const float4*>(row + piece * n + i);
+    f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+  }
+  if (e.bias) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) f[i] = f[i] + e.bias[min(first + i, nch - 1)];
+  }
+  float g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = e.gated ? f[2 * i] : f[i];
+  activate_n<8>(g, e.act, e.f32);
+  if (e.gated) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= f[2 * i + 1];
+  }
+  const int col = (e.gated ? ch0 >> 1 : ch0) + piece * 8, ncol = e.gated ? nch >> 1 : nch;
+  const int per16 = e.f32 ? 3 : 7;  // elements of 16 bytes, less one
+  if (col + 8 <= ncol && (ldy & per16) == 0 && (!e.res || (e.ldr & per16) == 0)) {
+    typedef float v4fl __attribute__((ext_vector_type(4)));
+    typedef uint32_t v4ul __attribute__((ext_vector_type(4)));
+    if (e.f32) {
+      v4fl lo{g[0], g[1], g[2], g[3]}, hi{g[4], g[5], g[6], g[7]};
+      if (e.res) {
+        const v4fl* r = reinterpret_cast<const v4fl*>(static_cast<const float*>(e.res) + tok * e.ldr + col);
+        lo += r[0];
+        hi += r[1];
+      }
+      v4fl* d = reinterpret_cast<v4fl*>(static_cast<float*>(Y) + tok * ldy + col);
+      __builtin_nontemporal_store(lo, d);
+      __builtin_nontemporal_store(hi, d + 1);
+    } else {
+      if (e.res) {
+        const v4ul r = *reinterpret_cast<const v4ul*>(static_cast<const uint16_t*>(e.res) + tok * e.ldr + col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[2 * i] += __uint_as_float(r[i] << 16);
+          g[2 * i + 1] += __uint_as_float(r[i] & 0xFFFF0000u);
+        }
+      }
+      const v4ul v{pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])};
+      __builtin_nontemporal_store(v, reinterpret_cast<v4ul*>(static_cast<uint16_t*>(Y) + tok * ldy + col));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (col + i >= ncol) break;
+    store_one(Y, tok * ldy + col + i, e.res ? g[i] + load_res(e, tok * e.ldr + col + i) : g[i], e.f32);
   }
 }
 

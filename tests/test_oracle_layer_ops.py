@@ -142,3 +142,31 @@ def test_attention_refusals():
                 lambda: ss.rotary(t, torch.zeros(4), torch.zeros(8)), lambda: ss.rotary(t.half(), None, None)):
         with pytest.raises(ss.SSError):
             bad()
+
+
+def test_epilogue_oracle_by_hand():
+    from oracle.fused_epilogue import activate, epilogue, epilogue_f32
+    z = np.array([[-2.0, 0.5, 1.0, 3.0]])
+    assert np.allclose(epilogue(z, bias=[1, 0, 0, 1], act="relu", residual=[[1, 1, 1, 1]]), [[1, 1.5, 2, 5]])
+    assert np.allclose(epilogue(z, gated=True), [[-1.0, 3.0]]) and np.allclose(epilogue(z, act="relu", gated=True), [[0, 3]])
+    assert np.allclose(activate(1.0, "silu"), 1 / (1 + math.exp(-1))) and np.allclose(activate(1.0, "gelu"), 0.8413447461)
+    assert np.allclose(activate(1.0, "gelu_tanh"), 0.8411919906) and activate(-800.0, "silu") == 0
+    assert np.array_equal(epilogue_f32(z, relu=True), np.maximum(z, 0).astype(np.float32))
+
+
+@built
+def test_epilogue_refusals():
+    import structured_sparse_quantized_amd as ss
+    odd = ctypes.c_void_p((1 << 20) + 8)
+
+    def call(N=32, act=0, gated=0, res=None, ldr=32, y=ss.SS_BF16, ldy=32, sx=FAKE, bias=None, ws=None, n=0, M=8, Kc=256):
+        return ss.lib.ss_spgemm_tiled_epilogue(0, M, N, Kc, ss.SS_I8, FAKE, FAKE, FAKE, Kc, sx, FAKE, bias, act, gated, res, ldr,
+                                               y, FAKE, ldy, ws, n, None)
+
+    assert call(y=ss.SS_I32) == ss.SS_ERR_DTYPE and call(act=5) == call(act=-1) == ss.SS_ERR_UNSUPPORTED
+    assert call(N=31, gated=1) == call(ldy=31) == call(res=FAKE, ldr=31) == call(Kc=100) == call(n=-1) == ss.SS_ERR_SHAPE
+    assert call(res=FAKE, ldr=40) == ss.SS_ERR_SHAPE  # Y itself with another stride
+    assert call(res=odd) == call(bias=ctypes.c_void_p(2)) == ss.SS_ERR_ALIGN and call(sx=None) == ss.SS_ERR_NULL
+    need = ss.spgemm_tiled_workspace_bytes(0, 40, 32, 256, "i8")
+    assert need > 0 and call(M=40) == ss.SS_ERR_NULL and call(M=40, ws=FAKE, n=need - 1) == ss.SS_ERR_SHAPE
+    assert call(M=0) == call(N=0) == ss.SS_OK
