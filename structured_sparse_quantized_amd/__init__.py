@@ -182,11 +182,11 @@ def dtype_code(d) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -396,34 +396,36 @@ def spgemm_tiled_epilogue(side: int, M: int, N: int, Kc: int, tvals: torch.Tenso
     the type of Y (bf16 or f32) and may be `out` itself. workspace: as spgemm_tiled (None takes one where needed)."""
     y = dtype_code(y_dtype)
     ab = dtype_code(dense.dtype)
-    if act not in ACTIVATIONS:
+    act_code = ACTIVATIONS.get(act)
+    if act_code is None:
         raise SSError(SS_ERR_UNSUPPORTED, f"act {act!r}: one of {', '.join(ACTIVATIONS)}")
     if y not in (SS_BF16, SS_F32):
         raise SSError(SS_ERR_DTYPE, "the output must be bf16 or f32")
     cols = N // 2 if gated else N
-    _check_tiled_product(side, M, N, Kc, ab, tvals, tmeta, dense, sx, sw, None, y)
+    rows, dn = (M, N) if side == SS_SPARSE_X else (N, M)
+    _need_bytes(tvals, lib.ss_tiled_vals_bytes(rows, Kc, ab), "tvals")
+    _need_bytes(tmeta, lib.ss_tiled_meta_bytes(rows, Kc, ab), "tmeta")
+    _need_mat(dense, dn, Kc, "dense")
+    for t, n, name in ((sx, M, "sx"), (sw, N, "sw"), (bias, N, "bias")):
+        if t is not None:
+            _need_vec(t, n, name)
+            _need_dtype(t, torch.float32, name)
     for t, name in ((out, "out"), (residual, "residual")):
-        _need_dtype(t, _TORCH[y], name)
-        _need_mat(t, M, cols, name)
-    _need_dtype(bias, torch.float32, "bias")
-    _need_vec(bias, N, "bias")
-    _on_gpu(bias, residual, out)
+        if t is not None:
+            _need_dtype(t, _TORCH[y], name)
+            _need_mat(t, M, cols, name)
     dev = dense.device
-    _same_device(dev, tvals=tvals, tmeta=tmeta, sx=sx, sw=sw, bias=bias, residual=residual, out=out)
-    Y = out if out is not None else torch.empty((M, cols), dtype=_TORCH[y], device=dev)
-    need = int(lib.ss_spgemm_tiled_workspace_bytes(side, M, N, Kc, ab))
-    if workspace is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    else:
-        ws = workspace
-        _need_bytes(ws, need, "workspace")
-        _on_gpu(ws)
-        _same_device(dev, workspace=ws)
-    with _on_device(dev):
-        _check(lib.ss_spgemm_tiled_epilogue(side, M, N, Kc, ab, _ptr(tvals), _ptr(tmeta), _ptr(dense), _ld(dense),
-                                            _ptr(sx), _ptr(sw), _ptr(bias), ACTIVATIONS[act], int(gated),
-                                            _ptr(residual), 0 if residual is None else _ld(residual), y, _ptr(Y),
-                                            _ld(Y), _ptr(ws), 0 if ws is None else _bytes(ws), _stream(dev)))
+    _same_gpu(dev, tvals, tmeta, sx, sw, bias, residual, out, workspace)
+    Y = out if out is not None else dense.new_empty((M, cols), dtype=_TORCH[y])
+    need = lib.ss_spgemm_tiled_workspace_bytes(side, M, N, Kc, ab)
+    if workspace is not None:
+        _need_bytes(workspace, need, "workspace")
+        need = _bytes(workspace)
+    elif need > 0:
+        workspace = dense.new_empty(need, dtype=torch.uint8)
+    _run(dev, lib.ss_spgemm_tiled_epilogue, side, M, N, Kc, ab, tvals.data_ptr(), tmeta.data_ptr(), dense.data_ptr(),
+         dense.stride(0), _ptr(sx), _ptr(sw), _ptr(bias), act_code, gated, _ptr(residual),
+         0 if residual is None else residual.stride(0), y, Y.data_ptr(), Y.stride(0), _ptr(workspace), max(need, 0))
     return Y
 
 
@@ -623,40 +625,37 @@ ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 
 def _need_heads(t, shape, name: str) -> None:
     """A [tokens, heads, D] view of this shape whose heads are contiguous."""
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape) or (t.numel() > 0 and shape[2] > 1 and t.stride(2) != 1):
+    if t.shape != shape or len(shape) != 3 or (t.stride(2) != 1 and shape[2] > 1 and t.numel() > 0):
         raise SSError(SS_ERR_SHAPE, f"{name}: needs {list(shape)} with unit stride along the last dimension, has "
                       f"{list(t.shape)} with strides {list(t.stride())}")
 
 
-def _need_ints(t, n: int, name: str, device) -> None:
+def _need_ints(t, n: int, name: str) -> None:
     if t is None:
         return
-    _need_dtype(t, torch.int32, name)
-    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not torch.int32:
+        raise SSError(SS_ERR_DTYPE, f"{name}: needs {torch.int32}, has {t.dtype}")
+    if t.shape != (n,) or not t.is_contiguous():
         raise SSError(SS_ERR_SHAPE, f"{name}: needs {n} contiguous int32 values, has {list(t.shape)}")
-    _same_device(device, **{name: t})
 
 
-def _same_device(device, **ts) -> None:
-    for name, t in ts.items():
+def _same_gpu(device, *ts) -> None:
+    if device.type != "cuda":
+        raise SSError(SS_ERR_UNSUPPORTED, f"tensor on {device}: the library runs on the GPU only")
+    for t in ts:
         if t is not None and t.device != device:
-            raise SSError(SS_ERR_UNSUPPORTED, f"{name} is on {t.device}, the call runs on {device}")
+            raise SSError(SS_ERR_UNSUPPORTED, f"tensor on {t.device}, the call runs on {device}")
 
 
-class _on_device:
-    """Makes a tensor's GPU the current one for a call: kernels launch on the current GPU."""
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.index != self.back:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.index != self.back:
-            torch.cuda.set_device(self.back)
+def _run(device, fn, *args) -> None:
+    """One call on the current stream of a tensor's GPU, made the current one: kernels launch on the current GPU."""
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status != SS_OK:
+        raise SSError(status)
 
 
 def rotary_steps(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0,
@@ -676,26 +675,28 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, steps: torch.Tensor, layout: str 
            inverse: bool = False, out=None):
     """Rotary positions on x [T, H, D] (bf16 or f32; any token and head strides), rot_dim = 2 * len(steps); pos: int32
     [T]. out may be x (in place); else it must not overlap x. inverse turns back (the gradient's direction)."""
-    _need_heads(x, x.shape if x.dim() == 3 else (0, 0, 0), "x")
+    _need_heads(x, x.shape, "x")
     T, H, D = x.shape
-    if layout not in ROPE_LAYOUT:
+    lay = ROPE_LAYOUT.get(layout)
+    if lay is None:
         raise SSError(SS_ERR_UNSUPPORTED, f"layout {layout!r}: one of {', '.join(ROPE_LAYOUT)}")
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
         raise SSError(SS_ERR_DTYPE, f"x: needs bf16 or f32, has {x.dtype}")
-    _need_dtype(steps, torch.int64, "steps")
+    _need_ints(pos, T, "pos")
+    if steps.dtype is not torch.int64:
+        raise SSError(SS_ERR_DTYPE, f"steps: needs {torch.int64}, has {steps.dtype}")
     if steps.dim() != 1 or not steps.is_contiguous():
         raise SSError(SS_ERR_SHAPE, f"steps: needs a contiguous vector, has {list(steps.shape)}")
     if out is not None:
         _need_heads(out, (T, H, D), "out")
         _need_dtype(out, x.dtype, "out")
-    _on_gpu(x, pos, steps, out)
-    _need_ints(pos, T, "pos", x.device)
-    _same_device(x.device, steps=steps, out=out)
-    y = out if out is not None else torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    with _on_device(x.device):
-        _check(lib.ss_rotary(_ptr(x), dtype_code(x.dtype), T, H, D, x.stride(0), x.stride(1), _ptr(pos), _ptr(steps),
-                             2 * steps.numel(), ROPE_LAYOUT[layout], mscale, int(inverse), _ptr(y), y.stride(0),
-                             y.stride(1), _stream(x.device)))
+    dev = x.device
+    _same_gpu(dev, pos, steps, out)
+    y = out if out is not None else x.new_empty((T, H, D))
+    xt, xh, _ = x.stride()
+    yt, yh, _ = y.stride()
+    _run(dev, lib.ss_rotary, x.data_ptr(), _FROM_TORCH[x.dtype], T, H, D, xt, xh, pos.data_ptr(), steps.data_ptr(),
+         2 * steps.shape[0], lay, mscale, inverse, y.data_ptr(), yt, yh)
     return y
 
 
@@ -709,40 +710,43 @@ def attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k=None
     strides), cu_q / cu_k int32 [B + 1] row bounds (None: one sequence), k_len int32 [B] keys in use (caches with
     room). scale defaults to 1 / sqrt(D). lse: a float32 [Hq, Tq] tensor that receives the rows' log-sum-exp.
     Calls with few query rows per sequence take a workspace from torch's allocator unless one is passed."""
-    _need_heads(q, q.shape if q.dim() == 3 else (0, 0, 0), "q")
-    _need_heads(k, k.shape if k.dim() == 3 else (0, 0, 0), "k")
+    _need_heads(q, q.shape, "q")
+    _need_heads(k, k.shape, "k")
     Tq, Hq, D = q.shape
-    Tk, Hkv, _ = k.shape
-    _need_heads(k, (Tk, Hkv, D), "k")
+    Tk, Hkv, Dk = k.shape
+    if Dk != D:
+        raise SSError(SS_ERR_SHAPE, f"heads of {D} in q, of {Dk} in k")
     _need_heads(v, (Tk, Hkv, D), "v")
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        _need_dtype(t, torch.bfloat16, name)
+        if t is not None and t.dtype is not torch.bfloat16:
+            raise SSError(SS_ERR_DTYPE, f"{name}: needs {torch.bfloat16}, has {t.dtype}")
     if out is not None:
         _need_heads(out, (Tq, Hq, D), "out")
-    _need_dtype(lse, torch.float32, "lse")
-    if lse is not None and (tuple(lse.shape) != (Hq, Tq) or not lse.is_contiguous()):
-        raise SSError(SS_ERR_SHAPE, f"lse: needs contiguous [{Hq}, {Tq}], has {list(lse.shape)}")
-    B = cu_q.numel() - 1 if cu_q is not None else cu_k.numel() - 1 if cu_k is not None else 1
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (Hq, Tq) or not lse.is_contiguous()):
+        raise SSError(SS_ERR_SHAPE, f"lse: needs contiguous float32 [{Hq}, {Tq}], has {lse.dtype} {list(lse.shape)}")
+    B = cu_q.shape[0] - 1 if cu_q is not None else cu_k.shape[0] - 1 if cu_k is not None else 1
     if B < 0:
         raise SSError(SS_ERR_SHAPE, "cu_q and cu_k hold one value more than there are sequences")
-    _on_gpu(q, k, v, cu_q, cu_k, k_len, out, lse, workspace)
+    _need_ints(cu_q, B + 1, "cu_q")
+    _need_ints(cu_k, B + 1, "cu_k")
+    _need_ints(k_len, B, "k_len")
     dev = q.device
-    _need_ints(cu_q, B + 1, "cu_q", dev)
-    _need_ints(cu_k, B + 1, "cu_k", dev)
-    _need_ints(k_len, B, "k_len", dev)
-    _same_device(dev, k=k, v=v, out=out, lse=lse, workspace=workspace)
-    o = out if out is not None else torch.empty((Tq, Hq, D), dtype=q.dtype, device=dev)
-    ws, nbytes = workspace, 0
-    if ws is None:
-        need = attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    elif not ws.is_contiguous():
+    _same_gpu(dev, k, v, cu_q, cu_k, k_len, out, lse, workspace)
+    o = out if out is not None else q.new_empty((Tq, Hq, D))
+    nbytes = 0
+    if workspace is None:
+        nbytes = lib.ss_attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D)
+        if nbytes > 0:
+            workspace = q.new_empty(nbytes, dtype=torch.uint8)
+    elif not workspace.is_contiguous():
         raise SSError(SS_ERR_SHAPE, "workspace is not contiguous")
-    if ws is not None:
-        nbytes = ws.numel() * ws.element_size()
-    with _on_device(dev):
-        _check(lib.ss_attn(_ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
-                           v.stride(1), _ptr(o), o.stride(0), o.stride(1), _ptr(lse), Tq, Tk, B, Hq, Hkv, D, _ptr(cu_q),
-                           _ptr(cu_k), _ptr(k_len), D ** -0.5 if scale is None else scale, int(causal), _ptr(ws), nbytes,
-                           _stream(dev)))
+    else:
+        nbytes = _bytes(workspace)
+    qt, qh, _ = q.stride()
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    ot, oh, _ = o.stride()
+    _run(dev, lib.ss_attn, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, o.data_ptr(), ot, oh,
+         _ptr(lse), Tq, Tk, B, Hq, Hkv, D, _ptr(cu_q), _ptr(cu_k), _ptr(k_len), D ** -0.5 if scale is None else scale,
+         causal, _ptr(workspace), max(nbytes, 0))
     return o

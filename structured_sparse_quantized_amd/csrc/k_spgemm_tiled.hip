@@ -430,6 +430,14 @@ __device__ __forceinline__ void spgemm_body(int R, int C, int KS, const uint8_t*
   }
 #pragma unroll
   for (int u = 0; u < TJ; ++u) s_b[u] = has_b ? scl[BM + (wn * TJ + u) * 16 + r16] : 1.0f;
+  float res[TI][TJ][4];  // the general epilogue's residuals, all on their way before the first store
+  if constexpr (YT == 3) {
+#pragma unroll
+    for (int t = 0; t < TI; ++t)
+#pragma unroll
+      for (int u = 0; u < TJ; ++u)
+        load_residual<SIDE_X>(res[t][u], r0 + (wm * TI + t) * 16 + 4 * jj, min(c0 + (wn * TJ + u) * 16 + r16, C - 1), R, ep);
+  }
 #pragma unroll
   for (int t = 0; t < TI; ++t) {
 #pragma unroll
@@ -451,7 +459,7 @@ __device__ __forceinline__ void spgemm_body(int R, int C, int KS, const uint8_t*
           y[q] = __fmul_rn(__fmul_rn((float)acc[t][u][q], s1), s2);
         }
       }
-      if constexpr (YT == 3) store_epilogue<SIDE_X>(Y, ldy, ar, bc, R, y, ep);
+      if constexpr (YT == 3) store_epilogue<SIDE_X>(Y, ldy, ar, bc, R, y, res[t][u], ep);
       else store_out<YT, SIDE_X>(Y, ldy, ar, bc, R, y, yi);
     }
   }
@@ -530,6 +538,10 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
   const int r16 = lane & 15, jj = lane >> 4;
   const int KS4 = (KS + 3) / 4, KSP = 4 * KS4;
   const int g0 = KS4 * wave / NW, g1 = KS4 * (wave + 1) / NW;  // this wave's 4-step groups
+  float res[4];
+  if constexpr (YT == 3) {  // under the product
+    if (wave < NCT) load_residual<false>(res, rb * 16 + 4 * jj, min(wave * 16 + r16, C - 1), R, ep);
+  }
   Acc acc[NCT];
 #pragma unroll
   for (int c = 0; c < NCT; ++c) acc[c] = Acc{0, 0, 0, 0};
@@ -596,7 +608,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
           y[q] = f;
         }
       }
-      if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, ep);
+      if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, res, ep);
       else store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
     }
   }
@@ -1005,7 +1017,8 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(int R, int C, int RP
   const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int bc = (int)(idx / quads), ar = (int)(idx % quads) * 4;
   if (bc >= C || ar >= R) return;
-  float y[4];
+  float y[4], res[4];
+  if constexpr (YT == 3) load_residual<false>(res, ar, bc, R, ep);
   int32_t yi[4];
   if constexpr (AB == 0) {
     int4 s = make_int4(0, 0, 0, 0);
@@ -1031,7 +1044,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(int R, int C, int RP
       y[q] = f;
     }
   }
-  if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, ep);
+  if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, res, ep);
   else store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
 }
 

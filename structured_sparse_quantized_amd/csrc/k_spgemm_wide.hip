@@ -35,6 +35,7 @@
 // over the step's columns (with one wave per SIMD, a run of loads would leave the matrix core idle while it
 // issues: spreading them was 6-13% faster than issuing the stage at the top of the step).
 #include <algorithm>
+#include <utility>
 
 #include "ss_device.h"
 #include "ss_kernels.h"
@@ -69,7 +70,7 @@ template <int BN, int W> struct Shape {
   static constexpr bool ADB = TJ == 8;            // A fragments double-buffered
   static constexpr int SLOTS = ADB ? 2 : 3;       // loads per column
   static_assert(PA * NW * 16 == BM && PB * NW * 8 == BN && TJ <= TJMAX && PA <= PAMAX, "load split");
-  static_assert((BM + BN) * 4 <= 8 * 1024, "the epilogue scales fit the index-word slot");
+  static_assert((512 + NW * 128) * 4 <= 8 * 1024, "the epilogue scales and biases fit the index-word slot");
 };
 template <int BN> constexpr int occupancy() { return BN == 256 ? 1 : 2; }  // workgroups per CU
 template <int AB> constexpr int meta_slot() { return RBT * Meta<AB>::BLOCK; }    // 16 KB / 8 KB
@@ -82,6 +83,12 @@ constexpr int vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0x
 // raw buffer resource over [p, p + bytes): base and size in scalar registers, 32-bit untyped data
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+
+// column(0), .., column(TJ - 1) as compile-time constants, pass(p) after every UP of them
+template <int UP, int... U, typename F, typename G>
+__device__ __forceinline__ void each_column(std::integer_sequence<int, U...>, const F& column, const G& pass) {
+  ((column(std::integral_constant<int, U>{}), U % UP == UP - 1 ? pass(U / UP) : (void)0), ...);
 }
 
 // (arrays that the loads index have fixed lengths: a length that depends on a template parameter in these
@@ -386,7 +393,7 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
     // takes the same two multiplies with no branch per value.
     const float* scl = reinterpret_cast<const float*>(smem + META);
     const bool has_a = sa != nullptr, has_b = sb != nullptr;
-    float s_a[TI][4], s_b[TJMAX];
+    float s_a[TI][4], s_b[TJMAX];  // (the general epilogue reads them where it needs them)
   #pragma unroll
     for (int t = 0; t < TI; ++t) {
       const float4 v = *reinterpret_cast<const float4*>(scl + (wm * TI + t) * 16 + 4 * jj);
@@ -411,10 +418,138 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
       }
     };
     if constexpr (YT == 3) {
-      // The general epilogue. The scaled sums go through the idle ring as float32 rows of tokens, and leave 8
-      // columns per lane and step: bias, activation and gate there, in one small loop (unrolled over a lane's
-      // accumulators the activations' code is too long to unroll, and the accumulators would go to memory), and
-      // the residual on the unrounded value.
+      if constexpr (!SX) {
+        const int ar0 = r0 + wm * TI * 16;
+        const bool inside = ar0 + 128 <= R;
+        if (!ep.f32 && (!ep.res || (!ep.gated && inside && (ep.ldr & 3) == 0))) {
+          // The general epilogue to bf16, weight-sparse side: bias, activation, gate and residual in the accumulators'
+          // own lanes (4 channels of one token each; column by column of the tile, so that the activations stay
+          // short unrolled runs), then rows of bf16 through the idle ring as below. The residuals of a column are
+          // on their way while the column is finished.
+          constexpr int STRIDE = 128 * 2 + 16;
+          constexpr int UP = up_rows(TJ, META / NW / (16 * STRIDE)), NP = TJ / UP, RP = 16 * UP;
+          static_assert(NW * RP * STRIDE <= META, "staging fits the stage ring");
+          SS_LDS uint8_t* stg = (SS_LDS uint8_t*)smem + wave * RP * STRIDE;
+          const int col0 = ar0 >> ep.gated, ncol = R >> ep.gated, wide = 128 >> ep.gated;
+          const bool yvec = inside && (ldy & 7) == 0;
+          // The channels' scales and biases are read from LDS for every column (64-lane reads of 4 addresses):
+          // kept in registers beside the accumulators they would spill. A wave keeps its 128 biases behind the scales.
+          const int wb = 512 + wave * 128;
+          if (ep.bias) {
+            float* b = reinterpret_cast<float*>(smem + META) + wb;
+            b[lane] = ep.bias[min(ar0 + lane, R - 1)];
+            b[lane + 64] = ep.bias[min(ar0 + lane + 64, R - 1)];
+            __builtin_amdgcn_wave_barrier();
+          }
+          auto column = [&](auto uc) __attribute__((always_inline)) {
+              constexpr int u = decltype(uc)::value, uu = u % UP;
+              uint2 res[TI];
+              if (ep.res) {
+                const uint16_t* at = static_cast<const uint16_t*>(ep.res) +
+                                     (int64_t)min(c0 + (wn * TJ + u) * 16 + r16, C - 1) * ep.ldr + ar0 + 4 * jj;
+                asm volatile("" : "+v"(at));  // one address and constant offsets, not an address per block
+  #pragma unroll
+                for (int t = 0; t < TI; ++t) res[t] = *reinterpret_cast<const uint2*>(at + t * 16);
+              }
+              uint32_t so = 0;
+              asm volatile("" : "+v"(so));
+              const float* sc = scl + so + wm * TI * 16 + 4 * jj;
+              float y[TI * 4];
+  #pragma unroll
+              for (int t = 0; t < TI; ++t) {
+                const float4 v = *reinterpret_cast<const float4*>(sc + t * 16);
+                const float s4[4] = {v.x, v.y, v.z, v.w};
+  #pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  y[4 * t + q] = __fmul_rn(__fmul_rn((float)acc[t][u][q], s_b[u]), has_a ? s4[q] : 1.0f);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+              if (ep.bias) {
+                const float* bs = scl + so + wb + 4 * jj;
+  #pragma unroll
+                for (int t = 0; t < TI; ++t) {
+                  const float4 v = *reinterpret_cast<const float4*>(bs + t * 16);
+                  y[4 * t] += v.x, y[4 * t + 1] += v.y, y[4 * t + 2] += v.z, y[4 * t + 3] += v.w;
+                }
+              }
+              SS_LDS uint8_t* d = stg + (uu * 16 + r16) * STRIDE;
+              if (ep.gated) {
+                float g[TI * 2];
+  #pragma unroll
+                for (int i = 0; i < TI * 2; ++i) g[i] = y[2 * i];
+                activate_n<TI * 2, true>(g, ep.act, false);
+  #pragma unroll
+                for (int t = 0; t < TI; ++t)
+                  *reinterpret_cast<SS_LDS uint32_t*>(d + (t * 8 + 2 * jj) * 2) =
+                      pack_bf16x2(g[2 * t] * y[4 * t + 1], g[2 * t + 1] * y[4 * t + 3]);
+              } else {
+                activate_n<TI * 4, true>(y, ep.act, false);
+                if (ep.res) {
+  #pragma unroll
+                  for (int t = 0; t < TI; ++t) {
+                    y[4 * t] += __uint_as_float(res[t].x << 16);
+                    y[4 * t + 1] += __uint_as_float(res[t].x & 0xFFFF0000u);
+                    y[4 * t + 2] += __uint_as_float(res[t].y << 16);
+                    y[4 * t + 3] += __uint_as_float(res[t].y & 0xFFFF0000u);
+                  }
+                }
+  #pragma unroll
+                for (int t = 0; t < TI; ++t)
+                  *reinterpret_cast<SS_LDS tiled::v2i*>(d + (t * 16 + 4 * jj) * 2) =
+                      tiled::v2i{(int)pack_bf16x2(y[4 * t], y[4 * t + 1]), (int)pack_bf16x2(y[4 * t + 2], y[4 * t + 3])};
+              }
+              __builtin_amdgcn_sched_barrier(0);  // one column's temporaries at a time
+          };
+          auto pass = [&](int p) {
+            __builtin_amdgcn_wave_barrier();
+            const int bc0 = c0 + (wn * TJ + p * UP) * 16, cpr = wide / 8, sh = ep.gated ? 3 : 4;
+            uint16_t* Yh = static_cast<uint16_t*>(Y);
+            if (yvec && bc0 + RP <= C) {
+              constexpr int IT = RP * 16 / 64;
+              v4i v[IT];
+  #pragma unroll
+              for (int k = 0; k < IT; ++k) {
+                const int i = lane + 64 * k;
+                if (k < IT >> ep.gated)
+                  v[k] = *reinterpret_cast<const SS_LDS v4i*>(stg + (i >> sh) * STRIDE + (i & (cpr - 1)) * 16);
+              }
+  #pragma unroll
+              for (int k = 0; k < IT; ++k) {
+                const int i = lane + 64 * k;
+                if (k < IT >> ep.gated)
+                  __builtin_nontemporal_store(
+                      v[k], reinterpret_cast<v4i*>(Yh + (int64_t)(bc0 + (i >> sh)) * ldy + col0 + (i & (cpr - 1)) * 8));
+              }
+            } else {
+  #pragma unroll 1
+              for (int i = lane; i < RP * cpr; i += 64) {
+                const int row = i >> sh, col = col0 + (i & (cpr - 1)) * 8;
+                if (bc0 + row >= C) continue;
+                const v4i v = *reinterpret_cast<const SS_LDS v4i*>(stg + row * STRIDE + (i & (cpr - 1)) * 16);
+                uint16_t* dst = Yh + (int64_t)(bc0 + row) * ldy + col;
+                if ((ldy & 7) == 0 && col + 8 <= ncol) {
+                  __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dst));
+                } else {
+                  const uint32_t w[4] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+  #pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    if (col + e < ncol) dst[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                }
+              }
+            }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+          };
+          // columns and passes in order, unrolled by hand (a loop this long is not unrolled, and the accumulators
+          // would go to memory)
+          each_column<UP>(std::make_integer_sequence<int, TJ>{}, column, pass);
+          return;
+        }
+      }
+      // To float32, and the sparse-activation side (where a lane holds one channel of 4 tokens): the scaled sums go
+      // through the idle ring as float32 rows of tokens, and leave 8 columns per lane and step, with bias,
+      // activation and gate in one small loop (unrolled over a lane's accumulators the exact activations' code is
+      // too long to unroll, and the accumulators would go to memory), and the residual on the unrounded value.
       constexpr int LD = (SX ? 16 * TJ : 128) + 4;  // floats of a staged row, padded against bank conflicts
       constexpr int UB = SX ? TI : TJ;                                     // 16-token blocks of this wave
       constexpr int UP = up_rows(UB, META / NW / (16 * LD * 4)), NP = UB / UP, RP = 16 * UP;  // per pass; passes
@@ -422,21 +557,43 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
       SS_LDS float* stg = (SS_LDS float*)((SS_LDS uint8_t*)smem + wave * RP * LD * 4);
       const int tok0 = SX ? r0 + wm * TI * 16 : c0 + wn * TJ * 16, ntok = SX ? R : C;
       const int ch0 = SX ? c0 + wn * TJ * 16 : r0 + wm * TI * 16, nch = SX ? C : R;
-      const int cpr = (SX ? 2 * TJ : 16) >> ep.gated;  // 8-column pieces of a row of Y
+      // A lane keeps its 8-column piece of a row (and that piece's bias) and takes every rps-th row of a pass.
+      const int cpr = (SX ? 2 * TJ : 16) >> ep.gated, rps = 64 / cpr, steps = RP / rps, row0 = lane / cpr;
+      static_assert(RP >= 2 * 64 / (SX ? TJ : 8), "a pass has two steps or more, an even number");
+      const Leave out(ep, Y, ldy, lane % cpr, ch0, nch);
+      auto fetch = [&](Leave::Res* r, int p, int k) {
+  #pragma unroll
+        for (int x = 0; x < 2; ++x)
+          out.residual(r[x], min(tok0 + p * RP + row0 + (k + x) * rps, ntok - 1));
+      };
+      Leave::Res cur[2];
+      fetch(cur, 0, 0);
   #pragma unroll
       for (int p = 0; p < NP; ++p) {
+        // the scales again from LDS (their slot stays): kept in registers through the passes they would spill
+        uint32_t so = 0;
+        asm volatile("" : "+v"(so));
+        const float* scp = scl + so;
+        auto scaled = [&](int t, int u, float* y) {
+          const float4 va = *reinterpret_cast<const float4*>(scp + (wm * TI + t) * 16 + 4 * jj);
+          const float a4[4] = {va.x, va.y, va.z, va.w}, b1 = scp[256 + (wn * TJ + u) * 16 + r16];
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float a1 = has_a ? a4[q] : 1.0f, bb = has_b ? b1 : 1.0f;
+            y[q] = __fmul_rn(__fmul_rn((float)acc[t][u][q], SX ? a1 : bb), SX ? bb : a1);
+          }
+        };
   #pragma unroll
         for (int uu = 0; uu < UP; ++uu) {
   #pragma unroll
           for (int x = 0; x < (SX ? TJ : TI); ++x) {
             float y[4];
-            int32_t yi[4];
             if constexpr (SX) {  // 4 tokens of one channel
-              result(p * UP + uu, x, y, yi);
+              scaled(p * UP + uu, x, y);
   #pragma unroll
               for (int q = 0; q < 4; ++q) stg[(uu * 16 + 4 * jj + q) * LD + x * 16 + r16] = y[q];
             } else {  // 4 channels of one token
-              result(x, p * UP + uu, y, yi);
+              scaled(x, p * UP + uu, y);
               *reinterpret_cast<SS_LDS v4i*>(stg + (uu * 16 + r16) * LD + x * 16 + 4 * jj) =
                   v4i{__float_as_int(y[0]), __float_as_int(y[1]), __float_as_int(y[2]), __float_as_int(y[3])};
             }
@@ -444,9 +601,17 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
         }
         __builtin_amdgcn_wave_barrier();
   #pragma unroll 1
-        for (int i = lane; i < RP * cpr; i += 64) {
-          const int row = i / cpr, piece = i % cpr, tok = tok0 + p * RP + row;
-          if (tok < ntok) leave8((const float*)(stg + row * LD), piece, Y, ldy, tok, ch0, nch, ep);
+        for (int k = 0; k < steps; k += 2) {  // two rows a step; the next two rows' residuals are on their way
+          Leave::Res nxt[2];
+          if (k + 2 < steps) fetch(nxt, p, k + 2);
+          else if (p + 1 < NP) fetch(nxt, p + 1, 0);
+  #pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int row = row0 + (k + x) * rps, tok = tok0 + p * RP + row;
+            if (tok < ntok) out.row((const float*)(stg + row * LD), cur[x], tok);
+          }
+          cur[0] = nxt[0];
+          cur[1] = nxt[1];
         }
         __builtin_amdgcn_wave_barrier();
       }

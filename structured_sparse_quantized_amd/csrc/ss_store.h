@@ -45,19 +45,35 @@ __device__ __forceinline__ float over_1p_exp(float num, float z, bool f32) {  //
   if (f32) return num / (1.0f + expf(-z));
   return num * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * z));
 }
-template <int N> __device__ __forceinline__ void activate_n(float* z, int act, bool f32) {
+// erf for results rounded to bf16: formula 7.1.26 of Abramowitz and Stegun, "Handbook of Mathematical Functions"
+// (absolute error 1.5e-7), with the chip's reciprocal and power: a third of the instructions of erff.
+__device__ __forceinline__ float erf_short(float x) {
+  const float a = fabsf(x), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, a, 1.0f));
+  float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  p = __builtin_fmaf(p, t, 1.421413741f);
+  p = __builtin_fmaf(p, t, -0.284496736f);
+  p = __builtin_fmaf(p, t, 0.254829592f);
+  return copysignf(1.0f - p * t * __builtin_amdgcn_exp2f(-1.44269504088896340736f * a * a), x);
+}
+// SHORT: for bf16 results only (f32 is false).
+template <int N, bool SHORT = false> __device__ __forceinline__ void activate_n(float* z, int act, bool f32) {
+  if constexpr (SHORT) f32 = false;
   if (act == 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] = fmaxf(z[i], 0.0f);
   } else if (act == 2) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678118654752440f));
-  } else if (act >= 3) {  // z / (1 + exp(-u)): u = z, or the tanh form's sqrt(8 / pi) (z + 0.044715 z^3)
-#pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float u = act == 3 ? 1.59576912160573071176f * __builtin_fmaf(0.044715f * z[i] * z[i], z[i], z[i]) : z[i];
-      z[i] = over_1p_exp(z[i], u, f32);
+      const float x = z[i] * 0.70710678118654752440f;
+      z[i] = 0.5f * z[i] * (1.0f + (f32 ? erff(x) : erf_short(x)));
     }
+  } else if (act == 3) {  // the tanh form: u = sqrt(8 / pi) (z + 0.044715 z^3)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      z[i] = over_1p_exp(z[i], 1.59576912160573071176f * __builtin_fmaf(0.044715f * z[i] * z[i], z[i], z[i]), f32);
+  } else if (act == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = over_1p_exp(z[i], z[i], f32);
   }
 }
 __device__ __forceinline__ float load_res(const Epilogue& e, int64_t at) {
@@ -92,31 +108,53 @@ __device__ __forceinline__ void finish(float* y, int64_t ar, int64_t bc, int64_t
   }
 }
 
-// store_out with the general epilogue: all lanes of a wave whose bc is below the count of B rows call it together.
+// store_out with the general epilogue, in two steps: the residuals of a lane's 4 results (the loads of several
+// tiles are issued before the first store: the residual may be Y, so none could move over one), then the rest.
+// All lanes of a wave whose bc is below the count of B rows call them together.
+template <bool SIDE_X>
+__device__ __forceinline__ void load_residual(float* r, int64_t ar, int64_t bc, int64_t R, const Epilogue& e) {
+  if (!e.res) return;
+  if constexpr (SIDE_X) {
+    const int64_t col = e.gated ? bc >> 1 : bc;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[q] = load_res(e, min(ar + q, R - 1) * e.ldr + col);
+  } else {
+    const int n = e.gated ? 2 : 4;
+    const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
+    if (n == 4 && !e.f32 && (e.ldr & 3) == 0 && col + 4 <= cols) {
+      const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.res) + bc * e.ldr + col);
+      r[0] = __uint_as_float(x.x << 16);
+      r[1] = __uint_as_float(x.x & 0xFFFF0000u);
+      r[2] = __uint_as_float(x.y << 16);
+      r[3] = __uint_as_float(x.y & 0xFFFF0000u);
+      return;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < n) r[q] = load_res(e, bc * e.ldr + min(col + q, cols - 1));
+  }
+}
 template <bool SIDE_X>
 __device__ __forceinline__ void store_epilogue(void* Y, int64_t ldy, int64_t ar, int64_t bc, int64_t R, float* y,
-                                               const Epilogue& e) {
+                                               const float* r, const Epilogue& e) {
   finish<SIDE_X>(y, ar, bc, R, e);
+  if (e.res) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (SIDE_X || q < 2 || !e.gated) y[q] += r[q];
+  }
   if constexpr (SIDE_X) {
     if (e.gated && (bc & 1)) return;
     const int64_t col = e.gated ? bc >> 1 : bc;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (ar + q >= R) break;
-      const float v = e.res ? y[q] + load_res(e, (ar + q) * e.ldr + col) : y[q];
-      store_one(Y, (ar + q) * ldy + col, v, e.f32);
+      store_one(Y, (ar + q) * ldy + col, y[q], e.f32);
     }
   } else {
     const int n = e.gated ? 2 : 4;
     const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
-    if (n == 4 && !e.f32 && (ldy & 3) == 0 && (e.ldr & 3) == 0 && col + 4 <= cols) {  // 8-byte vectors
-      if (e.res) {
-        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.res) + bc * e.ldr + col);
-        y[0] += __uint_as_float(r.x << 16);
-        y[1] += __uint_as_float(r.x & 0xFFFF0000u);
-        y[2] += __uint_as_float(r.y << 16);
-        y[3] += __uint_as_float(r.y & 0xFFFF0000u);
-      }
+    if (n == 4 && !e.f32 && (ldy & 3) == 0 && col + 4 <= cols) {  // 8-byte vectors
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + bc * ldy + col) =
           make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
       return;
@@ -124,72 +162,103 @@ __device__ __forceinline__ void store_epilogue(void* Y, int64_t ldy, int64_t ar,
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (q >= n || col + q >= cols) break;
-      const float v = e.res ? y[q] + load_res(e, bc * e.ldr + col + q) : y[q];
-      store_one(Y, bc * ldy + col + q, v, e.f32);
+      store_one(Y, bc * ldy + col + q, y[q], e.f32);
     }
   }
 }
 
-// Columns 8 piece .. +7 of one row of Y from a staged row of scaled sums (channels ch0, ch0 + 1, ..; `nch` of
-// them in all): 8 channels, or with a gate the 16 channels of 8 pairs.
-__device__ __forceinline__ void leave8(const float* row, int piece, void* Y, int64_t ldy, int64_t tok, int ch0, int nch,
-                                       const Epilogue& e) {
-  float f[16];
-  const int n = e.gated ? 16 : 8, first = ch0 + piece * n;
-  if (first >= nch) return;
+// Eight columns of one row of Y from a staged row of scaled sums (channels ch0, ch0 + 1, ..; nch of them in all):
+// piece i holds 8 channels, or with a gate the 16 channels of 8 pairs.
+struct Leave {
+  typedef float v4fl __attribute__((ext_vector_type(4)));
+  typedef uint32_t v4ul __attribute__((ext_vector_type(4)));
+  struct Res {
+    v4ul a, b;  // 8 bf16 in a, or 8 f32
+  };
+  const Epilogue& e;
+  void* Y;
+  int64_t ldy;
+  int piece, first, nch, col, ncol;
+  bool vec;        // whole 16-byte pieces of Y and of the residual
+  float bias[16];  // of this lane's piece
+
+  __device__ __forceinline__ Leave(const Epilogue& ep, void* y, int64_t ld, int pc, int ch0, int nc)
+      : e(ep), Y(y), ldy(ld), piece(pc), nch(nc) {
+    first = ch0 + (piece << (3 + e.gated));
+    col = (ch0 >> e.gated) + piece * 8;
+    ncol = nch >> e.gated;
+    const int per16 = e.f32 ? 3 : 7;  // elements of 16 bytes, less one
+    vec = col + 8 <= ncol && (ldy & per16) == 0 && (!e.res || (e.ldr & per16) == 0);
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    if (i >= n) break;
-    const float4 x = *reinterpret_cast<const float4*>(row + piece * n + i);
-    f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+    for (int i = 0; i < 16; ++i) bias[i] = e.bias && (i < 8 || e.gated) ? e.bias[min(first + i, nch - 1)] : 0.0f;
   }
-  if (e.bias) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) f[i] = f[i] + e.bias[min(first + i, nch - 1)];
-  }
-  float g[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = e.gated ? f[2 * i] : f[i];
-  activate_n<8>(g, e.act, e.f32);
-  if (e.gated) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] *= f[2 * i + 1];
-  }
-  const int col = (e.gated ? ch0 >> 1 : ch0) + piece * 8, ncol = e.gated ? nch >> 1 : nch;
-  const int per16 = e.f32 ? 3 : 7;  // elements of 16 bytes, less one
-  if (col + 8 <= ncol && (ldy & per16) == 0 && (!e.res || (e.ldr & per16) == 0)) {
-    typedef float v4fl __attribute__((ext_vector_type(4)));
-    typedef uint32_t v4ul __attribute__((ext_vector_type(4)));
+  __device__ __forceinline__ void residual(Res& r, int64_t tok) const {
+    if (!e.res || !vec) return;
     if (e.f32) {
-      v4fl lo{g[0], g[1], g[2], g[3]}, hi{g[4], g[5], g[6], g[7]};
-      if (e.res) {
-        const v4fl* r = reinterpret_cast<const v4fl*>(static_cast<const float*>(e.res) + tok * e.ldr + col);
-        lo += r[0];
-        hi += r[1];
-      }
-      v4fl* d = reinterpret_cast<v4fl*>(static_cast<float*>(Y) + tok * ldy + col);
-      __builtin_nontemporal_store(lo, d);
-      __builtin_nontemporal_store(hi, d + 1);
+      const v4ul* p = reinterpret_cast<const v4ul*>(static_cast<const float*>(e.res) + tok * e.ldr + col);
+      r.a = p[0];
+      r.b = p[1];
     } else {
+      r.a = *reinterpret_cast<const v4ul*>(static_cast<const uint16_t*>(e.res) + tok * e.ldr + col);
+    }
+  }
+  __device__ __forceinline__ void row(const float* staged, const Res& r, int64_t tok) const {
+    if (first >= nch) return;
+    float f[16], g[8];
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      if (i >= 8 && !e.gated) break;
+      const float4 x = *reinterpret_cast<const float4*>(staged + (piece << (3 + e.gated)) + i);
+      f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+    }
+    if (e.bias) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < 8 || e.gated) f[i] = f[i] + bias[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = e.gated ? f[2 * i] : f[i];
+    activate_n<8>(g, e.act, e.f32);
+    if (e.gated) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] *= f[2 * i + 1];
+    }
+    if (vec && e.f32) {
       if (e.res) {
-        const v4ul r = *reinterpret_cast<const v4ul*>(static_cast<const uint16_t*>(e.res) + tok * e.ldr + col);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          g[2 * i] += __uint_as_float(r[i] << 16);
-          g[2 * i + 1] += __uint_as_float(r[i] & 0xFFFF0000u);
+          g[i] += __uint_as_float(r.a[i]);
+          g[4 + i] += __uint_as_float(r.b[i]);
+        }
+      }
+      v4fl* d = reinterpret_cast<v4fl*>(static_cast<float*>(Y) + tok * ldy + col);
+      __builtin_nontemporal_store(v4fl{g[0], g[1], g[2], g[3]}, d);
+      __builtin_nontemporal_store(v4fl{g[4], g[5], g[6], g[7]}, d + 1);
+    } else if (vec) {
+      if (e.res) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[2 * i] += __uint_as_float(r.a[i] << 16);
+          g[2 * i + 1] += __uint_as_float(r.a[i] & 0xFFFF0000u);
         }
       }
       const v4ul v{pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7])};
       __builtin_nontemporal_store(v, reinterpret_cast<v4ul*>(static_cast<uint16_t*>(Y) + tok * ldy + col));
-    }
-    return;
-  }
+    } else {
+      int c = col;
+      asm volatile("" : "+v"(c));  // addresses made here, not kept for the whole tile
+      float x[8];
+      if (e.res) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (col + i >= ncol) break;
-    store_one(Y, tok * ldy + col + i, e.res ? g[i] + load_res(e, tok * e.ldr + col + i) : g[i], e.f32);
+        for (int i = 0; i < 8; ++i) x[i] = load_res(e, tok * e.ldr + min(c + i, ncol - 1));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (c + i >= ncol) break;
+        store_one(Y, tok * ldy + c + i, e.res ? g[i] + x[i] : g[i], e.f32);
+      }
+    }
   }
-}
+};
 
 }  // namespace ss
