@@ -1,7 +1,8 @@
 """Python binding of ``libss.so``, the gfx950 structured-sparse quantised GEMM library.
 
-Argument marshalling only: every step runs in the HIP kernels behind the C ABI
-declared in ``include/ss.h``. PyTorch supplies device memory and the current
+Argument marshalling only (ctypes; the calls that run between products through
+``_ssbind``): every step runs in the HIP kernels behind the C ABI declared in
+``include/ss.h``. PyTorch supplies device memory and the current
 stream. There is no CPU fallback: importing this package raises if the
 library has not been built, and every call raises ``SSError`` on a non-OK
 status.
@@ -40,6 +41,11 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libss.so")
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with structured_sparse_quantized_amd.build.build()")
 lib = ctypes.CDLL(_LIB_PATH)
+try:
+    from . import _ssbind  # argument checks and marshalling of the calls between products (csrc/ss_bind.cpp)
+except ImportError as e:
+    raise ImportError(f"the binding _ssbind.so next to {_LIB_PATH} does not load ({e}): build it with "
+                      "structured_sparse_quantized_amd.build.build()") from e
 
 SS_OK, SS_ERR_NULL, SS_ERR_SHAPE, SS_ERR_ALIGN, SS_ERR_DTYPE, SS_ERR_PATTERN, SS_ERR_UNSUPPORTED, SS_ERR_HIP = range(8)
 SS_F32, SS_BF16, SS_I8, SS_FP8E4M3, SS_I32 = range(5)
@@ -118,6 +124,9 @@ class SSError(RuntimeError):
         super().__init__(f"{msg}: {detail}")
 
 
+_ssbind.set_error(SSError)
+
+
 # Size checks made before a call reaches the C ABI: the library validates sizes, strides and alignment, but
 # it cannot see how large a tensor behind a pointer is. A tensor smaller than the region a call reads or
 # writes raises SSError(SS_ERR_SHAPE), a host tensor SSError(SS_ERR_UNSUPPORTED), before anything launches.
@@ -182,11 +191,11 @@ def dtype_code(d) -> int:
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _stream(device) -> ctypes.c_void_p:
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -394,39 +403,11 @@ def spgemm_tiled_epilogue(side: int, M: int, N: int, Kc: int, tvals: torch.Tenso
     + residual, all in the product's epilogue and rounded once. gated: weight rows 2j and 2j + 1 are the gate and
     the value of column j, y[:, j] = act(z[:, 2j]) * z[:, 2j + 1], so Y and residual are [M, N / 2]. residual has
     the type of Y (bf16 or f32) and may be `out` itself. workspace: as spgemm_tiled (None takes one where needed)."""
-    y = dtype_code(y_dtype)
-    ab = dtype_code(dense.dtype)
-    act_code = ACTIVATIONS.get(act)
-    if act_code is None:
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise SSError(SS_ERR_UNSUPPORTED, f"act {act!r}: one of {', '.join(ACTIVATIONS)}")
-    if y not in (SS_BF16, SS_F32):
-        raise SSError(SS_ERR_DTYPE, "the output must be bf16 or f32")
-    cols = N // 2 if gated else N
-    rows, dn = (M, N) if side == SS_SPARSE_X else (N, M)
-    _need_bytes(tvals, lib.ss_tiled_vals_bytes(rows, Kc, ab), "tvals")
-    _need_bytes(tmeta, lib.ss_tiled_meta_bytes(rows, Kc, ab), "tmeta")
-    _need_mat(dense, dn, Kc, "dense")
-    for t, n, name in ((sx, M, "sx"), (sw, N, "sw"), (bias, N, "bias")):
-        if t is not None:
-            _need_vec(t, n, name)
-            _need_dtype(t, torch.float32, name)
-    for t, name in ((out, "out"), (residual, "residual")):
-        if t is not None:
-            _need_dtype(t, _TORCH[y], name)
-            _need_mat(t, M, cols, name)
-    dev = dense.device
-    _same_gpu(dev, tvals, tmeta, sx, sw, bias, residual, out, workspace)
-    Y = out if out is not None else dense.new_empty((M, cols), dtype=_TORCH[y])
-    need = lib.ss_spgemm_tiled_workspace_bytes(side, M, N, Kc, ab)
-    if workspace is not None:
-        _need_bytes(workspace, need, "workspace")
-        need = _bytes(workspace)
-    elif need > 0:
-        workspace = dense.new_empty(need, dtype=torch.uint8)
-    _run(dev, lib.ss_spgemm_tiled_epilogue, side, M, N, Kc, ab, tvals.data_ptr(), tmeta.data_ptr(), dense.data_ptr(),
-         dense.stride(0), _ptr(sx), _ptr(sw), _ptr(bias), act_code, gated, _ptr(residual),
-         0 if residual is None else residual.stride(0), y, Y.data_ptr(), Y.stride(0), _ptr(workspace), max(need, 0))
-    return Y
+    return _ssbind.spgemm_tiled_epilogue(side, M, N, Kc, tvals, tmeta, dense, sx, sw, bias, code, gated, residual,
+                                         dtype_code(y_dtype), out, workspace)
 
 
 def spgemm_tiled_batched(side: int, batch: int, M: int, N: int, Kc: int, tvals: torch.Tensor, tmeta: torch.Tensor,
@@ -623,41 +604,6 @@ ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "smooth": 3, "yarn": 4}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 
 
-def _need_heads(t, shape, name: str) -> None:
-    """A [tokens, heads, D] view of this shape whose heads are contiguous."""
-    if t.shape != shape or len(shape) != 3 or (t.stride(2) != 1 and shape[2] > 1 and t.numel() > 0):
-        raise SSError(SS_ERR_SHAPE, f"{name}: needs {list(shape)} with unit stride along the last dimension, has "
-                      f"{list(t.shape)} with strides {list(t.stride())}")
-
-
-def _need_ints(t, n: int, name: str) -> None:
-    if t is None:
-        return
-    if t.dtype is not torch.int32:
-        raise SSError(SS_ERR_DTYPE, f"{name}: needs {torch.int32}, has {t.dtype}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise SSError(SS_ERR_SHAPE, f"{name}: needs {n} contiguous int32 values, has {list(t.shape)}")
-
-
-def _same_gpu(device, *ts) -> None:
-    if device.type != "cuda":
-        raise SSError(SS_ERR_UNSUPPORTED, f"tensor on {device}: the library runs on the GPU only")
-    for t in ts:
-        if t is not None and t.device != device:
-            raise SSError(SS_ERR_UNSUPPORTED, f"tensor on {t.device}, the call runs on {device}")
-
-
-def _run(device, fn, *args) -> None:
-    """One call on the current stream of a tensor's GPU, made the current one: kernels launch on the current GPU."""
-    if torch._C._cuda_getDevice() == device.index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
-    if status != SS_OK:
-        raise SSError(status)
-
-
 def rotary_steps(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0,
                  low: float = 1.0, high: float = 4.0, device="cuda"):
     """The frequencies of `rotary` on `device` (int64 [rot_dim / 2], turns per position times 2^64) and the factor on
@@ -675,29 +621,10 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, steps: torch.Tensor, layout: str 
            inverse: bool = False, out=None):
     """Rotary positions on x [T, H, D] (bf16 or f32; any token and head strides), rot_dim = 2 * len(steps); pos: int32
     [T]. out may be x (in place); else it must not overlap x. inverse turns back (the gradient's direction)."""
-    _need_heads(x, x.shape, "x")
-    T, H, D = x.shape
-    lay = ROPE_LAYOUT.get(layout)
-    if lay is None:
+    code = ROPE_LAYOUT.get(layout)
+    if code is None:
         raise SSError(SS_ERR_UNSUPPORTED, f"layout {layout!r}: one of {', '.join(ROPE_LAYOUT)}")
-    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
-        raise SSError(SS_ERR_DTYPE, f"x: needs bf16 or f32, has {x.dtype}")
-    _need_ints(pos, T, "pos")
-    if steps.dtype is not torch.int64:
-        raise SSError(SS_ERR_DTYPE, f"steps: needs {torch.int64}, has {steps.dtype}")
-    if steps.dim() != 1 or not steps.is_contiguous():
-        raise SSError(SS_ERR_SHAPE, f"steps: needs a contiguous vector, has {list(steps.shape)}")
-    if out is not None:
-        _need_heads(out, (T, H, D), "out")
-        _need_dtype(out, x.dtype, "out")
-    dev = x.device
-    _same_gpu(dev, pos, steps, out)
-    y = out if out is not None else x.new_empty((T, H, D))
-    xt, xh, _ = x.stride()
-    yt, yh, _ = y.stride()
-    _run(dev, lib.ss_rotary, x.data_ptr(), _FROM_TORCH[x.dtype], T, H, D, xt, xh, pos.data_ptr(), steps.data_ptr(),
-         2 * steps.shape[0], lay, mscale, inverse, y.data_ptr(), yt, yh)
-    return y
+    return _ssbind.rotary(x, pos, steps, code, mscale, inverse, out)
 
 
 def attn_workspace_bytes(Tq: int, Tk: int, B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -710,43 +637,4 @@ def attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k=None
     strides), cu_q / cu_k int32 [B + 1] row bounds (None: one sequence), k_len int32 [B] keys in use (caches with
     room). scale defaults to 1 / sqrt(D). lse: a float32 [Hq, Tq] tensor that receives the rows' log-sum-exp.
     Calls with few query rows per sequence take a workspace from torch's allocator unless one is passed."""
-    _need_heads(q, q.shape, "q")
-    _need_heads(k, k.shape, "k")
-    Tq, Hq, D = q.shape
-    Tk, Hkv, Dk = k.shape
-    if Dk != D:
-        raise SSError(SS_ERR_SHAPE, f"heads of {D} in q, of {Dk} in k")
-    _need_heads(v, (Tk, Hkv, D), "v")
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        if t is not None and t.dtype is not torch.bfloat16:
-            raise SSError(SS_ERR_DTYPE, f"{name}: needs {torch.bfloat16}, has {t.dtype}")
-    if out is not None:
-        _need_heads(out, (Tq, Hq, D), "out")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (Hq, Tq) or not lse.is_contiguous()):
-        raise SSError(SS_ERR_SHAPE, f"lse: needs contiguous float32 [{Hq}, {Tq}], has {lse.dtype} {list(lse.shape)}")
-    B = cu_q.shape[0] - 1 if cu_q is not None else cu_k.shape[0] - 1 if cu_k is not None else 1
-    if B < 0:
-        raise SSError(SS_ERR_SHAPE, "cu_q and cu_k hold one value more than there are sequences")
-    _need_ints(cu_q, B + 1, "cu_q")
-    _need_ints(cu_k, B + 1, "cu_k")
-    _need_ints(k_len, B, "k_len")
-    dev = q.device
-    _same_gpu(dev, k, v, cu_q, cu_k, k_len, out, lse, workspace)
-    o = out if out is not None else q.new_empty((Tq, Hq, D))
-    nbytes = 0
-    if workspace is None:
-        nbytes = lib.ss_attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D)
-        if nbytes > 0:
-            workspace = q.new_empty(nbytes, dtype=torch.uint8)
-    elif not workspace.is_contiguous():
-        raise SSError(SS_ERR_SHAPE, "workspace is not contiguous")
-    else:
-        nbytes = _bytes(workspace)
-    qt, qh, _ = q.stride()
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    ot, oh, _ = o.stride()
-    _run(dev, lib.ss_attn, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, o.data_ptr(), ot, oh,
-         _ptr(lse), Tq, Tk, B, Hq, Hkv, D, _ptr(cu_q), _ptr(cu_k), _ptr(k_len), D ** -0.5 if scale is None else scale,
-         causal, _ptr(workspace), max(nbytes, 0))
-    return o
+    return _ssbind.attn(q, k, v, cu_q, cu_k, k_len, causal, scale, out, lse, workspace)

@@ -23,6 +23,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ss_device.h"
 #include "ss_kernels.h"
@@ -37,13 +38,19 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kSlack = 8.0f;     // in powers of two
+constexpr int vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }  // s_waitcnt vmcnt(n)
 constexpr float kLow = -1.0e30f;   // below every finite score's exponent; 2^(kLow - m) = 0
-constexpr int NW = 4;              // waves per workgroup
-constexpr int BK = 64;             // keys per tile
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
+// The transposing LDS read, through a pointer that nothing else writes while it is read (the kernels' barriers and
+// waits see to that). Said without it, the compiler lets every such read wait for all loads to LDS in flight,
+// which exposed the latency of the next tile's load in every tile.
+__device__ __forceinline__ v4s read_tr(const SS_LDS void* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((SS_LDS v4s*)p);
+}
+
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int64_t uni64(int64_t x) {
   return ((int64_t)(uint32_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x);
@@ -113,13 +120,25 @@ template <int DP> struct Lds {
   __device__ static int swv(int row) { return DP >= 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
 };
 
-// ---- many rows: tiles of 4 waves x NQ x 32 rows ---------------------------------------------------------------
-template <int DP, int NQ>
-__global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(AttnArgs a, int slots) {
+// ---- many rows: tiles of 4 waves x 32 rows, two workgroups per CU ----------------------------------------------
+// The work of a wave is pipelined over stages of 32 keys (two to a tile of BK). Stage j, in program order:
+//   A: O += V P of stage j - 1 (its first 16 keys, then the others, whose powers are finished meanwhile), and the
+//      maximum of the scores of stage j; the K fragments of stage j + 1 on their way from LDS;
+//   (where a row's maximum has risen by more than kSlack: l and O rescaled)
+//   B: the scores of stage j + 1, and the first kEarly of each row's 16 powers of stage j; the V fragments of stage j
+//      on their way from LDS.
+// So every run of matrix instructions has vector work of about the same length beside it that does not wait for
+// it, and fragments are read a block ahead of their use.
+constexpr int NW = 4, BM = NW * 32;  // waves, rows
+constexpr int BK = 64;               // keys per tile
+constexpr int kEarly = 10;
+
+template <int DP>
+__global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slots) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;  // chunks a row, 16-value steps, 32-value blocks
-  constexpr int BM = NW * NQ * 32;
-  constexpr int KB = BK * DP * 2, TILE = 2 * KB;           // bytes of a K tile; of K and V
-  constexpr int LPW = KB / 1024 / NW;                      // 1 KB loads per wave and operand
+  constexpr int KB = BK * DP * 2;                          // bytes of a K or V tile
+  constexpr int LPW = KB / 1024 / NW, RPI = BK / LPW;      // 1 KB loads per wave and operand; rows between them
+  constexpr int VRING = 2 * KB;                            // two slots for K tiles, two for V tiles
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
   const int l32 = lane & 31, h = lane >> 5;
@@ -136,187 +155,240 @@ __global__ __launch_bounds__(64 * NW, 1) void prompt_kernel(AttnArgs a, int slot
 
   // the keys row r sees: 0 .. lim(r) - 1
   auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
-  const int r0 = tile * BM + wave * NQ * 32;
-  int row_lim[NQ];
-  bool row_ok[NQ];
-  int64_t row_tok[NQ];
-  int row_head[NQ];
-  v8bf qf[NQ][KST];
-#pragma unroll
-  for (int u = 0; u < NQ; ++u) {
-    const int r = min(r0 + u * 32 + l32, nr - 1);
-    row_ok[u] = r0 + u * 32 + l32 < nr;
-    row_lim[u] = lim(r);
-    row_tok[u] = s.q0 + r / a.G;
-    row_head[u] = kvh * a.G + r % a.G;
-    const uint16_t* p = a.q + row_tok[u] * a.sqt + row_head[u] * a.sqh;
+  const int r0 = tile * BM + wave * 32;
+  const int row = min(r0 + l32, nr - 1), row_lim = lim(row);
+  v8bf qf[KST];
+  {
+    const uint16_t* p = a.q + (s.q0 + row / a.G) * a.sqt + (int64_t)(kvh * a.G + row % a.G) * a.sqh;
 #pragma unroll
     for (int i = 0; i < KST; ++i) {
       const int c = 2 * i + h;
       v4u x = {0, 0, 0, 0};
       if (DP == a.D || c * 8 < a.D) x = *reinterpret_cast<const v4u*>(p + c * 8);
-      qf[u][i] = __builtin_bit_cast(v8bf, x);
+      qf[i] = __builtin_bit_cast(v8bf, x);
     }
   }
   const int kend = uni(lim(min(tile * BM + BM, nr) - 1));  // keys of the workgroup
-  const int wmin = uni(r0 < nr ? lim(r0) : 0), wmax = uni(r0 < nr ? lim(min(r0 + NQ * 32, nr) - 1) : 0);
+  const int wmin = uni(r0 < nr ? lim(r0) : 0), wmax = uni(r0 < nr ? lim(min(r0 + 32, nr) - 1) : 0);
   const int nt = (kend + BK - 1) / BK;
+  const int nw = (wmax + BK - 1) / BK, nfull = wmin / BK;  // this wave's tiles; those every row sees whole
 
-  // DMA of a tile: instruction q of this wave fills bytes 1024 (wave LPW + q) + 16 lane. The buffer resource
-  // starts at the tile and ends behind the sequence's last key: what is read past it is zero, so keys behind a
-  // sequence, whatever they hold, meet the product as zeros. The resource moves with the tile in 64 bits;
-  // lane offsets stay within one tile.
-  uint32_t ofk[4], ofv[4];  // LPW of them
-  static_assert(LPW <= 4, "loads per wave");
-#pragma unroll
-  for (int i = 0; i < LPW; ++i) {
-    const int x = (wave * LPW + i) * 64 + lane, row = x / CH, ck = (x % CH) ^ Lds<DP>::swk(row),
-              cv = (x % CH) ^ Lds<DP>::swv(row);
-    ofk[i] = ck * 8 < a.D ? (uint32_t)row * (uint32_t)a.skt * 2u + ck * 16 : 0xFFFFFF00u;
-    ofv[i] = cv * 8 < a.D ? (uint32_t)row * (uint32_t)a.svt * 2u + cv * 16 : 0xFFFFFF00u;
+  // DMA of a tile: load i of a wave brings rows RPI i + .. to byte 1024 (NW i + wave) + 16 lane of its slot; the rows
+  // of a lane differ by RPI, a multiple of 16, so they share one place in the swizzle and one lane offset. The
+  // buffer resource starts at the load's first row and ends behind the sequence's last key: what is read past it is
+  // zero, so keys behind a sequence, whatever they hold, meet the product as zeros (rows wholly behind it: no
+  // memory access). Resources move in 64 bits; lane offsets stay within a few rows.
+  uint32_t ofk, ofv;
+  {
+    const int r = wave * (64 / CH) + lane / CH, ck = (lane % CH) ^ Lds<DP>::swk(r), cv = (lane % CH) ^ Lds<DP>::swv(r);
+    static_assert(RPI % 16 == 0 && RPI == NW * (64 / CH), "rows of a lane share the swizzle");
+    ofk = ck * 8 < a.D ? (uint32_t)r * (uint32_t)a.skt * 2u + ck * 16 : 0x80000000u;  // past every resource, also with the
+    ofv = cv * 8 < a.D ? (uint32_t)r * (uint32_t)a.svt * 2u + cv * 16 : 0x80000000u;  // rows (below 2^31 bytes) added
   }
   const uint16_t* kp = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
   const uint16_t* vp = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
-  auto issue = [&](int t, int slot_bytes) {
-    const int rows = min(s.lk - t * BK, BK);  // >= 1
-    const uint32_t nk = (uint32_t)(rows - 1) * (uint32_t)a.skt * 2u + a.D * 2,
-                   nv = (uint32_t)(rows - 1) * (uint32_t)a.svt * 2u + a.D * 2;
-    const __amdgpu_buffer_rsrc_t rk = rsrc(kp + (int64_t)t * BK * a.skt, nk), rv = rsrc(vp + (int64_t)t * BK * a.svt, nv);
-    SS_LDS uint8_t* dst = (SS_LDS uint8_t*)smem + slot_bytes + wave * LPW * 1024;
+  // the tiles that are being brought in: where they start, and the keys from there to the sequence's end
+  const uint8_t *kb = reinterpret_cast<const uint8_t*>(kp), *vb = reinterpret_cast<const uint8_t*>(vp);
+  int kleft = s.lk, vleft = s.lk;
+  const uint32_t kr2 = (uint32_t)a.skt * 2u, vr2 = (uint32_t)a.svt * 2u;  // bytes from row to row
+  auto load_k = [&](int i, uint32_t to) __attribute__((always_inline)) {
+    const int last = min(max(kleft, 0), BK) - 1;  // -1: nothing is left, a resource of no bytes
+    const uint32_t n = ((uint32_t)last * kr2 + a.D * 2) & ~(uint32_t)(last >> 31);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(kb, n), (SS_LDS void*)((SS_LDS uint8_t*)smem + to + (NW * i + wave) * 1024), 16,
+                                             ofk + (uint32_t)(i * RPI) * kr2, 0, 0, 0);
+  };
+  auto load_v = [&](int i, uint32_t to) __attribute__((always_inline)) {
+    const int last = min(max(vleft, 0), BK) - 1;  // -1: nothing is left, a resource of no bytes
+    const uint32_t n = ((uint32_t)last * vr2 + a.D * 2) & ~(uint32_t)(last >> 31);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(vb, n), (SS_LDS void*)((SS_LDS uint8_t*)smem + to + (NW * i + wave) * 1024), 16,
+                                             ofv + (uint32_t)(i * RPI) * vr2, 0, 0, 0);
+  };
+  auto next_k = [&]() __attribute__((always_inline)) { kb += (int64_t)BK * kr2, kleft -= BK; };
+  auto next_v = [&]() __attribute__((always_inline)) { vb += (int64_t)BK * vr2, vleft -= BK; };
+
+  // this lane's places in a tile: K row l32 (chunk 2 i + h), V row 4 h + (lane % 16) / 4 of a 16-key step; the XOR
+  // of the swizzle leaves KST addresses for K and DB for V, the rest are constant offsets
+  const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
+  uint32_t ka[KST], va[DB];
 #pragma unroll
-    for (int i = 0; i < LPW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (SS_LDS void*)(dst + i * 1024), 16, ofk[i], 0, 0, 0);
+  for (int i = 0; i < KST; ++i) ka[i] = l32 * DP * 2 + ((2 * i + h) ^ Lds<DP>::swk(l32)) * 16;
 #pragma unroll
-    for (int i = 0; i < LPW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (SS_LDS void*)(dst + KB + i * 1024), 16, ofv[i], 0, 0, 0);
+  for (int d = 0; d < DB; ++d) va[d] = vrow * DP * 2 + ((d * 4 + vcol) ^ Lds<DP>::swv(vrow)) * 16 + vsub;
+
+  v16f O[DB], S0, S1;
+  v8bf kf[KST], vf[2][DB], P[2];
+  float m = kLow, l = 0.0f;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) {
+    O[d] = v16f{};
+    vf[0][d] = vf[1][d] = __builtin_bit_cast(v8bf, v4u{0, 0, 0, 0});
+  }
+  P[0] = P[1] = __builtin_bit_cast(v8bf, v4u{0, 0, 0, 0});
+
+  auto read_k = [&](int i, uint32_t at) __attribute__((always_inline)) {
+    kf[i] = *reinterpret_cast<const SS_LDS v8bf*>((const SS_LDS uint8_t*)smem + at + ka[i]);
+  };
+  auto read_v = [&](int kk, int d, uint32_t at) __attribute__((always_inline)) {  // 16 keys
+    const SS_LDS uint8_t* p = (const SS_LDS uint8_t*)smem + at + va[d] + kk * 16 * DP * 2;
+    const v4s x = read_tr(p), y = read_tr(p + 8 * DP * 2);
+    vf[kk][d] = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  // one stage: `cur` holds its scores, `nxt` receives those of the next; kn: LDS offset of the keys of the stage after
+  // the next, vc: of this stage's values; `side`: work beside it (loads)
+  auto stage = [&](v16f& cur, v16f& nxt, uint32_t kn, uint32_t vc, int first, auto side, auto maskc) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(maskc)::value) {
+      const int left = row_lim - first - 4 * h;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * (i / 4) + i % 4 >= left) cur[i] = -INFINITY;
+    }
+    float mt = cur[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, cur[i]);
+    mt = pair_max(mt) * a.c;
+    if (__any(mt > m + kSlack)) {
+      const float mn = fmaxf(m, ceilf(mt)), f = __builtin_amdgcn_exp2f(m - mn);  // a power of two: exact
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[d][i] *= f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        v4u w = __builtin_bit_cast(v4u, P[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+        P[k] = __builtin_bit_cast(v8bf, w);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    side();
+    nxt = v16f{};
+    v4u pk[2];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // a step of the scores' chain, a step of the values, two powers; then the fragments just used are read anew
+#pragma unroll
+      for (int j = i * KST / 8; j < (i + 1) * KST / 8; ++j) {
+        nxt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[j], qf[j], nxt, 0, 0, 0);
+        read_k(j, kn);
+      }
+#pragma unroll
+      for (int j = i * 2 * DB / 8; j < (i + 1) * 2 * DB / 8; ++j) {
+        O[j % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[j / DB][j % DB], P[j / DB], O[j % DB], 0, 0, 0);
+        read_v(j / DB, j % DB, vc);
+      }
+      const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i], a.c, -m));
+      const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i + 1], a.c, -m));
+      sum += x + y;
+      pk[i / 4][i % 4] = pack_bf16x2(x, y);
+    }
+    l += sum;
+    P[0] = __builtin_bit_cast(v8bf, pk[0]);
+    P[1] = __builtin_bit_cast(v8bf, pk[1]);
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  v16f O[NQ][DB];
-  float m[NQ], l[NQ];
+  // Iteration t reads K tile t + 1 and V tile t and brings in K tile t + 2 and V tile t + 1, into the slots of K tile t
+  // and V tile t - 1, which were read in iteration t - 1: one wait and one barrier a tile.
+  uint32_t k0 = 0, k1 = KB, v0 = VRING, v1 = VRING + KB;  // slots of tiles t, t + 1
+  if (nt > 0) {
 #pragma unroll
-  for (int u = 0; u < NQ; ++u) {
-    m[u] = kLow;
-    l[u] = 0.0f;
+    for (int i = 0; i < LPW; ++i) load_k(i, k0);
+    next_k();
 #pragma unroll
-    for (int d = 0; d < DB; ++d) O[u][d] = v16f{};
-  }
-  // this lane's places in a tile: K row l32 (chunk 2 i + h), V row 4 h + (lane % 16) / 4 of a 16-key step
-  const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
-
-  if (nt > 0) issue(0, 0);
-  for (int t = 0; t < nt; ++t) {
-    __builtin_amdgcn_s_waitcnt(0);  // this wave's loads of tile t, and its LDS reads of tile t - 1
+    for (int i = 0; i < LPW; ++i) load_k(i, k1);
+    next_k();
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) load_v(i, v0);
+    next_v();
+    __builtin_amdgcn_s_waitcnt(vm(2 * LPW));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const int cur = (t & 1) * TILE;
-    if (t + 1 < nt) issue(t + 1, TILE - cur);
-    if (t * BK >= wmax) continue;  // no row of this wave sees this tile
-    const SS_LDS uint8_t* kt = (const SS_LDS uint8_t*)smem + cur;
-    const SS_LDS uint8_t* vt = kt + KB;
-    v16f S[NQ][2];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int i = 0; i < KST; ++i) read_k(i, 0);
+    S0 = v16f{};
 #pragma unroll
-      for (int u = 0; u < NQ; ++u) S[u][kb] = v16f{};
+    for (int i = 0; i < KST; ++i) S0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], qf[i], S0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < KST; ++i) {
-        const int row = kb * 32 + l32;
-        const v8bf kf = *reinterpret_cast<const SS_LDS v8bf*>(kt + row * DP * 2 + ((2 * i + h) ^ Lds<DP>::swk(row)) * 16);
-#pragma unroll
-        for (int u = 0; u < NQ; ++u) S[u][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[u][i], S[u][kb], 0, 0, 0);
-      }
-    }
-    if (t * BK + BK > wmin) {  // some row of this wave does not see the whole tile
-#pragma unroll
-      for (int u = 0; u < NQ; ++u) {
-        const int left = row_lim[u] - t * BK - 4 * h;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (kb * 32 + 8 * (i / 4) + i % 4 >= left) S[u][kb][i] = -INFINITY;
-      }
-    }
-    v8bf P[NQ][4];
-#pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-      float mt = S[u][0][0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) mt = fmaxf(mt, S[u][i / 16][i % 16]);
-      mt = pair_max(mt) * a.c;
-      if (__any(mt > m[u] + kSlack)) {
-        const float mn = fmaxf(m[u], mt), f = __builtin_amdgcn_exp2f(m[u] - mn);
-        m[u] = mn;
-        l[u] *= f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) O[u][d][i] *= f;
-      }
-      float sum = 0.0f;
-      v4u pk[4];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[u][i / 16][i % 16], a.c, -m[u]));
-        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(S[u][i / 16][i % 16 + 1], a.c, -m[u]));
-        sum += x + y;
-        pk[i / 8][(i % 8) / 2] = pack_bf16x2(x, y);
-      }
-      l[u] += sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) P[u][i] = __builtin_bit_cast(v8bf, pk[i]);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {  // 16 keys each
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        v8bf vf;
-        {
-          const int ra = kk * 16 + vrow, rb = ra + 8, c = d * 4 + vcol;
-          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (SS_LDS v4s*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
-          const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (SS_LDS v4s*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
-          vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
-#pragma unroll
-        for (int u = 0; u < NQ; ++u) O[u][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, P[u][kk], O[u][d], 0, 0, 0);
-      }
-    }
+    for (int i = 0; i < KST; ++i) read_k(i, KB / 2);
   }
+  auto turn = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x7 << 4);  // vmcnt(0), lgkmcnt(0): this wave's loads and LDS reads
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto rotate = [&]() __attribute__((always_inline)) {
+    next_k();
+    next_v();
+    const uint32_t x = k0, y = v0;
+    k0 = k1, k1 = x;
+    v0 = v1, v1 = y;
+  };
+  auto tile_of = [&](int t, auto maskc) __attribute__((always_inline)) {
+    turn();
+    stage(S0, S1, k1, v0, t * BK, [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) load_v(i, v1);
+    }, maskc);
+    stage(S1, S0, k1 + KB / 2, v0 + KB / 2, t * BK + 32, [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) load_k(i, k0);
+    }, maskc);
+    rotate();
+  };
+  int t = 0;
+  for (; t < nfull; ++t) tile_of(t, std::false_type{});
+  for (; t < nw; ++t) tile_of(t, std::true_type{});
+#pragma unroll
+  for (int j = 0; j < 2 * DB; ++j)  // the last stage's values
+    O[j % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[j / DB][j % DB], P[j / DB], O[j % DB], 0, 0, 0);
+  for (; t < nt; ++t) {  // the other waves' tiles
+    turn();
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) load_v(i, v1);
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) load_k(i, k0);
+    rotate();
+  }
+  __builtin_amdgcn_s_waitcnt(vm(0));  // no load may outlive the workgroup
 
+  const float lt = pair_sum(l);
+  const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;  // a row that sees no key: zeros
+  const bool ok = r0 + l32 < nr;
+  const int64_t tok = s.q0 + row / a.G;
+  const int head = kvh * a.G + row % a.G;
+  if (a.lse && ok && h == 0)
+    a.lse[head * a.Tq + tok] = lt > 0.0f ? (m + __builtin_amdgcn_logf(lt)) * 0.69314718056f : -INFINITY;
+  uint16_t* op = a.o + tok * a.sot + head * a.soh;
 #pragma unroll
-  for (int u = 0; u < NQ; ++u) {
-    const float lt = pair_sum(l[u]);
-    const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;  // a row that sees no key: zeros
-    if (a.lse && row_ok[u] && h == 0)
-      a.lse[row_head[u] * a.Tq + row_tok[u]] = lt > 0.0f ? (m[u] + __builtin_amdgcn_logf(lt)) * 0.69314718056f : -INFINITY;
-    uint16_t* op = a.o + row_tok[u] * a.sot + row_head[u] * a.soh;
+  for (int d = 0; d < DB; ++d) {
 #pragma unroll
-    for (int d = 0; d < DB; ++d) {
+    for (int g = 0; g < 4; g += 2) {
+      // lane l holds values 8g + 4h .. +3 and 8(g+1) + 4h .. +3 of its row; exchanged with lane l ^ 32, the lower
+      // lane has 8g .. 8g+7 and the upper 8(g+1) .. 8(g+1)+7
+      uint32_t x[2], y[2];
 #pragma unroll
-      for (int g = 0; g < 4; g += 2) {
-        // lane l holds values 8g + 4h .. +3 and 8(g+1) + 4h .. +3 of its row; exchanged with lane l ^ 32, the
-        // lower lane has 8g .. 8g+7 and the upper 8(g+1) .. 8(g+1)+7
-        uint32_t x[2], y[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          x[e] = pack_bf16x2(O[u][d][4 * g + 2 * e] * inv, O[u][d][4 * g + 2 * e + 1] * inv);
-          y[e] = pack_bf16x2(O[u][d][4 * g + 4 + 2 * e] * inv, O[u][d][4 * g + 5 + 2 * e] * inv);
-        }
-        const auto r0_ = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
-        const auto r1_ = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
-        const int col = d * 32 + 8 * (g + h);
-        if (row_ok[u] && (DP == a.D || col < a.D))
-          *reinterpret_cast<v4u*>(op + col) = v4u{r0_[0], r1_[0], r0_[1], r1_[1]};
+      for (int e = 0; e < 2; ++e) {
+        x[e] = pack_bf16x2(O[d][4 * g + 2 * e] * inv, O[d][4 * g + 2 * e + 1] * inv);
+        y[e] = pack_bf16x2(O[d][4 * g + 4 + 2 * e] * inv, O[d][4 * g + 5 + 2 * e] * inv);
       }
+      const auto e0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+      const auto e1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+      const int col = d * 32 + 8 * (g + h);
+      if (ok && (DP == a.D || col < a.D)) *reinterpret_cast<v4u*>(op + col) = v4u{e0[0], e1[0], e0[1], e1[1]};
     }
   }
 }
 
-template <int DP, int NQ> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
-  auto kern = prompt_kernel<DP, NQ>;
-  constexpr int lds = 2 * 2 * BK * DP * 2, BM = NW * NQ * 32;
+template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
+  auto kern = prompt_kernel<DP>;
+  constexpr int lds = 4 * BK * DP * 2;
   const hipError_t e = lds_limit((const void*)kern, lds);
   if (e != hipSuccess) return e;
   const int64_t slots = a.Tq * a.G / BM + a.B;
@@ -456,10 +528,8 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         const int ra = kk * 16 + vrow, rb = ra + 8, c = d * 4 + vcol;
-        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (SS_LDS v4s*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
-        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (SS_LDS v4s*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
+        const v4s x = read_tr((const SS_LDS uint8_t*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
+        const v4s y = read_tr((const SS_LDS uint8_t*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
         const v8bf vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
         O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, P[kk], O[d], 0, 0, 0);
       }
@@ -600,7 +670,7 @@ int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int6
 
 hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {
   if (a.Tk > 0 && attn::few_rows(a.Tq, a.B, a.G)) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
-  return a.D <= 64 ? attn::launch_prompt<64, 2>(a, st) : attn::launch_prompt<128, 2>(a, st);
+  return a.D <= 64 ? attn::launch_prompt<64>(a, st) : attn::launch_prompt<128>(a, st);
 }
 
 }  // namespace ss

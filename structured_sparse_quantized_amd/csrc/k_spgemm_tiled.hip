@@ -430,13 +430,67 @@ __device__ __forceinline__ void spgemm_body(int R, int C, int KS, const uint8_t*
   }
 #pragma unroll
   for (int u = 0; u < TJ; ++u) s_b[u] = has_b ? scl[BM + (wn * TJ + u) * 16 + r16] : 1.0f;
-  float res[TI][TJ][4];  // the general epilogue's residuals, all on their way before the first store
   if constexpr (YT == 3) {
+    // The general epilogue: the scaled sums go through the idle ring as float32 rows of tokens, half of a wave's 64
+    // tokens at a time, and leave 8 columns per lane and step in one small loop. (Taken tile by tile from the
+    // registers, the code of 16 tiles passed through the instruction cache once, which cost 3-10 us a call.)
+    constexpr int LD = 64 + 4, RP = 32;  // floats of a staged row; rows a pass
+    static_assert(TI == 4 && TJ == 4 && NW * RP * LD * 4 <= ::ss::tiled::LDS, "staging fits the stage ring");
+    float* stg = reinterpret_cast<float*>(smem) + wave * RP * LD;
+    const int tok0 = SIDE_X ? r0 + wm * 64 : c0 + wn * 64, ntok = SIDE_X ? R : C;
+    const int ch0 = SIDE_X ? c0 + wn * 64 : r0 + wm * 64, nch = SIDE_X ? C : R;
+    const int cpr = 8 >> ep.gated, rps = 64 / cpr, steps = RP / rps, row0 = lane / cpr;
+    const bool pieces = aligned_rows(ep, ldy);
+    const Leave out(ep, Y, ldy, lane % cpr, ch0, nch);
+    auto fetch = [&](Leave::Res* r, int p, int k) {
 #pragma unroll
-    for (int t = 0; t < TI; ++t)
+      for (int x = 0; x < 2; ++x) out.residual(r[x], min(tok0 + p * RP + row0 + (k + x) * rps, ntok - 1));
+    };
+    Leave::Res cur[2];
+    if (pieces) fetch(cur, 0, 0);
+    __syncthreads();  // every wave is done with the ring
 #pragma unroll
-      for (int u = 0; u < TJ; ++u)
-        load_residual<SIDE_X>(res[t][u], r0 + (wm * TI + t) * 16 + 4 * jj, min(c0 + (wn * TJ + u) * 16 + r16, C - 1), R, ep);
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int t = SIDE_X ? p * 2 + h : x, u = SIDE_X ? x : p * 2 + h;
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float s1 = SIDE_X ? s_a[t][q] : s_b[u], s2 = SIDE_X ? s_b[u] : s_a[t][q];
+            y[q] = __fmul_rn(__fmul_rn((float)acc[t][u][q], s1), s2);
+          }
+          if constexpr (SIDE_X) {  // 4 tokens of one channel
+#pragma unroll
+            for (int q = 0; q < 4; ++q) stg[(h * 16 + 4 * jj + q) * LD + x * 16 + r16] = y[q];
+          } else {  // 4 channels of one token
+            *reinterpret_cast<float4*>(stg + (h * 16 + r16) * LD + x * 16 + 4 * jj) = make_float4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      __builtin_amdgcn_wave_barrier();
+      if (!pieces) {
+        if (tok0 + p * RP < ntok) leave_columns<64>(stg, LD, RP, tok0 + p * RP, ntok, ch0, nch, Y, ldy, ep);
+        __builtin_amdgcn_wave_barrier();
+        continue;
+      }
+#pragma unroll 1
+      for (int k = 0; k < steps; k += 2) {  // two rows a step; the next two rows' residuals are on their way
+        Leave::Res nxt[2];
+        if (k + 2 < steps) fetch(nxt, p, k + 2);
+        else if (p == 0) fetch(nxt, 1, 0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = row0 + (k + x) * rps, tok = tok0 + p * RP + row;
+          if (tok < ntok) out.row(stg + row * LD, cur[x], tok);
+        }
+        cur[0] = nxt[0];
+        cur[1] = nxt[1];
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    return;
   }
 #pragma unroll
   for (int t = 0; t < TI; ++t) {
@@ -459,8 +513,7 @@ __device__ __forceinline__ void spgemm_body(int R, int C, int KS, const uint8_t*
           y[q] = __fmul_rn(__fmul_rn((float)acc[t][u][q], s1), s2);
         }
       }
-      if constexpr (YT == 3) store_epilogue<SIDE_X>(Y, ldy, ar, bc, R, y, res[t][u], ep);
-      else store_out<YT, SIDE_X>(Y, ldy, ar, bc, R, y, yi);
+      store_out<YT, SIDE_X>(Y, ldy, ar, bc, R, y, yi);
     }
   }
 }
@@ -608,7 +661,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
           y[q] = f;
         }
       }
-      if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, res, ep);
+      if constexpr (YT == 3) finish_and_store(Y, ldy, ar, bc, R, y, res, ep);
       else store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
     }
   }
@@ -1044,7 +1097,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(int R, int C, int RP
       y[q] = f;
     }
   }
-  if constexpr (YT == 3) store_epilogue<false>(Y, ldy, ar, bc, R, y, res, ep);
+  if constexpr (YT == 3) finish_and_store(Y, ldy, ar, bc, R, y, res, ep);
   else store_out<YT, false>(Y, ldy, ar, bc, R, y, yi);
 }
 

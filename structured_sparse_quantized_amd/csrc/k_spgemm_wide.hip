@@ -421,7 +421,7 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
       if constexpr (!SX) {
         const int ar0 = r0 + wm * TI * 16;
         const bool inside = ar0 + 128 <= R;
-        if (!ep.f32 && (!ep.res || (!ep.gated && inside && (ep.ldr & 3) == 0))) {
+        if (!ep.f32 && (ldy & 7) == 0 && (!ep.res || (!ep.gated && inside && (ep.ldr & 3) == 0))) {
           // The general epilogue to bf16, weight-sparse side: bias, activation, gate and residual in the accumulators'
           // own lanes (4 channels of one token each; column by column of the tile, so that the activations stay
           // short unrolled runs), then rows of bf16 through the idle ring as below. The residuals of a column are
@@ -431,7 +431,6 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
           static_assert(NW * RP * STRIDE <= META, "staging fits the stage ring");
           SS_LDS uint8_t* stg = (SS_LDS uint8_t*)smem + wave * RP * STRIDE;
           const int col0 = ar0 >> ep.gated, ncol = R >> ep.gated, wide = 128 >> ep.gated;
-          const bool yvec = inside && (ldy & 7) == 0;
           // The channels' scales and biases are read from LDS for every column (64-lane reads of 4 addresses):
           // kept in registers beside the accumulators they would spill. A wave keeps its 128 biases behind the scales.
           const int wb = 512 + wave * 128;
@@ -504,7 +503,7 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
             __builtin_amdgcn_wave_barrier();
             const int bc0 = c0 + (wn * TJ + p * UP) * 16, cpr = wide / 8, sh = ep.gated ? 3 : 4;
             uint16_t* Yh = static_cast<uint16_t*>(Y);
-            if (yvec && bc0 + RP <= C) {
+            if (inside && bc0 + RP <= C) {
               constexpr int IT = RP * 16 / 64;
               v4i v[IT];
   #pragma unroll
@@ -527,7 +526,7 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
                 if (bc0 + row >= C) continue;
                 const v4i v = *reinterpret_cast<const SS_LDS v4i*>(stg + row * STRIDE + (i & (cpr - 1)) * 16);
                 uint16_t* dst = Yh + (int64_t)(bc0 + row) * ldy + col;
-                if ((ldy & 7) == 0 && col + 8 <= ncol) {
+                if (col + 8 <= ncol) {
                   __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dst));
                 } else {
                   const uint32_t w[4] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
@@ -560,6 +559,7 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
       // A lane keeps its 8-column piece of a row (and that piece's bias) and takes every rps-th row of a pass.
       const int cpr = (SX ? 2 * TJ : 16) >> ep.gated, rps = 64 / cpr, steps = RP / rps, row0 = lane / cpr;
       static_assert(RP >= 2 * 64 / (SX ? TJ : 8), "a pass has two steps or more, an even number");
+      const bool pieces = aligned_rows(ep, ldy);
       const Leave out(ep, Y, ldy, lane % cpr, ch0, nch);
       auto fetch = [&](Leave::Res* r, int p, int k) {
   #pragma unroll
@@ -567,9 +567,9 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
           out.residual(r[x], min(tok0 + p * RP + row0 + (k + x) * rps, ntok - 1));
       };
       Leave::Res cur[2];
-      fetch(cur, 0, 0);
-  #pragma unroll
-      for (int p = 0; p < NP; ++p) {
+      if (pieces) fetch(cur, 0, 0);
+      auto one = [&](auto pc) __attribute__((always_inline)) {
+        constexpr int p = decltype(pc)::value;
         // the scales again from LDS (their slot stays): kept in registers through the passes they would spill
         uint32_t so = 0;
         asm volatile("" : "+v"(so));
@@ -600,6 +600,12 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
           }
         }
         __builtin_amdgcn_wave_barrier();
+        if (!pieces) {
+          if (tok0 + p * RP < ntok)
+            leave_columns<LD - 4>((const float*)stg, LD, RP, tok0 + p * RP, ntok, ch0, nch, Y, ldy, ep);
+          __builtin_amdgcn_wave_barrier();
+          return;
+        }
   #pragma unroll 1
         for (int k = 0; k < steps; k += 2) {  // two rows a step; the next two rows' residuals are on their way
           Leave::Res nxt[2];
@@ -614,7 +620,8 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
           cur[1] = nxt[1];
         }
         __builtin_amdgcn_wave_barrier();
-      }
+      };
+      each_column<1>(std::make_integer_sequence<int, NP>{}, one, [](int) {});  // (unrolled by hand, as above)
       return;
     }
     constexpr int EB = YT == 0 ? 2 : 4;  // output element bytes

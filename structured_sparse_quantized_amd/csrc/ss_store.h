@@ -83,34 +83,9 @@ __device__ __forceinline__ void store_one(void* Y, int64_t at, float v, bool f32
   if (f32) static_cast<float*>(Y)[at] = v;
   else static_cast<uint16_t*>(Y)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
 }
-// a column's bias and activation for a lane's 4 scaled results (columns ar..ar+3 of side W, column bc of side X),
-// in place; gated: the results move to y[0], y[1] (side W) or stay in the even lanes (side X)
-template <bool SIDE_X>
-__device__ __forceinline__ void finish(float* y, int64_t ar, int64_t bc, int64_t R, const Epilogue& e) {
-  if (e.bias) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) y[q] = y[q] + e.bias[SIDE_X ? bc : min(ar + q, R - 1)];
-  }
-  if constexpr (SIDE_X) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float up = e.gated ? __shfl_xor(y[q], 1, 64) : 1.0f;
-      activate_n<1>(y + q, e.act, e.f32);
-      if (e.gated) y[q] *= up;
-    }
-  } else if (e.gated) {
-    float g[2] = {y[0], y[2]};
-    activate_n<2>(g, e.act, e.f32);
-    y[0] = g[0] * y[1];
-    y[1] = g[1] * y[3];
-  } else {
-    activate_n<4>(y, e.act, e.f32);
-  }
-}
-
-// store_out with the general epilogue, in two steps: the residuals of a lane's 4 results (the loads of several
-// tiles are issued before the first store: the residual may be Y, so none could move over one), then the rest.
-// All lanes of a wave whose bc is below the count of B rows call them together.
+// store_out with the general epilogue, in steps: the residuals of a lane's 4 results (the loads of several tiles
+// are issued before the first store: the residual may be Y, so none could move over one); and, of finished results
+// (gated: y[0], y[1] on side W, the even lanes' on side X), the sum with the residual and the store.
 template <bool SIDE_X>
 __device__ __forceinline__ void load_residual(float* r, int64_t ar, int64_t bc, int64_t R, const Epilogue& e) {
   if (!e.res) return;
@@ -137,7 +112,6 @@ __device__ __forceinline__ void load_residual(float* r, int64_t ar, int64_t bc, 
 template <bool SIDE_X>
 __device__ __forceinline__ void store_epilogue(void* Y, int64_t ldy, int64_t ar, int64_t bc, int64_t R, float* y,
                                                const float* r, const Epilogue& e) {
-  finish<SIDE_X>(y, ar, bc, R, e);
   if (e.res) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -167,6 +141,30 @@ __device__ __forceinline__ void store_epilogue(void* Y, int64_t ldy, int64_t ar,
   }
 }
 
+// The few-token kernels' epilogue: one lane, 4 channels ar..ar+3 of token bc, scaled.
+__device__ __forceinline__ void finish_and_store(void* Y, int64_t ldy, int64_t ar, int64_t bc, int64_t R, float* y,
+                                                 const float* r, const Epilogue& e) {
+  if (e.bias) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] += e.bias[min(ar + q, R - 1)];
+  }
+  if (e.gated) {
+    float g[2] = {y[0], y[2]};
+    activate_n<2>(g, e.act, e.f32);
+    y[0] = g[0] * y[1];
+    y[1] = g[1] * y[3];
+  } else {
+    activate_n<4>(y, e.act, e.f32);
+  }
+  store_epilogue<false>(Y, ldy, ar, bc, R, y, r, e);
+}
+
+// Whether rows of Y and of the residual start on 16 bytes (their pointers do).
+__device__ __forceinline__ bool aligned_rows(const Epilogue& e, int64_t ldy) {
+  const int per16 = e.f32 ? 3 : 7;  // elements of 16 bytes, less one
+  return (ldy & per16) == 0 && (!e.res || (e.ldr & per16) == 0);
+}
+
 // Eight columns of one row of Y from a staged row of scaled sums (channels ch0, ch0 + 1, ..; nch of them in all):
 // piece i holds 8 channels, or with a gate the 16 channels of 8 pairs.
 struct Leave {
@@ -179,7 +177,7 @@ struct Leave {
   void* Y;
   int64_t ldy;
   int piece, first, nch, col, ncol;
-  bool vec;        // whole 16-byte pieces of Y and of the residual
+  bool vec;        // this lane's piece is whole
   float bias[16];  // of this lane's piece
 
   __device__ __forceinline__ Leave(const Epilogue& ep, void* y, int64_t ld, int pc, int ch0, int nc)
@@ -187,8 +185,7 @@ struct Leave {
     first = ch0 + (piece << (3 + e.gated));
     col = (ch0 >> e.gated) + piece * 8;
     ncol = nch >> e.gated;
-    const int per16 = e.f32 ? 3 : 7;  // elements of 16 bytes, less one
-    vec = col + 8 <= ncol && (ldy & per16) == 0 && (!e.res || (e.ldr & per16) == 0);
+    vec = col + 8 <= ncol;
 #pragma unroll
     for (int i = 0; i < 16; ++i) bias[i] = e.bias && (i < 8 || e.gated) ? e.bias[min(first + i, nch - 1)] : 0.0f;
   }
@@ -247,18 +244,54 @@ struct Leave {
     } else {
       int c = col;
       asm volatile("" : "+v"(c));  // addresses made here, not kept for the whole tile
-      float x[8];
-      if (e.res) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = load_res(e, tok * e.ldr + min(c + i, ncol - 1));
-      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (c + i >= ncol) break;
-        store_one(Y, tok * ldy + c + i, e.res ? g[i] + x[i] : g[i], e.f32);
+        store_one(Y, tok * ldy + c + i, e.res ? g[i] + load_res(e, tok * e.ldr + c + i) : g[i], e.f32);
       }
     }
   }
 };
+
+// The same for rows that do not start on 16 bytes: a lane per column, so that a wave's loads and stores are runs of
+// adjacent elements; 4 rows at a time, their residuals fetched before the first store. COLS staged channels a row.
+template <int COLS>
+__device__ __forceinline__ void leave_columns(const float* stg, int ld, int rows, int64_t tok0, int64_t ntok, int ch0, int nch,
+                                              void* Y, int64_t ldy, const Epilogue& e) {
+  const int lane = threadIdx.x & 63, wide = COLS >> e.gated, col0 = ch0 >> e.gated, ncol = nch >> e.gated;
+  const int have = (int)min((int64_t)rows, ntok - tok0);  // rows of Y
+#pragma unroll 1
+  for (int c = lane; c < wide; c += 64) {
+    if (col0 + c >= ncol) break;
+    const int at = c << e.gated;
+    const float b0 = e.bias ? e.bias[ch0 + at] : 0.0f, b1 = e.bias && e.gated ? e.bias[ch0 + at + 1] : 0.0f;
+#pragma unroll 1
+    for (int r = 0; r < have; r += 4) {
+      float res[4], z[4], up[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = min(r + x, have - 1);
+        res[x] = e.res ? load_res(e, (tok0 + row) * e.ldr + col0 + c) : 0.0f;
+        z[x] = stg[row * ld + at];
+        up[x] = e.gated ? stg[row * ld + at + 1] : 1.0f;
+      }
+      if (e.bias) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          z[x] += b0;
+          if (e.gated) up[x] += b1;
+        }
+      }
+      activate_n<4>(z, e.act, e.f32);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (r + x >= have) break;
+        float v = e.gated ? z[x] * up[x] : z[x];
+        if (e.res) v += res[x];
+        store_one(Y, (tok0 + r + x) * ldy + col0 + c, v, e.f32);
+      }
+    }
+  }
+}
 
 }  // namespace ss
