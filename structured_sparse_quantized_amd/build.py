@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libss.so")
 BIND = os.path.join(PKG, "_ssbind.so")
 SOURCES = ["ss_api.hip", "k_quant_lift.hip", "k_prune.hip", "k_slide.hip", "k_spgemm.hip", "k_spgemm_tiled.hip",
-           "k_spgemm_wide.hip", "k_quant_spgemm.hip", "k_rotary.hip", "k_attn.hip"]
+           "k_spgemm_wide.hip", "k_spgemm_small.hip", "k_quant_spgemm.hip", "k_rotary.hip",
+           "k_attn.hip"]
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))

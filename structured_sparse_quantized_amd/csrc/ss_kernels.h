@@ -68,6 +68,11 @@ hipError_t launch_spgemm_wide(int bn, bool side_x, int ab, int yt, int R, int C,
                               const uint8_t* tm, const uint8_t* bd, int ldb, const float* sx, const float* sw, void* Y,
                               int ldy, const Epilogue& ep, hipStream_t st);
 
+// The small-tile kernel of k_spgemm_small.hip (general epilogue): 64 x 32 tj tiles, tj = 1, 2 or 4; arguments as above.
+hipError_t launch_spgemm_small(int tj, bool side_x, int ab, int R, int C, int KS, const uint8_t* tv, const uint8_t* tm,
+                               const uint8_t* bd, int ldb, const float* sx, const float* sw, void* Y, int ldy,
+                               const Epilogue& ep, hipStream_t st);
+
 // A batch of same-shaped tiled products (one launch; blockIdx.y = problem); strides in bytes for the tiled
 // operand and the dense operand, in elements for the scales and Y.
 hipError_t launch_spgemm_tiled_batched(bool side_x, int ab, int yt, int64_t batch, int64_t R, int64_t C, int64_t Kc,

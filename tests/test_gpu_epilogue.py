@@ -140,6 +140,27 @@ def test_prefill(ss, side, q, M, N, K):
     p.check(ss, act="silu")
 
 
+@pytest.mark.parametrize("side,q,M,N,K", [
+    ("W", "i8", 65, 4098, 600), ("W", "fp8", 130, 2047, 256), ("W", "bf16", 200, 1000, 1000),  # widths of 32
+    ("W", "i8", 350, 2050, 256), ("W", "fp8", 250, 4094, 512), ("W", "bf16", 800, 1100, 128),  # 64
+    ("W", "i8", 400, 4097, 256), ("W", "fp8", 385, 3970, 640), ("W", "bf16", 1000, 2044, 256),  # 128
+    ("X", "i8", 500, 1001, 600), ("X", "fp8", 1500, 333, 256), ("X", "bf16", 777, 900, 500),
+    ("X", "i8", 1030, 990, 256), ("X", "fp8", 1100, 1601, 256), ("X", "bf16", 2047, 250, 256),
+    ("W", "i8", 10, 16390, 256), ("W", "fp8", 16, 12290, 256), ("W", "bf16", 64, 16450, 128), ("W", "fp8", 30, 20001, 512)])
+def test_small_tiles(ss, side, q, M, N, K):
+    p = Problem(ss, side, q, M, N, K, seed=N)
+    for act, gated, y in (("none", False, "bf16"), ("silu", True, "bf16"), ("gelu", False, "f32"), ("relu", True, "f32")):
+        if gated and N % 2:
+            continue
+        b, r = _extras(p, gated, y)
+        Y = p.check(ss, bias=b, act=act, gated=gated, residual=r, y=y)
+        assert torch.equal(Y, p.run(ss, bias=b, act=act, gated=gated, residual=r, y_dtype=y))
+    p.check(ss, act="silu")
+    if M > 64:
+        plain = ss.spgemm_tiled(p.side, M, N, p.Kc, p.tv, p.tm, p.dense, p.sx, p.sw, "f32")
+        assert torch.equal(plain, p.run(ss, y_dtype="f32"))
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 300, 256), (40, 600, 512), (300, 300, 256), (2200, 4096, 256)])
 def test_equals_the_plain_product_without_extras(ss, M, N, K):
     for q in ("i8", "fp8"):
