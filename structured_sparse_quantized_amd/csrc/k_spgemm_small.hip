@@ -8,9 +8,11 @@
 // bounds such a problem is the length of the reduction at one tile per CU, so the loads run far ahead: a ring of
 // S stages of one 128-position step each (4 KB of compressed values, their index words, the B rows), every
 // wave bringing the same number of pieces per stage by LDS DMA, so that "the next stage has landed" is a wait for a
-// constant count. The fragments of step j + 1 are read while step j multiplies; one barrier a step, which costs 0.15,
-// 0.18 and 0.24 us at TJ = 1, 2 and 4 (FP8, 4096 rows, 64 to 512 tokens: 9.0 us at 128 tokens and K = 4096, 21.4 us at 14336,
-// where the 256 x 128 tiles take 20.8 and 51.8).
+// constant count. The fragments of step j + 1 are read while step j multiplies, before its loads set out (after them: 5% slower);
+// one barrier a step. A step costs 0.14, 0.18 and 0.24 us at TJ = 1, 2 and 4: at TJ = 1 a CU takes in its 9 KB at 65 B/ns,
+// 17 TB/s over 256 of them, from the L2s. A barrier per two steps measured the same at TJ = 1 and lost at TJ = 2 and 4, whose
+// LDS holds too few stages for it. FP8, 4096 rows, 128 tokens: 8.6 us at K = 4096, 20.2 us at 14336, where the 256 x 128
+// tiles take 20.8 and 51.8.
 #include <type_traits>
 
 #include "ss_device.h"
@@ -110,8 +112,9 @@ __global__ __launch_bounds__(64 * NW, 2) void small_kernel(int R, int C, int KS,
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's own reads
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    issue(j + S - 1);
     read(nxt, j + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(j + S - 1);
 #pragma unroll
     for (int u = 0; u < TJ; ++u)
 #pragma unroll
