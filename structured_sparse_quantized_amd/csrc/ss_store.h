@@ -254,24 +254,33 @@ struct Leave {
 };
 
 // The same for rows that do not start on 16 bytes: a lane per column, so that a wave's loads and stores are runs of
-// adjacent elements; 4 rows at a time, their residuals fetched before the first store. COLS staged channels a row.
+// adjacent elements, and narrow rows side by side over the 64 lanes; 4 rows a lane at a time, their residuals fetched before
+// the first store (a pass costs about a load's latency). COLS staged channels a row, a power of two.
 template <int COLS>
 __device__ __forceinline__ void leave_columns(const float* stg, int ld, int rows, int64_t tok0, int64_t ntok, int ch0, int nch,
                                               void* Y, int64_t ldy, const Epilogue& e) {
   const int lane = threadIdx.x & 63, wide = COLS >> e.gated, col0 = ch0 >> e.gated, ncol = nch >> e.gated;
   const int have = (int)min((int64_t)rows, ntok - tok0);  // rows of Y
+  const int beside = wide < 64 ? 64 / wide : 1, first = lane / wide;  // rows next to each other, and this lane's first
 #pragma unroll 1
-  for (int c = lane; c < wide; c += 64) {
+  for (int c = lane & (min(wide, 64) - 1); c < wide; c += 64) {
     if (col0 + c >= ncol) break;
     const int at = c << e.gated;
     const float b0 = e.bias ? e.bias[ch0 + at] : 0.0f, b1 = e.bias && e.gated ? e.bias[ch0 + at + 1] : 0.0f;
 #pragma unroll 1
-    for (int r = 0; r < have; r += 4) {
-      float res[4], z[4], up[4];
+    for (int r = first; r < have; r += 4 * beside) {
+      float res[4] = {0, 0, 0, 0}, z[4], up[4];
+      auto fetch = [&](auto f32) __attribute__((always_inline)) {  // the type's branch outside, so the four are in flight together
+        Epilogue of = e;
+        of.f32 = decltype(f32)::value;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) res[x] = load_res(of, (tok0 + min(r + x * beside, have - 1)) * e.ldr + col0 + c);
+      };
+      if (e.res && e.f32) fetch(std::true_type{});
+      if (e.res && !e.f32) fetch(std::false_type{});
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int row = min(r + x, have - 1);
-        res[x] = e.res ? load_res(e, (tok0 + row) * e.ldr + col0 + c) : 0.0f;
+        const int row = min(r + x * beside, have - 1);
         z[x] = stg[row * ld + at];
         up[x] = e.gated ? stg[row * ld + at + 1] : 1.0f;
       }
@@ -285,10 +294,11 @@ __device__ __forceinline__ void leave_columns(const float* stg, int ld, int rows
       activate_n<4>(z, e.act, e.f32);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        if (r + x >= have) break;
+        const int row = r + x * beside;
+        if (row >= have) break;
         float v = e.gated ? z[x] * up[x] : z[x];
         if (e.res) v += res[x];
-        store_one(Y, (tok0 + r + x) * ldy + col0 + c, v, e.f32);
+        store_one(Y, (tok0 + row) * ldy + col0 + c, v, e.f32);
       }
     }
   }
