@@ -588,32 +588,46 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
 }
 
 // o = sum_s w_s part_s, w_s = 2^(lg_s - max) / sum of them: one workgroup per (token, head), 16 bytes a thread,
-// the parts dealt over groups of threads and joined in LDS in a fixed order.
+// the parts dealt over groups of threads and joined in LDS in a fixed order. A launch this small is a chain of load
+// latencies, so the first kPre parts of a thread set out together with the logarithms their weights need.
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __restrict__ part, int splits) {
+  constexpr int kPre = 4;
   __shared__ float4 acc[256];
   const int Hq = a.Hkv * a.G;
   const int64_t row = blockIdx.x, tok = row / Hq, n = a.Tq * Hq;
   const int head = (int)(row - tok * Hq);
-  // rows of no sequence have no parts
-  if (tok < bound(a.cu_q, 0, a.Tq) || tok >= bound(a.cu_q, a.B, a.Tq)) return;
   const float* lg = part + (int64_t)splits * n * a.D + row;
-  const int lane = threadIdx.x & 63;
-  float M = -INFINITY;
-  for (int s = lane; s < splits; s += 64) M = fmaxf(M, lg[s * n]);
+  const int lane = threadIdx.x & 63, last = splits - 1;
+  const int quads = a.D / 4, groups = 256 / quads, g = threadIdx.x / quads, c = threadIdx.x % quads;
+  auto at = [&](int s) { return *reinterpret_cast<const float4*>(part + (s * n + row) * a.D + c * 4); };
+  const float l0 = lg[min(lane, last) * n];
+  float lp[kPre];
+  float4 xp[kPre];
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) {
+    lp[i] = lg[min(g + i * groups, last) * n];
+    xp[i] = at(min(g + i * groups, last));
+  }
+  // rows of no sequence have no parts (what was read of them is not used)
+  if (tok < bound(a.cu_q, 0, a.Tq) || tok >= bound(a.cu_q, a.B, a.Tq)) return;
+  float M = l0;
+  for (int s = lane + 64; s < splits; s += 64) M = fmaxf(M, lg[s * n]);
   M = wave_max(M);
-  float sum = 0.0f;
-  for (int s = lane; s < splits; s += 64) sum += M > -INFINITY ? __builtin_amdgcn_exp2f(lg[s * n] - M) : 0.0f;
+  float sum = lane < splits && M > -INFINITY ? __builtin_amdgcn_exp2f(l0 - M) : 0.0f;
+  for (int s = lane + 64; s < splits; s += 64) sum += M > -INFINITY ? __builtin_amdgcn_exp2f(lg[s * n] - M) : 0.0f;
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  const int quads = a.D / 4, groups = 256 / quads, g = threadIdx.x / quads, c = threadIdx.x % quads;
   float4 o = make_float4(0, 0, 0, 0);
+  auto add = [&](float l, const float4& x) {
+    const float w = __builtin_amdgcn_exp2f(l - M) * inv;
+    o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
+  };
   if (g < groups && M > -INFINITY) {
-    for (int s = g; s < splits; s += groups) {
-      const float w = __builtin_amdgcn_exp2f(lg[s * n] - M) * inv;
-      const float4 x = *reinterpret_cast<const float4*>(part + (s * n + row) * a.D + c * 4);
-      o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
-    }
+#pragma unroll
+    for (int i = 0; i < kPre; ++i)
+      if (g + i * groups < splits) add(lp[i], xp[i]);
+    for (int s = g + kPre * groups; s < splits; s += groups) add(lg[s * n], at(s));
   }
   acc[threadIdx.x] = o;
   __syncthreads();
