@@ -129,19 +129,22 @@ template <int DP> struct Lds {
 //      on their way from LDS.
 // So every run of matrix instructions has vector work of about the same length beside it that does not wait for
 // it, and fragments are read a block ahead of their use.
-constexpr int NW = 4, BM = NW * 32;  // waves, rows
+// With NS = 2 the workgroup has two such sets of waves, each with LDS of its own, for the first and the second half
+// of the keys; the second set hands its O, m and l to the first through LDS at the end.
+constexpr int NW = 4, BM = NW * 32;  // waves of a part, rows
 constexpr int BK = 64;               // keys per tile
 constexpr int kEarly = 10;
 
-template <int DP>
-__global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slots) {
+template <int DP, int NS>
+__global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int slots) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;  // chunks a row, 16-value steps, 32-value blocks
   constexpr int KB = BK * DP * 2;                          // bytes of a K or V tile
   constexpr int LPW = KB / 1024 / NW, RPI = BK / LPW;      // 1 KB loads per wave and operand; rows between them
   constexpr int VRING = 2 * KB;                            // two slots for K tiles, two for V tiles
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  extern __shared__ __align__(16) uint8_t smem_all[];
+  const int lane = threadIdx.x & 63, part = NS > 1 ? uni(threadIdx.x >> 6) / NW : 0, wave = uni(threadIdx.x >> 6) % NW;
   const int l32 = lane & 31, h = lane >> 5;
+  uint8_t* smem = smem_all + part * 4 * KB;
 
   // Workgroups go to the 8 XCDs round-robin: with the key head as the fast index, the tiles of a head meet in
   // one L2 (for 8 key heads; in few for other counts). The last rows, which see the most keys under a causal
@@ -170,8 +173,9 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slot
   }
   const int kend = uni(lim(min(tile * BM + BM, nr) - 1));  // keys of the workgroup
   const int wmin = uni(r0 < nr ? lim(r0) : 0), wmax = uni(r0 < nr ? lim(min(r0 + 32, nr) - 1) : 0);
-  const int nt = (kend + BK - 1) / BK;
-  const int nw = (wmax + BK - 1) / BK, nfull = wmin / BK;  // this wave's tiles; those every row sees whole
+  const int all = (kend + BK - 1) / BK, nt = (all + NS - 1) / NS, t0 = part * nt;  // tiles; of a part; its first
+  // this wave's tiles; those every row sees whole
+  const int nw = min(max((wmax + BK - 1) / BK - t0, 0), nt), nfull = min(max(wmin / BK - t0, 0), nt);
 
   // DMA of a tile: load i of a wave brings rows RPI i + .. to byte 1024 (NW i + wave) + 16 lane of its slot; the rows
   // of a lane differ by RPI, a multiple of 16, so they share one place in the swizzle and one lane offset. The
@@ -188,9 +192,10 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slot
   const uint16_t* kp = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
   const uint16_t* vp = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
   // the tiles that are being brought in: where they start, and the keys from there to the sequence's end
-  const uint8_t *kb = reinterpret_cast<const uint8_t*>(kp), *vb = reinterpret_cast<const uint8_t*>(vp);
-  int kleft = s.lk, vleft = s.lk;
   const uint32_t kr2 = (uint32_t)a.skt * 2u, vr2 = (uint32_t)a.svt * 2u;  // bytes from row to row
+  const uint8_t *kb = reinterpret_cast<const uint8_t*>(kp) + (int64_t)t0 * BK * kr2,
+                *vb = reinterpret_cast<const uint8_t*>(vp) + (int64_t)t0 * BK * vr2;
+  int kleft = s.lk - t0 * BK, vleft = kleft;
   auto load_k = [&](int i, uint32_t to) __attribute__((always_inline)) {
     const int last = min(max(kleft, 0), BK) - 1;  // -1: nothing is left, a resource of no bytes
     const uint32_t n = ((uint32_t)last * kr2 + a.D * 2) & ~(uint32_t)(last >> 31);
@@ -332,11 +337,11 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slot
   };
   auto tile_of = [&](int t, auto maskc) __attribute__((always_inline)) {
     turn();
-    stage(S0, S1, k1, v0, t * BK, [&]() __attribute__((always_inline)) {
+    stage(S0, S1, k1, v0, (t0 + t) * BK, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_v(i, v1);
     }, maskc);
-    stage(S1, S0, k1 + KB / 2, v0 + KB / 2, t * BK + 32, [&]() __attribute__((always_inline)) {
+    stage(S1, S0, k1 + KB / 2, v0 + KB / 2, (t0 + t) * BK + 32, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_k(i, k0);
     }, maskc);
@@ -358,7 +363,36 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slot
   }
   __builtin_amdgcn_s_waitcnt(vm(0));  // no load may outlive the workgroup
 
-  const float lt = pair_sum(l);
+  float lt = pair_sum(l);
+  if constexpr (NS > 1) {  // the second part's results go through its LDS to the waves of the first
+    static_assert(NS == 2, "two parts");
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    __shared__ float red[2][64 * NW];
+    SS_LDS v4f* to = (SS_LDS v4f*)(smem_all + 4 * KB) + wave * 64 + lane;
+    __syncthreads();
+    if (part == 1) {
+      red[0][wave * 64 + lane] = m;
+      red[1][wave * 64 + lane] = lt;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) to[(d * 4 + g) * NW * 64] = v4f{O[d][4 * g], O[d][4 * g + 1], O[d][4 * g + 2], O[d][4 * g + 3]};
+    }
+    __syncthreads();
+    if (part == 1) return;
+    const float m1 = red[0][wave * 64 + lane], mn = fmaxf(m, m1);
+    const float f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(m1 - mn);
+    m = mn;
+    lt = lt * f0 + red[1][wave * 64 + lane] * f1;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const v4f x = to[(d * 4 + g) * NW * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[d][4 * g + e] = O[d][4 * g + e] * f0 + x[e] * f1;
+      }
+  }
   const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;  // a row that sees no key: zeros
   const bool ok = r0 + l32 < nr;
   const int64_t tok = s.q0 + row / a.G;
@@ -386,14 +420,22 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(AttnArgs a, int slot
   }
 }
 
+// Two parts where a CU has few workgroups and a row many keys. Heads of 64, 12 of them: 15.3 against 17.7 us at 1000 causal
+// tokens (96 workgroups), 47.1 / 57.4 at 4000 (384), 20.0 / 24.5 at 1500 without a mask. Heads of 128: 8 of them, 31.2 / 35.1
+// at 2048 tokens (136), 58.0 / 64.3 at 4000 (256); 32 over 8, 15.4 / 14.4 at 512 tokens, 22.5 / 22.4 at 960 (248), 34.6 / 35.5
+// at 1536 (392); 12, no mask, 106.6 / 97.9 at 3500 (336).
 template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
-  auto kern = prompt_kernel<DP>;
-  constexpr int lds = 4 * BK * DP * 2;
-  const hipError_t e = lds_limit((const void*)kern, lds);
-  if (e != hipSuccess) return e;
   const int64_t slots = a.Tq * a.G / BM + a.B;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * a.Hkv)), dim3(64 * NW), lds, st, a, (int)slots);
-  return hipGetLastError();
+  auto go = [&](auto kern, int parts) -> hipError_t {
+    const int lds = parts * 4 * BK * DP * 2;
+    const hipError_t e = lds_limit((const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(slots * a.Hkv)), dim3(64 * NW * parts), lds, st, a, (int)slots);
+    return hipGetLastError();
+  };
+  const int64_t wgs = slots * a.Hkv, cus = num_cus_p();
+  const bool two = DP <= 64 ? 2 * wgs <= 3 * cus && a.Tk >= 512 * (int64_t)a.B : wgs <= cus && a.Tk >= 1024 * (int64_t)a.B;
+  return two ? go(prompt_kernel<DP, 2>, 2) : go(prompt_kernel<DP, 1>, 1);
 }
 
 // ---- few rows per sequence: the keys split over waves and workgroups ---------------------------------------------

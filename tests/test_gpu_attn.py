@@ -91,6 +91,21 @@ def test_many_tiles(ss, Hq, Hkv, lq, lk):
     _run(ss, lq, lk, Hq, Hkv, 128, True, seed=3)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 2, 64), (3, 1, 40), (2, 1, 128), (1, 1, 96)])
+@pytest.mark.parametrize("lq,lk", [
+    ([100], [1100]), ([1100], [1100]), ([1090], [1025]), ([70, 40], [2100, 63]), ([33, 200, 40], [3200, 0, 1]), ([40], [6000])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_workgroups_split_the_keys(ss, lq, lk, causal, Hq, Hkv, D):
+    q, k, v, o, lse = _run(ss, lq, lk, Hq, Hkv, D, causal, seed=D)
+    again = torch.empty_like(lse)
+    assert torch.equal(ss.attn(q, k, v, _i32(_cum(lq)), _i32(_cum(lk)), causal=causal, lse=again), o) and torch.equal(again, lse)
+
+
+def test_many_workgroups_of_long_keys(ss):
+    _run(ss, [1300, 2000], [1300, 2000], 16, 16, 64, True, seed=8)
+    _run(ss, [1500], [1500], 24, 24, 128, False, seed=9)
+
+
 @pytest.mark.parametrize("D", [8, 64, 72, 128])
 @pytest.mark.parametrize("lq,lk", [([1], [5000]), ([1, 1, 1], [3000, 1, 0]), ([4], [4097]), ([3, 1], [33, 6001]), ([2], [1])])
 def test_few_rows_split_over_workgroups(ss, lq, lk, D):
