@@ -452,7 +452,7 @@ ss_status ss_rotary_steps(int rot_dim, double base, ss_rope_scaling scaling, dou
  * token and head strides sxt, sxh / syt, syh >= 0. pos: T int32, any values.
  * steps: rot_dim / 2 device words of ss_rotary_steps, 8-byte aligned;
  * 2 <= rot_dim <= D, even. mscale finite. y may be x with the same strides (in
- * place), else the two must not overlap. x and y need the alignment of their
+ * place), else the two must not overlap, nor the heads of y each other. x and y need the alignment of their
  * elements only; 16-byte vectors are used where pointers, strides and sizes
  * allow. */
 ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t D, int64_t sxt, int64_t sxh,
@@ -473,7 +473,8 @@ ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t 
  * last query row with the last key: row i of lq sees keys 0 .. i + lk - lq. A
  * row that sees no key gives zeros (and lse -inf). Query rows in no sequence
  * leave o and lse untouched; key rows in no sequence or behind k_len are never
- * part of a result, whatever they hold.
+ * part of a result, whatever they hold; a NaN or an infinity in a key row that
+ * only some rows see reaches those alone. Heads of o must not overlap.
  *   lse: NULL, or [Hq][Tq] floats that receive the natural logarithm of each
  * row's sum of exp(scale * q . k).
  *   8 <= D <= 128, D % 8 == 0 (SS_ERR_UNSUPPORTED otherwise), Hq % Hkv == 0, scale finite and

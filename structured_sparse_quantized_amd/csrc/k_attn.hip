@@ -35,6 +35,7 @@ namespace attn {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kSlack = 8.0f;     // in powers of two
@@ -119,6 +120,34 @@ template <int DP> struct Lds {
   __device__ static int swk(int row) { return row & (CH - 1); }
   __device__ static int swv(int row) { return DP >= 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
 };
+
+// A causal mask gives the rows of a tile different keys, but one product takes them all: a power of zero keeps a finite
+// value of an unseen key out of a row, not an infinity or a NaN. Where a tile's values hold one, it is replaced by zero
+// in the operand and added to the rows that see it by hand (its power is above zero, so the sum is v itself).
+__device__ __forceinline__ uint32_t odd_bf16x2(uint32_t w) {  // bits 31, 15: that half is infinite or NaN
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t even_out(uint32_t w) {
+  asm volatile("" : "+v"(w));  // (computed anew: its parts are not kept from the test)
+  return w & ~((odd_bf16x2(w) >> 15) * 0xFFFFu);
+}
+// `vt`: 32 rows of values in LDS, of which row r of the lane sees the first `seen`
+template <int DP> __device__ __forceinline__ void add_odd(v16f* O, const SS_LDS uint8_t* vt, int seen, int h) {
+  asm volatile("" : "+v"(h), "+v"(seen));  // (nothing of this is kept in registers beside the loop that calls it)
+#pragma unroll 1
+  for (int k = 0; k < 32; ++k)
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const v2u w = *reinterpret_cast<const SS_LDS v2u*>(vt + k * DP * 2 + ((d * 4 + g) ^ Lds<DP>::swv(k)) * 16 + h * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+          if (k < seen && !__builtin_isfinite(v)) O[d][4 * g + e] += v;
+        }
+      }
+}
 
 // ---- many rows: tiles of 4 waves x 32 rows, two workgroups per CU ----------------------------------------------
 // The work of a wave is pipelined over stages of 32 keys (two to a tile of BK). Stage j, in program order:
@@ -296,6 +325,27 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     P[0] = __builtin_bit_cast(v8bf, pk[0]);
     P[1] = __builtin_bit_cast(v8bf, pk[1]);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(maskc)::value) {
+      if (wmin < wmax && first + 32 > wmin) {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int j = 0; j < 2 * DB; ++j) {
+          const v4u w = __builtin_bit_cast(v4u, vf[j / DB][j % DB]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd |= odd_bf16x2(w[i]);
+        }
+        if (__builtin_expect(__any(odd != 0), 0)) {
+#pragma unroll
+          for (int j = 0; j < 2 * DB; ++j) {
+            v4u w = __builtin_bit_cast(v4u, vf[j / DB][j % DB]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = even_out(w[i]);
+            vf[j / DB][j % DB] = __builtin_bit_cast(v8bf, w);
+          }
+          add_odd<DP>(O, (const SS_LDS uint8_t*)smem + vc, row_lim - first, h);
+        }
+      }
+    }
   };
 
   // Iteration t reads K tile t + 1 and V tile t and brings in K tile t + 2 and V tile t + 1, into the slots of K tile t
@@ -393,12 +443,12 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
         for (int e = 0; e < 4; ++e) O[d][4 * g + e] = O[d][4 * g + e] * f0 + x[e] * f1;
       }
   }
-  const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;  // a row that sees no key: zeros
+  const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;  // a row that sees no key: zeros (of a NaN: NaN)
   const bool ok = r0 + l32 < nr;
   const int64_t tok = s.q0 + row / a.G;
   const int head = kvh * a.G + row % a.G;
   if (a.lse && ok && h == 0)
-    a.lse[head * a.Tq + tok] = lt > 0.0f ? (m + __builtin_amdgcn_logf(lt)) * 0.69314718056f : -INFINITY;
+    a.lse[head * a.Tq + tok] = lt == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(lt)) * 0.69314718056f;
   uint16_t* op = a.o + tok * a.sot + head * a.soh;
 #pragma unroll
   for (int d = 0; d < DB; ++d) {
@@ -524,7 +574,28 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
     __builtin_amdgcn_sched_barrier(0);
     const SS_LDS uint8_t* kt = ring + at;
     const SS_LDS uint8_t* vt = kt + KB;
+    const int vo = at + KB;
     at = RING / FR - at;
+    if (kmin < kend && u * 32 + 32 > kmin) {  // rows that see different keys of this unit
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < LPU; ++i) {
+        const v4u w = *reinterpret_cast<const SS_LDS v4u*>(vt + (i * 64 + lane) * 16);
+        odd |= odd_bf16x2(w[0]) | odd_bf16x2(w[1]) | odd_bf16x2(w[2]) | odd_bf16x2(w[3]);
+      }
+      if (__builtin_expect(__any(odd != 0), 0)) {
+        add_odd<DP>(O, vt, row_lim - u * 32, h);
+#pragma unroll 1
+        for (int i = 0; i < LPU; ++i) {
+          SS_LDS v4u* p = (SS_LDS v4u*)(ring + vo + (i * 64 + lane) * 16);
+          const v4u w = *p;
+          *p = v4u{even_out(w[0]), even_out(w[1]), even_out(w[2]), even_out(w[3])};
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        asm volatile("" ::: "memory");  // the reads below stay below
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     v16f S = v16f{};
 #pragma unroll
     for (int i = 0; i < KST; ++i) {
@@ -613,10 +684,10 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
       const float4 x = *reinterpret_cast<const float4*>(smem + w * RING + row * OST + c * 4);
       o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int rr = r0 + row, head = kvh * a.G + rr % a.G;
     const int64_t tok = s.q0 + rr / a.G;
-    const float lg = L > 0.0f ? M2 + __builtin_amdgcn_logf(L) : -INFINITY;  // log2 of the row's sum
+    const float lg = L == 0.0f ? -INFINITY : M2 + __builtin_amdgcn_logf(L);  // log2 of the row's sum
     if constexpr (SPLIT) {
       const int64_t Hq = (int64_t)a.Hkv * a.G, at_row = (blockIdx.y * a.Tq + tok) * Hq + head;
       *reinterpret_cast<float4*>(part + at_row * a.D + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -655,17 +726,18 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __re
   float M = l0;
   for (int s = lane + 64; s < splits; s += 64) M = fmaxf(M, lg[s * n]);
   M = wave_max(M);
-  float sum = lane < splits && M > -INFINITY ? __builtin_amdgcn_exp2f(l0 - M) : 0.0f;
-  for (int s = lane + 64; s < splits; s += 64) sum += M > -INFINITY ? __builtin_amdgcn_exp2f(lg[s * n] - M) : 0.0f;
+  auto power = [&](float l) { return l == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(l - M); };  // (of a NaN: NaN)
+  float sum = lane < splits ? power(l0) : 0.0f;
+  for (int s = lane + 64; s < splits; s += 64) sum += power(lg[s * n]);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float4 o = make_float4(0, 0, 0, 0);
   auto add = [&](float l, const float4& x) {
-    const float w = __builtin_amdgcn_exp2f(l - M) * inv;
+    const float w = power(l) * inv;
     o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
   };
-  if (g < groups && M > -INFINITY) {
+  if (g < groups) {
 #pragma unroll
     for (int i = 0; i < kPre; ++i)
       if (g + i * groups < splits) add(lp[i], xp[i]);
@@ -682,7 +754,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __re
         make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   }
   if (a.lse && threadIdx.x == 0)
-    a.lse[head * a.Tq + tok] = sum > 0.0f ? (M + __builtin_amdgcn_logf(sum)) * 0.69314718056f : -INFINITY;
+    a.lse[head * a.Tq + tok] = sum == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.69314718056f;
 }
 
 // Calls whose sequences have 32 rows or fewer on average go to few_kernel.
@@ -722,6 +794,12 @@ int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int6
   if (Tk == 0 || !attn::few_rows(Tq, B, G)) return 0;
   const int64_t n = attn::splits(Tq, Tk, B, G, Hkv);
   return n == 1 ? 0 : n * Tq * Hq * (D + 1) * 4;
+}
+
+// a launch holds fewer than 2^32 threads
+bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv) {
+  const int64_t G = Hq / Hkv, few = Tk > 0 && attn::few_rows(Tq, B, G);
+  return (few ? attn::few_slots(Tq, B, G) * 64 * attn::FW : (Tq * G / attn::BM + B) * 64 * attn::NW) * Hkv <= 0xFFFFFFFFLL;
 }
 
 hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {

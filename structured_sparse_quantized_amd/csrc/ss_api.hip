@@ -649,7 +649,8 @@ ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_
     return fail(SS_ERR_SHAPE, "%lld query heads do not divide into %lld key heads", (long long)Hq, (long long)Hkv);
   if (D < 8 || D > 128 || D % 8 != 0) return fail(SS_ERR_UNSUPPORTED, "D=%lld must be a multiple of 8 within 8..128", (long long)D);
   if (!(scale > 0) || !std::isfinite(scale * 1.5f)) return fail(SS_ERR_SHAPE, "scale must be positive and finite");
-  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL)
+  if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL ||
+      !ss::attn_fits(Tq, Tk, B, Hq, Hkv))
     return fail(SS_ERR_SHAPE, "too large");
   if ((!cu_q || !cu_k) && B != 1) return fail(SS_ERR_NULL, "cu_q and cu_k are required with %lld sequences", (long long)B);
   // the stride of a single token or head is never taken

@@ -117,6 +117,7 @@ struct AttnArgs {
   int causal;
 };
 int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv);  // (a launch's threads)
 hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st);
 
 // Rotary positions on [T][H][D] views (strides in elements, t: token, h: head); y may be x (same strides).

@@ -113,6 +113,35 @@ def test_few_rows_split_over_workgroups(ss, lq, lk, D):
     _run(ss, lq, lk, 4, 4, D, False, seed=D + 1)
 
 
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [
+    (200, 200, 2, 2, 128), (300, 333, 3, 1, 64), (150, 100, 2, 1, 40),  # tiles of many rows
+    (100, 1100, 2, 1, 128), (1100, 1100, 1, 1, 64),  # the keys in two parts
+    (6, 500, 4, 1, 128), (7, 90, 2, 2, 64), (4, 5000, 7, 1, 72)])  # few rows, one workgroup and several
+def test_infinities_and_nan_reach_the_rows_that_see_them(ss, lq, lk, Hq, Hkv, D):
+    g = torch.Generator(device="cuda").manual_seed(lq)
+    q = torch.randn((lq, Hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    k, v = (torch.randn((lk, Hkv, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    clean, lse, lse_k = ss.attn(q, k, v), torch.empty((Hq, lq), device="cuda"), torch.empty((Hq, lq), device="cuda")
+    ss.attn(q, k, v, lse=lse)
+    seen = (torch.arange(lq, device="cuda") + lk - lq + 1).clamp(0, lk)  # keys of a row
+    for back in (1, 2, min(lq - 1, 5), min(lq - 1, 40)):
+        j = max(lk - back, 0)
+        rows = seen > j
+        vb = v.clone()
+        vb[j, :, 1], vb[j, :, 3], vb[j, :, D - 1] = float("nan"), float("inf"), -float("inf")
+        o = ss.attn(q, k, vb, lse=lse_k)
+        assert torch.equal(o[~rows], clean[~rows]) and torch.equal(lse_k, lse)
+        other = [c for c in range(D) if c not in (1, 3, D - 1)]
+        assert torch.equal(o[:, :, other], clean[:, :, other])
+        assert o[rows][:, :, 1].isnan().all() and (o[rows][:, :, 3] == float("inf")).all()
+        assert (o[rows][:, :, D - 1] == -float("inf")).all()
+        kb = k.clone()
+        kb[j, :, 2] = float("nan")
+        o = ss.attn(q, kb, v, lse=lse_k)
+        assert torch.equal(o[~rows], clean[~rows]) and torch.equal(lse_k[:, ~rows], lse[:, ~rows])
+        assert o[rows].isnan().all() and lse_k[:, rows].isnan().all()
+
+
 def test_own_workspace(ss):
     """A workspace of the stated size serves; its contents before do not matter."""
     q = torch.randn((2, 8, 64), device="cuda").to(torch.bfloat16)

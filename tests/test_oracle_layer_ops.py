@@ -127,6 +127,7 @@ def test_attention_refusals():
     assert call(q=odd) == call(k=odd) == call(o=odd) == call(st=60) == call(skh=12) == call(lse=ctypes.c_void_p(2)) == ss.SS_ERR_ALIGN
     assert call(sot=8) == call(st=-64) == ss.SS_ERR_SHAPE
     assert call(skt=1 << 24) == ss.SS_ERR_UNSUPPORTED
+    assert call(B=1 << 27, Hq=64, Hkv=64) == call(Tq=1 << 30, Hq=512, Hkv=512) == ss.SS_ERR_SHAPE  # 2^32 threads and more
     assert call(B=2, cq=None) == call(B=2, ck=None) == ss.SS_ERR_NULL
     assert call(Tq=0, q=None) == call(B=0) == call(Hq=0, Hkv=0) == ss.SS_OK
     need = ss.attn_workspace_bytes(8, 10000, 1, 4, 2, 16)  # few rows, many keys: split over workgroups
