@@ -276,7 +276,8 @@ ss_status ss_spgemm_tiled_ws(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_
  * makes Y [M][N / 2] (N even): weight rows 2j and 2j + 1 hold the gate and the
  * value of column j (a caller interleaves the two matrices before the weight
  * preparation). Exponentials, where y_dt is BF16, are the chip's own (relative
- * error below 2^-19 for |z| < 16).
+ * error below 2^-19 for |z| < 16) and erf is good to 1.5e-7 absolute. A NaN of z
+ * stays a NaN under every activation.
  * Sides, operands, scales (both for I8 and FP8E4M3), workspace and errors as
  * ss_spgemm_tiled_ws; the workspace query is the same. */
 typedef enum {

@@ -60,7 +60,7 @@ template <int N, bool SHORT = false> __device__ __forceinline__ void activate_n(
   if constexpr (SHORT) f32 = false;
   if (act == 1) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = fmaxf(z[i], 0.0f);
+    for (int i = 0; i < N; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];  // (a NaN stays)
   } else if (act == 2) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -197,6 +197,22 @@ def test_large_arguments(ss):
             assert torch.isfinite(p.run(ss, bias=100 * z, act=act, y_dtype=y)).all()
 
 
+@pytest.mark.parametrize("side,M,N", [("W", 3, 70), ("W", 40, 600), ("W", 300, 602), ("X", 100, 90), ("W", 2200, 4096)])
+def test_nan_stays_in_its_column(ss, side, M, N):
+    p = Problem(ss, side, "fp8", M, N, 256, seed=6)
+    b = torch.randn(N, device="cuda")
+    nan = b.clone()
+    nan[[6, N - 3]] = float("nan")  # a gate (even) and a value (odd)
+    for act in ACTS:
+        for gated in (False, True):
+            for y in ("bf16", "f32"):
+                kw = dict(act=act, gated=gated, y_dtype=y)
+                got, clean = p.run(ss, bias=nan, **kw), p.run(ss, bias=b, **kw)
+                bad = torch.zeros(got.shape[1], dtype=torch.bool, device="cuda")
+                bad[[6 >> gated, (N - 3) >> gated]] = True
+                assert got[:, bad].isnan().all() and torch.equal(got[:, ~bad], clean[:, ~bad])
+
+
 def test_workspace_stream_and_graph(ss):
     for M, N in ((40, 600), (2200, 4096)):
         p = Problem(ss, "W", "fp8", M, N, 512, seed=5)
