@@ -11,6 +11,8 @@
 // Bound: every value is read and written once (HBM). No cos/sin table is read: a thread computes the angles
 // of its pairs once and applies them to several heads of the token; it loads a batch of heads before it
 // stores the first, so that several loads are in flight also where the output is the input.
+// Measured: 16384 tokens, 40 heads of 128, bf16: 67 us, 5.0 TB/s (a large copy: 4.9); 777 tokens, 14 heads of 80 of which
+// 32 turn, float32: 4.1 us; one token, 40 heads: 2.5 us, which is what a launch takes.
 #include <algorithm>
 
 #include "ss_device.h"
