@@ -111,10 +111,9 @@ template <int BM> __device__ __forceinline__ bool find_tile(const AttnArgs& a, i
 
 // LDS tiles are row-major (DP values a row, in 16-byte chunks) with the chunks of a row permuted by an XOR, so
 // that the fragment reads below spread over the banks: a K fragment reads one chunk column of 32 rows, a V
-// fragment 4 chunks of 4 rows.
+// fragment 4 chunks of 4 rows (rows of 64 values lie two to a turn of the banks, so pairs of rows share a place).
 template <int DP> struct Lds {
-  static constexpr int CH = DP / 8;  // chunks a row
-  __device__ static int swk(int row) { return row & (CH - 1); }
+  __device__ static int swk(int row) { return DP >= 128 ? row & 15 : (row >> 1) & 7; }
   __device__ static int swv(int row) { return DP >= 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
 };
 
