@@ -283,9 +283,8 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     float mt = cur[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) mt = fmaxf(mt, cur[i]);
-    mt = pair_max(mt) * a.c;
-    if (__any(mt > m + kSlack)) {
-      const float mn = fmaxf(m, ceilf(mt)), f = __builtin_amdgcn_exp2f(m - mn);  // a power of two: exact
+    if (__any(mt * a.c > m + kSlack)) {  // (of the row's two lanes one sees it)
+      const float mn = fmaxf(m, ceilf(pair_max(mt) * a.c)), f = __builtin_amdgcn_exp2f(m - mn);  // a power of two: exact
       m = mn;
       l *= f;
 #pragma unroll
@@ -616,9 +615,8 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
     float mt = S[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) mt = fmaxf(mt, S[i]);
-    mt = pair_max(mt) * a.c;
-    if (__any(mt > m + kSlack)) {
-      const float mn = fmaxf(m, mt), f = __builtin_amdgcn_exp2f(m - mn);
+    if (__any(mt * a.c > m + kSlack)) {
+      const float mn = fmaxf(m, pair_max(mt) * a.c), f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= f;
 #pragma unroll
