@@ -3,8 +3,9 @@
 // Mathematics. One pass over the keys with a running maximum and sum: for a query row, after keys 0..j,
 //   m = max_i s_i, l = sum_i 2^(c s_i - m), O = sum_i 2^(c s_i - m) v_i  (s = q.k, c = scale * log2 e),
 // and o = O / l. A new maximum m' multiplies l and O by 2^(m - m'). m only has to keep the powers in range,
-// so it is raised only when a row's maximum passes it by more than kSlack (the powers then stay below 2^kSlack;
-// their relative precision is the same), which leaves O untouched on almost every tile. Scores, m, l and O are
+// so it is raised only when a row's maximum passes it by more than kSlack, or (tiles of many rows) when 16 of its
+// powers sum to more than kRise: the powers then stay below 2^8, their relative precision is the same, and O is left
+// untouched on almost every tile. Scores, m, l and O are
 // float32; the powers are rounded to bf16 (nearest even) for the second product, because the matrix
 // instructions take bf16 there: with q, k, v in bf16 that adds one rounding of at most 2^-8 relative per
 // key, independent over the keys. l sums the powers before that rounding.
@@ -39,6 +40,7 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr float kSlack = 8.0f;     // in powers of two
+constexpr float kRise = 256.0f;
 constexpr int vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }  // s_waitcnt vmcnt(n)
 constexpr float kLow = -1.0e30f;   // below every finite score's exponent; 2^(kLow - m) = 0
 
@@ -145,15 +147,18 @@ template <int DP> __device__ __forceinline__ void add_odd(v16f* O, const SS_LDS 
       }
 }
 
+// What is computed from x is computed anew from here on (in the loops that have no registers to keep it in).
+__device__ __forceinline__ void renew(uint32_t& x) { asm volatile("" : "+v"(x)); }
+
 // ---- many rows: tiles of 4 waves x 32 rows, two workgroups per CU ----------------------------------------------
 // The work of a wave is pipelined over stages of 32 keys (two to a tile of BK). Stage j, in program order:
-//   A: O += V P of stage j - 1 (its first 16 keys, then the others, whose powers are finished meanwhile), and the
-//      maximum of the scores of stage j; the K fragments of stage j + 1 on their way from LDS;
-//   (where a row's maximum has risen by more than kSlack: l and O rescaled)
-//   B: the scores of stage j + 1, and the first kEarly of each row's 16 powers of stage j; the V fragments of stage j
-//      on their way from LDS.
-// So every run of matrix instructions has vector work of about the same length beside it that does not wait for
-// it, and fragments are read a block ahead of their use.
+//   the scores of stage j + 1, O += V P of stage j - 1, and between them the powers of stage j, step by step; a
+//   fragment that has been used is read anew from LDS for the next stage at once;
+//   where a lane's 16 powers sum to more than kRise (or overflow): the row's maximum found, l and O rescaled, the powers
+//   taken again. Looking at the sum that is there anyway, after the fact, keeps 8 instructions and a branch
+//   that waits for them out of every stage (1-3% for heads of 128, 6% for 64); the first stage's maximum is found ahead.
+// So the matrix instructions have vector work of about the same length beside them that does not wait for
+// them, and fragments are read a stage ahead of their use.
 // Measured: one prompt of 8192 tokens, 32 heads of 128 over 8, causal: 525 us, 1.05 PFLOP/s of the seen pairs (matrix cores
 // busy 62% of the cycles, at the 1.8 GHz the card keeps under this load; its large bf16 product runs at 1.37); 9 packed
 // prompts, 8001 tokens, 28 heads over 4: 90 us, 0.66 PFLOP/s. What bounds it is the vector work beside the matrix
@@ -165,7 +170,6 @@ template <int DP> __device__ __forceinline__ void add_odd(v16f* O, const SS_LDS 
 // of the keys; the second set hands its O, m and l to the first through LDS at the end.
 constexpr int NW = 4, BM = NW * 32;  // waves of a part, rows
 constexpr int BK = 64;               // keys per tile
-constexpr int kEarly = 10;
 
 template <int DP, int NS>
 __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int slots) {
@@ -280,27 +284,6 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
       for (int i = 0; i < 16; ++i)
         if (8 * (i / 4) + i % 4 >= left) cur[i] = -INFINITY;
     }
-    float mt = cur[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, cur[i]);
-    if (__any(mt * a.c > m + kSlack)) {  // (of the row's two lanes one sees it)
-      const float mn = fmaxf(m, ceilf(pair_max(mt) * a.c)), f = __builtin_amdgcn_exp2f(m - mn);  // a power of two: exact
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) O[d][i] *= f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        v4u w = __builtin_bit_cast(v4u, P[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
-        P[k] = __builtin_bit_cast(v8bf, w);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
     side();
     nxt = v16f{};
     v4u pk[2];
@@ -322,6 +305,27 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
       const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i + 1], a.c, -m));
       sum += x + y;
       pk[i / 4][i % 4] = pack_bf16x2(x, y);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (__builtin_expect(__any(sum > kRise), 0)) {
+      float mt = cur[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) mt = fmaxf(mt, cur[i]);
+      const float mn = fmaxf(m, ceilf(pair_max(mt) * a.c)), f = __builtin_amdgcn_exp2f(m - mn);  // a power of two: exact
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[d][i] *= f;
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i], a.c, -m));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i + 1], a.c, -m));
+        sum += x + y;
+        pk[i / 4][i % 4] = pack_bf16x2(x, y);
+      }
     }
     l += sum;
     P[0] = __builtin_bit_cast(v8bf, pk[0]);
@@ -373,6 +377,12 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     for (int i = 0; i < KST; ++i) S0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], qf[i], S0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < KST; ++i) read_k(i, KB / 2);
+    const int left = row_lim - t0 * BK - 4 * h;
+    float mt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (8 * (i / 4) + i % 4 < left) mt = fmaxf(mt, S0[i]);
+    m = fmaxf(m, ceilf(pair_max(mt) * a.c));
   }
   auto turn = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
@@ -389,6 +399,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   };
   auto tile_of = [&](int t, auto maskc) __attribute__((always_inline)) {
     turn();
+    if constexpr (decltype(maskc)::value) renew(ofk), renew(ofv);
     stage(S0, S1, k1, v0, (t0 + t) * BK, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_v(i, v1);

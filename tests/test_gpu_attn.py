@@ -113,6 +113,23 @@ def test_few_rows_split_over_workgroups(ss, lq, lk, D):
     _run(ss, lq, lk, 4, 4, D, False, seed=D + 1)
 
 
+@pytest.mark.parametrize("amp", [1.0, 30.0, 800.0])
+@pytest.mark.parametrize("lq,lk,D", [(200, 700, 128), (1500, 1500, 64), (90, 1300, 128), (5, 900, 64)])
+def test_maxima_that_rise_along_the_keys(ss, lq, lk, D, amp):
+    """Scores that grow (and for half of the rows fall) from key to key, by less and by far more than a float's range
+    of exponents from one tile to the next."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q = 0.1 * torch.randn((lq, 2, D), generator=g, device="cuda")
+    k = 0.1 * torch.randn((lk, 2, D), generator=g, device="cuda")
+    v = torch.randn((lk, 2, D), generator=g, device="cuda").to(torch.bfloat16)
+    q[:, :, 0] = torch.where(torch.arange(lq, device="cuda") % 2 == 0, 1.0, -1.0)[:, None] * D ** 0.5
+    k[:, :, 0] = torch.linspace(-amp, amp, lk, device="cuda")[:, None]
+    q, k = q.to(torch.bfloat16), k.to(torch.bfloat16)
+    lse = torch.empty((2, lq), device="cuda")
+    o = ss.attn(q, k, v, causal=True, lse=lse)
+    _compare(o, lse, attention(*(t.float().cpu().numpy() for t in (q, k, v)), [0, lq], [0, lk], None, True, None), norm=False)
+
+
 @pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [
     (200, 200, 2, 2, 128), (300, 333, 3, 1, 64), (150, 100, 2, 1, 40),  # tiles of many rows
     (100, 1100, 2, 1, 128), (1100, 1100, 1, 1, 64),  # the keys in two parts
