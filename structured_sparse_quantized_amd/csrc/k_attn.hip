@@ -483,10 +483,11 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   }
 }
 
-// Two parts where a CU has few workgroups and a row many keys. Heads of 64, 12 of them: 15.3 against 17.7 us at 1000 causal
-// tokens (96 workgroups), 47.1 / 57.4 at 4000 (384), 20.0 / 24.5 at 1500 without a mask. Heads of 128: 8 of them, 31.2 / 35.1
-// at 2048 tokens (136), 58.0 / 64.3 at 4000 (256); 32 over 8, 15.4 / 14.4 at 512 tokens, 22.5 / 22.4 at 960 (248), 34.6 / 35.5
-// at 1536 (392); 12, no mask, 106.6 / 97.9 at 3500 (336).
+// Two parts where a CU has few workgroups and a row many keys. Heads of 64: 12 of them, 14.2 against 15.6 us at 1000 causal
+// tokens (96 workgroups), 43.0 / 49.3 at 4000 (384), 18.2 / 20.4 at 1500 without a mask; 8 of them, 86.8 / 99.1 at 8000 (504);
+// 8.6 / 8.0 at 300, 11.3 / 11.5 at 600. Heads of 128: 8 of them, 31.1 / 33.6 at 2048 tokens (136), 55.1 / 60.7 at 4000
+// (256), 22.1 / 22.7 at 1200 without a mask; 32 over 8, 15.5 / 14.3 at 512 tokens, 22.3 / 21.6 at 960 (248), 34.9 / 34.0 at
+// 1536 (392); 12, no mask, 101.1 / 90.3 at 3500 (336).
 template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
   const int64_t slots = a.Tq * a.G / BM + a.B;
   auto go = [&](auto kern, int parts) -> hipError_t {
@@ -497,7 +498,7 @@ template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
     return hipGetLastError();
   };
   const int64_t wgs = slots * a.Hkv, cus = num_cus_p();
-  const bool two = DP <= 64 ? 2 * wgs <= 3 * cus && a.Tk >= 512 * (int64_t)a.B : wgs <= cus && a.Tk >= 1024 * (int64_t)a.B;
+  const bool two = DP <= 64 ? wgs <= 2 * cus && a.Tk >= 512 * (int64_t)a.B : wgs <= cus && a.Tk >= 1024 * (int64_t)a.B;
   return two ? go(prompt_kernel<DP, 2>, 2) : go(prompt_kernel<DP, 1>, 1);
 }
 
