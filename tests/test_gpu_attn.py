@@ -172,6 +172,33 @@ def test_own_workspace(ss):
         ss.attn(q, k, v, workspace=ws[: need - 1])
 
 
+def test_offsets_beyond_32_bits(ss):
+    """Sequences behind more than 2^31 elements of keys, and one sequence longer than that."""
+    far = 2200000
+    k, v = (torch.zeros((far, 8, 128), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k[-900:], v[-900:] = (torch.randn((900, 8, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    for lq in (1, 200):
+        q = torch.randn((lq, 16, 128), generator=g, device="cuda").to(torch.bfloat16)
+        o = ss.attn(q, k, v, _i32([0, lq]), _i32([far - 900, far]))
+        ref = attention(q.float().cpu().numpy(), *(t[-900:].float().cpu().numpy() for t in (k, v)), [0, lq], [0, 900])
+        _compare(o, None, ref)
+    del k, v
+    n = 17000000
+    k, v = (torch.zeros((n, 1, 128), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+    k[-100:, 0] = 6 * q.float().mean(1).to(torch.bfloat16)
+    v[-100:] = torch.randn((100, 1, 128), generator=g, device="cuda").to(torch.bfloat16)
+    o = ss.attn(q, k, v)
+    s = k[-100:, 0].double() @ q[0].double().T * 128 ** -0.5  # the other keys score 0
+    e = torch.exp(s)
+    p = e / (e.sum(0) + (n - 100))
+    want = (p.T[:, :, None] * v[None, -100:, 0].double()).sum(1)
+    mass = (p.T[:, :, None] * v[None, -100:, 0].double().abs()).sum(1)
+    assert float(p.sum(0).min()) > 0.5  # the last keys carry the row
+    assert ((o[0].double() - want).abs() <= mass * (2.0 ** -8 + float(s.abs().max()) * 8e-5 + 6e-5) + 2.0 ** -8 * want.abs()).all()
+
+
 def test_large_scores(ss):
     """Scores far apart: the running maximum rises many times and most powers vanish."""
     _run(ss, [130], [260], 2, 1, 64, True, seed=5, amp=8.0)

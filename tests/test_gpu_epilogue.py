@@ -244,6 +244,18 @@ def test_workspace_stream_and_graph(ss):
             assert torch.equal(out, eager)
 
 
+@pytest.mark.parametrize("gated,N", [(False, 28672), (False, 28671), (True, 57344)])
+def test_outputs_beyond_32_bits(ss, gated, N):
+    M, K, cols = 80000, 256, N // 2 if gated else N
+    p = Problem(ss, "W", "fp8", 400, N, K, seed=8)
+    dense, sx = p.dense.repeat(M // 400, 1), p.sx.repeat(M // 400)
+    res = torch.zeros((M, cols), device="cuda", dtype=torch.bfloat16)
+    res[-400:] = torch.randn((400, cols), device="cuda").to(torch.bfloat16)
+    want = p.run(ss, act="relu", gated=gated, residual=res[-400:].clone())
+    y = ss.spgemm_tiled_epilogue(p.side, M, N, p.Kc, p.tv, p.tm, dense, sx, p.sw, act="relu", gated=gated, residual=res)
+    assert torch.equal(y[-400:], want)
+
+
 def test_refused(ss):
     p = Problem(ss, "W", "i8", 8, 32, 256)
     one = torch.zeros((8, 32), device="cuda")

@@ -129,6 +129,17 @@ def test_stream_and_graph(ss):
         assert torch.equal(y, ss.rotary(x, pos, steps))
 
 
+def test_offsets_beyond_32_bits(ss):
+    T, H, D = 430000, 40, 128
+    steps, m = ss.rotary_steps(D)
+    x = torch.zeros((T, H, D), device="cuda", dtype=torch.bfloat16)
+    x[-50:] = torch.randn((50, H, D), device="cuda").to(torch.bfloat16)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    want = ss.rotary(x[-50:].clone(), pos[-50:].clone(), steps, mscale=m)
+    assert torch.equal(ss.rotary(x, pos, steps, mscale=m)[-50:], want)
+    assert torch.equal(ss.rotary(x, pos, steps, mscale=m, out=x)[-50:], want)
+
+
 def test_empty_and_refused(ss):
     steps, _ = ss.rotary_steps(32)
     pos = torch.zeros(0, dtype=torch.int32, device="cuda")
