@@ -72,18 +72,26 @@ struct Seq {
   int64_t q0, k0;  // first query and key row
   int lq, lk;      // rows
 };
+__device__ __forceinline__ int64_t inside(int x, int64_t n) { return min(max((int64_t)x, (int64_t)0), n); }
 __device__ __forceinline__ int64_t bound(const int32_t* cu, int i, int64_t n) {  // NULL: one sequence of all rows
-  return cu ? min(max((int64_t)cu[i], (int64_t)0), n) : i == 0 ? 0 : n;
+  return cu ? inside(cu[i], n) : i == 0 ? 0 : n;
 }
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  int64_t q0, q1, k0, k1;
+  int len = 0x7FFFFFFF;
+  if (a.cu_q && a.cu_k) {  // the five loads set out together (a call of few keys is a chain of such latencies)
+    const int x0 = a.cu_q[b], x1 = a.cu_q[b + 1], y0 = a.cu_k[b], y1 = a.cu_k[b + 1], n = (a.k_len ? a.k_len : a.cu_q)[b];
+    q0 = inside(x0, a.Tq), q1 = inside(x1, a.Tq), k0 = inside(y0, a.Tk), k1 = inside(y1, a.Tk);
+    if (a.k_len) len = n;
+  } else {
+    q0 = bound(a.cu_q, b, a.Tq), q1 = bound(a.cu_q, b + 1, a.Tq), k0 = bound(a.cu_k, b, a.Tk), k1 = bound(a.cu_k, b + 1, a.Tk);
+    if (a.k_len) len = a.k_len[b];
+  }
   Seq s;
-  const int64_t q0 = bound(a.cu_q, b, a.Tq), q1 = max(bound(a.cu_q, b + 1, a.Tq), q0);
-  const int64_t k0 = bound(a.cu_k, b, a.Tk), k1 = max(bound(a.cu_k, b + 1, a.Tk), k0);
   s.q0 = q0;
   s.k0 = k0;
-  s.lq = (int)(q1 - q0);
-  s.lk = (int)(k1 - k0);
-  if (a.k_len) s.lk = min(max(a.k_len[b], 0), s.lk);
+  s.lq = (int)(max(q1, q0) - q0);
+  s.lk = min(max(len, 0), (int)(max(k1, k0) - k0));
   return s;
 }
 
@@ -109,6 +117,19 @@ template <int BM> __device__ __forceinline__ bool find_tile(const AttnArgs& a, i
   b = uni(lo);
   tile = uni((int)(slot - start(b)));
   return tile >= 0;
+}
+
+// The tile and sequence of a slot; false where there is none.
+template <int BM> __device__ __forceinline__ bool locate(const AttnArgs& a, int slot, Seq& s, int& tile) {
+  if (a.B == 1) {
+    s = load_seq(a, 0);
+    tile = slot - (int)(s.q0 * a.G / BM);
+  } else {
+    int b;
+    if (!find_tile<BM>(a, slot, b, tile)) return false;
+    s = load_seq(a, b);
+  }
+  return tile >= 0 && tile * BM < s.lq * a.G;
 }
 
 // LDS tiles are row-major (DP values a row, in 16-byte chunks) with the chunks of a row permuted by an XOR, so
@@ -186,11 +207,10 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   // one L2 (for 8 key heads; in few for other counts). The last rows, which see the most keys under a causal
   // mask, start first.
   const int kvh = blockIdx.x % a.Hkv, slot = slots - 1 - blockIdx.x / a.Hkv;
-  int b, tile;
-  if (!find_tile<BM>(a, slot, b, tile)) return;
-  const Seq s = load_seq(a, b);
+  int tile;
+  Seq s;
+  if (!locate<BM>(a, slot, s, tile)) return;
   const int nr = s.lq * a.G;  // rows of this sequence and key head
-  if (tile * BM >= nr) return;
 
   // the keys row r sees: 0 .. lim(r) - 1
   auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
@@ -524,11 +544,10 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
   const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
   const int l32 = lane & 31, h = lane >> 5;
   const int kvh = blockIdx.x % a.Hkv, slot = blockIdx.x / a.Hkv;
-  int b, tile;
-  if (!find_tile<FM>(a, slot, b, tile)) return;
-  const Seq s = load_seq(a, b);
+  int tile;
+  Seq s;
+  if (!locate<FM>(a, slot, s, tile)) return;
   const int nr = s.lq * a.G;
-  if (tile * FM >= nr) return;
   auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
   const int r0 = tile * FM, rows = min(nr - r0, FM);
   const int r = min(r0 + l32, nr - 1);
