@@ -531,6 +531,7 @@ template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
 // Measured: 64 caches of 4096 keys on average (32 heads of 128 over 8): 241 us, 5.0 TB/s, a large copy's rate on this card
 // (4.9); one cache of 4000: 7 us here and 3 in the join, both chains of latencies (lengths, keys, LDS, parts).
 constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
+constexpr int kMaxParts = 32;           // workgroups that share a tile's keys
 
 template <int DP, bool SPLIT>
 __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, float* __restrict__ part) {
@@ -736,9 +737,9 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
 
 // o = sum_s w_s part_s, w_s = 2^(lg_s - max) / sum of them: one workgroup per (token, head), 16 bytes a thread,
 // the parts dealt over groups of threads and joined in LDS in a fixed order. A launch this small is a chain of load
-// latencies, so the first kPre parts of a thread set out together with the logarithms their weights need.
+// latencies, so all parts (kMaxParts at most) set out together with the logarithms their weights need.
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __restrict__ part, int splits) {
-  constexpr int kPre = 4;
+  constexpr int kPre = kMaxParts / 8;  // parts a thread: D <= 128 leaves 8 groups or more
   __shared__ float4 acc[256];
   const int Hq = a.Hkv * a.G;
   const int64_t row = blockIdx.x, tok = row / Hq, n = a.Tq * Hq;
@@ -757,12 +758,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __re
   }
   // rows of no sequence have no parts (what was read of them is not used)
   if (tok < bound(a.cu_q, 0, a.Tq) || tok >= bound(a.cu_q, a.B, a.Tq)) return;
-  float M = l0;
-  for (int s = lane + 64; s < splits; s += 64) M = fmaxf(M, lg[s * n]);
-  M = wave_max(M);
+  const float M = wave_max(l0);
   auto power = [&](float l) { return l == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(l - M); };  // (of a NaN: NaN)
   float sum = lane < splits ? power(l0) : 0.0f;
-  for (int s = lane + 64; s < splits; s += 64) sum += power(lg[s * n]);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -775,7 +773,6 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __re
 #pragma unroll
     for (int i = 0; i < kPre; ++i)
       if (g + i * groups < splits) add(lp[i], xp[i]);
-    for (int s = g + kPre * groups; s < splits; s += groups) add(lg[s * n], at(s));
   }
   acc[threadIdx.x] = o;
   __syncthreads();
@@ -794,17 +791,22 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __re
 // Calls whose sequences have 32 rows or fewer on average go to few_kernel.
 inline bool few_rows(int64_t Tq, int64_t B, int64_t G) { return Tq * G <= FM * B; }
 inline int64_t few_slots(int64_t Tq, int64_t B, int64_t G) { return Tq * G / FM + B; }
-// Workgroups per tile: enough for kFill workgroups a CU, with at least two units of 32 keys for every wave if the
-// keys were spread evenly over the sequences.
-constexpr int kFill = 8;
-inline int splits(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv) {
-  const int64_t wgs = few_slots(Tq, B, G) * Hkv, want = (kFill * (int64_t)num_cus_p() + wgs - 1) / wgs;
-  const int64_t most = Tk / B / (FW * 2 * 32);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 256));
+// Workgroups per tile. The chip holds two workgroups a CU (four for heads up to 64), and about as many in all is the
+// best split: one cache of 4096 keys, 32 heads of 128 over 8: 10.4 us in 32 parts, 11.6 in 16, 12.0 in 64; 8 caches of 2048
+// 19.6 in 8, 22.9 in 4, 22.5 in 16; 16 of 2048 29.7 in 4, 35.7 in 2, 31.7 in 8. Where the tiles alone fill it, up to 4 parts
+// of 1024 keys even out lengths: 64 caches of 1 to 8192 keys 213 in 4, 274 whole (all of 8192: 384 / 393). The join costs 3
+// us: below 512 keys a tile stays whole (9.8 in one, 9.7 in 3 at 384), below 1024 where it would be cut in few parts
+// (16 caches of 512: 12.8 whole, 13.5 in 4).
+inline int splits(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv, int64_t D) {
+  const int64_t tiles = std::max<int64_t>(B, Tq * G / FM) * Hkv, keys = Tk / B;
+  int64_t n = std::min<int64_t>((D <= 64 ? 4 : 2) * (int64_t)num_cus_p() / tiles, kMaxParts);
+  if (keys < (n < 8 ? 1024 : 512)) return 1;
+  if (n < 4) n = std::max<int64_t>(n, std::min<int64_t>(keys / 1024, 4));
+  return (int)std::min<int64_t>(n, keys / 64);
 }
 
 template <int DP> hipError_t launch_few(const AttnArgs& a, void* ws, hipStream_t st) {
-  const int n = splits(a.Tq, a.Tk, a.B, a.G, a.Hkv);
+  const int n = splits(a.Tq, a.Tk, a.B, a.G, a.Hkv, a.D);
   const int64_t slots = few_slots(a.Tq, a.B, a.G);
   constexpr int lds = FW * FR * 2 * 32 * DP * 2;
   const dim3 grid((unsigned)(slots * a.Hkv), (unsigned)n);
@@ -826,7 +828,7 @@ template <int DP> hipError_t launch_few(const AttnArgs& a, void* ws, hipStream_t
 int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   const int64_t G = Hq / Hkv;
   if (Tk == 0 || !attn::few_rows(Tq, B, G)) return 0;
-  const int64_t n = attn::splits(Tq, Tk, B, G, Hkv);
+  const int64_t n = attn::splits(Tq, Tk, B, G, Hkv, D);
   return n == 1 ? 0 : n * Tq * Hq * (D + 1) * 4;
 }
 
