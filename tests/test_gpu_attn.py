@@ -93,12 +93,22 @@ def test_many_tiles(ss, Hq, Hkv, lq, lk):
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(2, 2, 64), (3, 1, 40), (2, 1, 128), (1, 1, 96)])
 @pytest.mark.parametrize("lq,lk", [
-    ([100], [1100]), ([1100], [1100]), ([1090], [1025]), ([70, 40], [2100, 63]), ([33, 200, 40], [3200, 0, 1]), ([40], [6000])])
+    ([100], [1100]), ([1100], [1100]), ([1090], [1025]), ([70, 40], [2100, 63]), ([33, 200, 40], [3200, 0, 1]), ([40], [6000]),
+    ([700], [1100]), ([1300, 1, 30], [2100, 1500, 0])])
 @pytest.mark.parametrize("causal", [True, False])
 def test_few_workgroups_split_the_keys(ss, lq, lk, causal, Hq, Hkv, D):
     q, k, v, o, lse = _run(ss, lq, lk, Hq, Hkv, D, causal, seed=D)
     again = torch.empty_like(lse)
     assert torch.equal(ss.attn(q, k, v, _i32(_cum(lq)), _i32(_cum(lk)), causal=causal, lse=again), o) and torch.equal(again, lse)
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [
+    ([100], [6000], 8, 2, 128), ([16], [1030], 32, 8, 64), ([50, 1, 0, 77], [2100, 2500, 900, 4000], 4, 2, 72),
+    ([130], [4100], 7, 1, 128), ([64, 64], [9000, 100], 4, 4, 40)])
+def test_chunks_over_long_caches(ss, lq, lk, Hq, Hkv, D):
+    for causal in (True, False):
+        q, k, v, o, lse = _run(ss, lq, lk, Hq, Hkv, D, causal, seed=D)
+        assert torch.equal(ss.attn(q, k, v, _i32(_cum(lq)), _i32(_cum(lk)), causal=causal), o)
 
 
 def test_many_workgroups_of_long_keys(ss):
