@@ -483,7 +483,7 @@ ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t 
  *   workspace: ss_attn_workspace_bytes bytes (16-byte aligned; NULL where that
  * is 0), as for ss_spgemm_tiled_ws: no initialisation, undefined afterwards,
  * calls that share one must be stream-ordered. It serves calls with few query
- * rows per sequence (single tokens over a cache), which split the keys over
+ * rows per sequence (single tokens, or short chunks over a long cache), which split the keys over
  * workgroups and join the parts in a fixed order in a second kernel. */
 int64_t ss_attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,

@@ -528,8 +528,9 @@ template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
 // ring of its own in LDS (whole 1 KB DMA loads, no barrier in the loop: a wave waits for its own loads only),
 // and gridDim.y workgroups share a tile's keys. The waves of a workgroup join through LDS, the workgroups through
 // float32 parts (each normalised, with its row's log2 of the sum) that join_kernel adds in order.
-// Measured: 64 caches of 4096 keys on average (32 heads of 128 over 8): 241 us, 5.0 TB/s, a large copy's rate on this card
-// (4.9); one cache of 4000: 7 us here and 3 in the join, both chains of latencies (lengths, keys, LDS, parts).
+// Measured: 64 caches of 4096 keys on average (32 heads of 128 over 8): 240 us, 5.0 TB/s, a large copy's rate on this card
+// (4.9); one cache of 4000: 6.5 us here and 3 in the join, both chains of latencies (lengths, keys, LDS, parts).
+// Short chunks of tokens over a long cache come here too, several tiles of 32 rows to a sequence (few_rows).
 constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
 constexpr int kMaxParts = 32;           // workgroups that share a tile's keys
 
@@ -612,26 +613,6 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
     const SS_LDS uint8_t* vt = kt + KB;
     const int vo = at + KB;
     at = RING / FR - at;
-    if (kmin < kend && u * 32 + 32 > kmin) {  // rows that see different keys of this unit
-      uint32_t odd = 0;
-#pragma unroll
-      for (int i = 0; i < LPU; ++i) {
-        const v4u w = *reinterpret_cast<const SS_LDS v4u*>(vt + (i * 64 + lane) * 16);
-        odd |= odd_bf16x2(w[0]) | odd_bf16x2(w[1]) | odd_bf16x2(w[2]) | odd_bf16x2(w[3]);
-      }
-      if (__builtin_expect(__any(odd != 0), 0)) {
-        add_odd<DP>(O, vt, row_lim - u * 32, h);
-#pragma unroll 1
-        for (int i = 0; i < LPU; ++i) {
-          SS_LDS v4u* p = (SS_LDS v4u*)(ring + vo + (i * 64 + lane) * 16);
-          const v4u w = *p;
-          *p = v4u{even_out(w[0]), even_out(w[1]), even_out(w[2]), even_out(w[3])};
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        asm volatile("" ::: "memory");  // the reads below stay below
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
     v16f S = v16f{};
 #pragma unroll
     for (int i = 0; i < KST; ++i) {
@@ -655,6 +636,26 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
+    }
+    if (kmin < kend && u * 32 + 32 > kmin) {  // rows that see different keys of this unit
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < LPU; ++i) {
+        const v4u w = *reinterpret_cast<const SS_LDS v4u*>(vt + (i * 64 + lane) * 16);
+        odd |= odd_bf16x2(w[0]) | odd_bf16x2(w[1]) | odd_bf16x2(w[2]) | odd_bf16x2(w[3]);
+      }
+      if (__builtin_expect(__any(odd != 0), 0)) {
+        add_odd<DP>(O, vt, row_lim - u * 32, h);
+#pragma unroll 1
+        for (int i = 0; i < LPU; ++i) {
+          SS_LDS v4u* p = (SS_LDS v4u*)(ring + vo + (i * 64 + lane) * 16);
+          const v4u w = *p;
+          *p = v4u{even_out(w[0]), even_out(w[1]), even_out(w[2]), even_out(w[3])};
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        asm volatile("" ::: "memory");  // the reads below stay below
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     v8bf P[2];
     {
@@ -788,8 +789,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, const float* __re
     a.lse[head * a.Tq + tok] = sum == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.69314718056f;
 }
 
-// Calls whose sequences have 32 rows or fewer on average go to few_kernel.
-inline bool few_rows(int64_t Tq, int64_t B, int64_t G) { return Tq * G <= FM * B; }
+// Calls whose sequences have 32 rows or fewer on average go to few_kernel, and those whose tiles of 32 rows are few beside
+// the keys (128 at most, and 40 keys or more for each): a chunk of tokens over a long cache, where the tiles of 128 rows would
+// leave the chip idle. 16 tokens, 32 heads of 128 over 8 (16 tiles): 14.9 against 18.4 us over 1024 keys, 23.3 / 47.5 over
+// 4096; 128 tokens (128 tiles): 24.0 / 20.1 over 1024, 36.2 / 49.6 over 4096, 78.9 / 170 over 16384; 4 chunks of 64 rows, 28
+// heads over 4 (32 tiles): 22.0 / 18.7 over 1024, 24.8 / 28.7 over 2048.
+inline bool few_rows(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv) {
+  const int64_t tiles = (Tq * G + (FM - 1) * B) / FM * Hkv;
+  return Tk > 0 && (Tq * G <= FM * B || (tiles <= 128 && tiles <= Tk / B / 40));
+}
 inline int64_t few_slots(int64_t Tq, int64_t B, int64_t G) { return Tq * G / FM + B; }
 // Workgroups per tile. The chip holds two workgroups a CU (four for heads up to 64), and about as many in all is the
 // best split: one cache of 4096 keys, 32 heads of 128 over 8: 10.4 us in 32 parts, 11.6 in 16, 12.0 in 64; 8 caches of 2048
@@ -827,19 +835,19 @@ template <int DP> hipError_t launch_few(const AttnArgs& a, void* ws, hipStream_t
 
 int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   const int64_t G = Hq / Hkv;
-  if (Tk == 0 || !attn::few_rows(Tq, B, G)) return 0;
+  if (!attn::few_rows(Tq, Tk, B, G, Hkv)) return 0;
   const int64_t n = attn::splits(Tq, Tk, B, G, Hkv, D);
   return n == 1 ? 0 : n * Tq * Hq * (D + 1) * 4;
 }
 
 // a launch holds fewer than 2^32 threads
 bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv) {
-  const int64_t G = Hq / Hkv, few = Tk > 0 && attn::few_rows(Tq, B, G);
+  const int64_t G = Hq / Hkv, few = attn::few_rows(Tq, Tk, B, G, Hkv);
   return (few ? attn::few_slots(Tq, B, G) * 64 * attn::FW : (Tq * G / attn::BM + B) * 64 * attn::NW) * Hkv <= 0xFFFFFFFFLL;
 }
 
 hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {
-  if (a.Tk > 0 && attn::few_rows(a.Tq, a.B, a.G)) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
+  if (attn::few_rows(a.Tq, a.Tk, a.B, a.G, a.Hkv)) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
   return a.D <= 64 ? attn::launch_prompt<64>(a, st) : attn::launch_prompt<128>(a, st);
 }
 
