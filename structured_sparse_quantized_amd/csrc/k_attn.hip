@@ -180,9 +180,9 @@ __device__ __forceinline__ void renew(uint32_t& x) { asm volatile("" : "+v"(x));
 //   that waits for them out of every stage (1-3% for heads of 128, 6% for 64); the first stage's maximum is found ahead.
 // So the matrix instructions have vector work of about the same length beside them that does not wait for
 // them, and fragments are read a stage ahead of their use.
-// Measured: one prompt of 8192 tokens, 32 heads of 128 over 8, causal: 485 us, 1.13 PFLOP/s of the seen pairs (matrix cores
+// Measured: one prompt of 8192 tokens, 32 heads of 128 over 8, causal: 475 us, 1.16 PFLOP/s of the seen pairs (matrix cores
 // busy 65% of the cycles, at the 1.8 GHz the card keeps under this load; its large bf16 product runs at 1.37); 9 packed
-// prompts, 8001 tokens, 28 heads over 4: 86 us, 0.69 PFLOP/s. What bounds it is the vector work beside the matrix
+// prompts, 8001 tokens, 28 heads over 4: 85 us, 0.70 PFLOP/s. What bounds it is the vector work beside the matrix
 // instructions, some 60 instructions per 16 scores a lane (the 16 powers at a quarter of the rate), about as long as
 // the products themselves. Tried and not kept: 64 rows a wave (608 us for the first prompt, when this form took 537,
 // the accumulators crowd the registers), 8 waves on one tile (561), stages not merged (557), deeper rings, the two
