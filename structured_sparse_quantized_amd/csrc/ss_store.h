@@ -254,42 +254,48 @@ struct Leave {
 };
 
 // The same for rows that do not start on 16 bytes: a lane per column, so that a wave's loads and stores are runs of
-// adjacent elements, and narrow rows side by side over the 64 lanes; 4 rows a lane at a time, their residuals fetched before
-// the first store (a pass costs about a load's latency). COLS staged channels a row, a power of two.
+// adjacent elements, and narrow rows side by side over the 64 lanes; 4 rows a lane at a time, the residuals of the next 4
+// on their way while these are finished. (Pieces of 16 bytes from where each row first meets one measured 20-50% slower:
+// every wave has ends of rows, which go by elements, in every step.) COLS staged channels a row, a power of two.
 template <int COLS>
 __device__ __forceinline__ void leave_columns(const float* stg, int ld, int rows, int64_t tok0, int64_t ntok, int ch0, int nch,
                                               void* Y, int64_t ldy, const Epilogue& e) {
   const int lane = threadIdx.x & 63, wide = COLS >> e.gated, col0 = ch0 >> e.gated, ncol = nch >> e.gated;
   const int have = (int)min((int64_t)rows, ntok - tok0);  // rows of Y
   const int beside = wide < 64 ? 64 / wide : 1, first = lane / wide;  // rows next to each other, and this lane's first
+  const int es = e.f32 ? 4 : 2, shift = e.f32 ? 0 : 16;
 #pragma unroll 1
   for (int c = lane & (min(wide, 64) - 1); c < wide; c += 64) {
     if (col0 + c >= ncol) break;
     const int at = c << e.gated;
     const float b0 = e.bias ? e.bias[ch0 + at] : 0.0f, b1 = e.bias && e.gated ? e.bias[ch0 + at + 1] : 0.0f;
+    const uint8_t* rp = static_cast<const uint8_t*>(e.res) + (tok0 * e.ldr + col0 + c) * es;
+    uint8_t* yp = static_cast<uint8_t*>(Y) + (tok0 * ldy + col0 + c) * es;
+    const int64_t rstep = e.ldr * es, ystep = ldy * es;
+    uint32_t next[4] = {0, 0, 0, 0};  // residuals as they lie in memory
+    auto fetch = [&](int r) __attribute__((always_inline)) {  // the type's branch outside, so the four are in flight together
+      if (e.res && e.f32) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) next[x] = *reinterpret_cast<const uint32_t*>(rp + min(r + x * beside, have - 1) * rstep);
+      }
+      if (e.res && !e.f32) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) next[x] = *reinterpret_cast<const uint16_t*>(rp + min(r + x * beside, have - 1) * rstep);
+      }
+    };
+    fetch(first);
 #pragma unroll 1
     for (int r = first; r < have; r += 4 * beside) {
-      float res[4] = {0, 0, 0, 0}, z[4], up[4];
-      auto fetch = [&](auto f32) __attribute__((always_inline)) {  // the type's branch outside, so the four are in flight together
-        Epilogue of = e;
-        of.f32 = decltype(f32)::value;
+      uint32_t res[4];
+      float z[4], up[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) res[x] = load_res(of, (tok0 + min(r + x * beside, have - 1)) * e.ldr + col0 + c);
-      };
-      if (e.res && e.f32) fetch(std::true_type{});
-      if (e.res && !e.f32) fetch(std::false_type{});
+      for (int x = 0; x < 4; ++x) res[x] = next[x];
+      fetch(r + 4 * beside);  // (behind the last row: the last one again)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int row = min(r + x * beside, have - 1);
-        z[x] = stg[row * ld + at];
-        up[x] = e.gated ? stg[row * ld + at + 1] : 1.0f;
-      }
-      if (e.bias) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          z[x] += b0;
-          if (e.gated) up[x] += b1;
-        }
+        const float* p = stg + min(r + x * beside, have - 1) * ld + at;
+        z[x] = p[0] + b0;
+        up[x] = p[e.gated] + b1;
       }
       activate_n<4>(z, e.act, e.f32);
 #pragma unroll
@@ -297,8 +303,9 @@ __device__ __forceinline__ void leave_columns(const float* stg, int ld, int rows
         const int row = r + x * beside;
         if (row >= have) break;
         float v = e.gated ? z[x] * up[x] : z[x];
-        if (e.res) v += res[x];
-        store_one(Y, (tok0 + row) * ldy + col0 + c, v, e.f32);
+        if (e.res) v += __uint_as_float(res[x] << shift);
+        if (e.f32) *reinterpret_cast<float*>(yp + row * ystep) = v;
+        else *reinterpret_cast<uint16_t*>(yp + row * ystep) = (uint16_t)pack_bf16x2(v, 0.0f);
       }
     }
   }
