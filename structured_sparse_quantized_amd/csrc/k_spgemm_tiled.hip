@@ -1200,17 +1200,18 @@ static int wide_bn(bool side_x, int64_t R, int64_t C, int64_t KS, int64_t ldb_by
 // kernel (FP8, 4096 x 4096): 9.0 against 20.8 us at 128 tokens, 12.0 / 20.9 at 256, 17.0 / 22.1 at 512, where the next
 // width down takes 17.7; at 768 tokens (more than 256 tiles of any width, 25.5 / 23.1) the large tiles win. At two per CU:
 // 28672 x 4096, 48 and 64 tokens, 18.1 / 22.6 and 18.8 / 24.0 against the split reduction; 128 tokens, 448 tiles of width
-// 128, 31.2 / 24.1, so that width stops at one per CU. Where a workspace allows the split reduction (17 to 64 tokens), small
+// 128, 31.2 / 24.1, so that width stops at one per CU. Reductions of up to 8 steps take width 64 at three per CU: 3000
+// tokens, 1024 rows (752 tiles) 12.8 / 15.9 us at 2 steps, 14.4 / 17.4 at 8, 21.2 / 20.4 at 16. Where a workspace allows the split reduction (17 to 64 tokens), small
 // tiles take reductions of up to 48 steps: at 4096 x 4096 (32 steps) 8.6-8.8 / 9.4-12.2 us, at 512 x 8192 (64) 13.2 / 11.1-12.3,
 // at 4096 x 14336 (112) 21 / 14.2-17.7. From 9 tokens on, where 64-row tiles fill three quarters of the CUs by themselves, they
 // take every reduction: 28672 x 4096 15.4 against 17.4 us of the row-block kernel at 10 tokens, 15.2 / 20.7 at 16;
 // 14336 x 8192 16.5 / 20.7 at 24; at 8 tokens 15.0 / 16.3 and 9.0 / 8.1 (12288 x 4096), at 4 tokens 15.0 / 14.4.
-static int small_tj(int64_t R, int64_t C) {
+static int small_tj(int64_t R, int64_t C, int64_t KS) {
   const int64_t cus = num_cus_p(), tr = (R + 63) / 64;
   auto tiles = [&](int tj) { return tr * ((C + 32 * tj - 1) / (32 * tj)); };
   for (int tj = 1; tj <= 4; tj *= 2)
     if (tiles(tj) <= cus) return tj;
-  return tiles(1) <= 2 * cus ? 1 : tiles(2) <= 2 * cus ? 2 : 0;
+  return tiles(1) <= 2 * cus ? 1 : tiles(2) <= (KS <= 8 ? 3 : 2) * cus ? 2 : 0;
 }
 // The split-K path (with a workspace) serves the few-token products with more than 16 tokens.
 static bool use_splitk(bool side_x, int64_t R, int64_t C) { return few_tokens(side_x, R, C) && C > 16; }
@@ -1301,7 +1302,7 @@ hipError_t launch_spgemm_tiled(bool side_x, int ab, int yt, int64_t R, int64_t C
   const bool dec = few_tokens(side_x, R, C);
   const bool spk = ws != nullptr && use_splitk(side_x, R, C);
   const bool fills = dec && C > 8 && 4 * ((R + 63) / 64) > 3 * num_cus_p();
-  const int tj = yt == 3 && (!dec || fills || (spk && ks <= 48)) ? small_tj(R, C) : 0;
+  const int tj = yt == 3 && (!dec || fills || (spk && ks <= 48)) ? small_tj(R, C, ks) : 0;
   if (tj) return launch_spgemm_small(tj, side_x, ab, r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, ep, st);
   const int bn = spk || dec ? 0 : wide_bn(side_x, R, C, ks, ldb_bytes);
   if (bn) return launch_spgemm_wide(bn, side_x, ab, yt, r, c, ks, tv, tm, b, lb, sx, sw, Y, ly, ep, st);

@@ -146,6 +146,7 @@ def test_prefill(ss, side, q, M, N, K):
     ("W", "i8", 400, 4097, 256), ("W", "fp8", 385, 3970, 640), ("W", "bf16", 1000, 2044, 256),  # 128
     ("X", "i8", 500, 1001, 600), ("X", "fp8", 1500, 333, 256), ("X", "bf16", 777, 900, 500),
     ("X", "i8", 1030, 990, 256), ("X", "fp8", 1100, 1601, 256), ("X", "bf16", 2047, 250, 256),
+    ("W", "fp8", 2999, 1030, 256), ("X", "i8", 1100, 2600, 500),  # three of width 64 a CU
     ("W", "i8", 10, 16390, 256), ("W", "fp8", 16, 12290, 256), ("W", "bf16", 64, 16450, 128), ("W", "fp8", 30, 20001, 512)])
 def test_small_tiles(ss, side, q, M, N, K):
     p = Problem(ss, side, q, M, N, K, seed=N)
