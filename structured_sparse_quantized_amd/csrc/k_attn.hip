@@ -140,9 +140,10 @@ template <int DP> struct Lds {
   __device__ static int swv(int row) { return DP >= 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
 };
 
-// A causal mask gives the rows of a tile different keys, but one product takes them all: a power of zero keeps a finite
-// value of an unseen key out of a row, not an infinity or a NaN. Where a tile's values hold one, it is replaced by zero
-// in the operand and added to the rows that see it by hand (its power is above zero, so the sum is v itself).
+// Under a causal mask a tile's keys go past what some of its rows see, or all of them (rows of one token, with 32 query heads
+// and more to a key head: a tile is loaded up to the sequence's last key), and one product takes them all: a power of
+// zero keeps a finite value of an unseen key out of a row, not an infinity or a NaN. Where a tile's values hold one, it is
+// replaced by zero in the operand and added to the rows that see it by hand (its power is above zero, so the sum is v itself).
 __device__ __forceinline__ uint32_t odd_bf16x2(uint32_t w) {  // bits 31, 15: that half is infinite or NaN
   return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
@@ -352,7 +353,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     P[1] = __builtin_bit_cast(v8bf, pk[1]);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (decltype(maskc)::value) {
-      if (wmin < wmax && first + 32 > wmin) {
+      if (wmin < s.lk && first + 32 > wmin) {  // keys were loaded that some row does not see (its rows may be one token's)
         uint32_t odd = 0;
 #pragma unroll
         for (int j = 0; j < 2 * DB; ++j) {
@@ -637,7 +638,7 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
     }
-    if (kmin < kend && u * 32 + 32 > kmin) {  // rows that see different keys of this unit
+    if (kmin < s.lk && u * 32 + 32 > kmin) {  // keys were loaded that some row does not see (the rows may be one token's)
       uint32_t odd = 0;
 #pragma unroll
       for (int i = 0; i < LPU; ++i) {
