@@ -475,7 +475,8 @@ ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t 
  * row that sees no key gives zeros (and lse -inf). Query rows in no sequence
  * leave o and lse untouched; key rows in no sequence or behind k_len are never
  * part of a result, whatever they hold; a NaN or an infinity in a key row that
- * only some rows see reaches those alone. Heads of o must not overlap.
+ * only some rows see reaches those alone. Scores are float32, of any finite size (scale log2 e q . k within
+ * float32's range); a score of -inf counts as a key not seen. Heads of o must not overlap, nor o an input.
  *   lse: NULL, or [Hq][Tq] floats that receive the natural logarithm of each
  * row's sum of exp(scale * q . k).
  *   8 <= D <= 128, D % 8 == 0 (SS_ERR_UNSUPPORTED otherwise), Hq % Hkv == 0, scale finite and

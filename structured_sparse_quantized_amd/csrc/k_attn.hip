@@ -42,7 +42,12 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr float kSlack = 8.0f;     // in powers of two
 constexpr float kRise = 256.0f;
 constexpr int vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }  // s_waitcnt vmcnt(n)
-constexpr float kLow = -1.0e30f;   // below every finite score's exponent; 2^(kLow - m) = 0
+constexpr float kLow = -3.402823466e38f;  // below every finite score's exponent, and finite: kLow - kLow = 0
+// From this size of a maximum m on, the power's argument is the rounded product c s less m. Below it both come out of one
+// fused step, whose exact product may pass the rounded maximum by half of a unit of m's last place: 2^7 at 2^31, a power that
+// overflows (or, below m, a largest score whose power is 0).
+constexpr float kBig = 16777216.0f;  // 2^24
+__device__ __forceinline__ bool is_big(float m) { return m != kLow && fabsf(m) >= kBig; }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
@@ -280,6 +285,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   v16f O[DB], S0, S1;
   v8bf kf[KST], vf[2][DB], P[2];
   float m = kLow, l = 0.0f;
+  float rise = kRise;  // below any sum while a row's maximum is big: every stage then takes its powers the careful way
 #pragma unroll
   for (int d = 0; d < DB; ++d) {
     O[d] = v16f{};
@@ -328,7 +334,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
       pk[i / 4][i % 4] = pack_bf16x2(x, y);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (__builtin_expect(__any(sum > kRise), 0)) {
+    if (__builtin_expect(__any(sum > rise), 0)) {
       float mt = cur[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) mt = fmaxf(mt, cur[i]);
@@ -339,11 +345,14 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
+      const bool big = is_big(m);
+      rise = __any(big) ? -1.0f : kRise;
       sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i], a.c, -m));
-        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(cur[2 * i + 1], a.c, -m));
+        const float s0 = cur[2 * i], s1 = cur[2 * i + 1];
+        const float x = __builtin_amdgcn_exp2f(big ? s0 * a.c - m : __builtin_fmaf(s0, a.c, -m));
+        const float y = __builtin_amdgcn_exp2f(big ? s1 * a.c - m : __builtin_fmaf(s1, a.c, -m));
         sum += x + y;
         pk[i / 4][i % 4] = pack_bf16x2(x, y);
       }
@@ -404,6 +413,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     for (int i = 0; i < 16; ++i)
       if (8 * (i / 4) + i % 4 < left) mt = fmaxf(mt, S0[i]);
     m = fmaxf(m, ceilf(pair_max(mt) * a.c));
+    rise = __any(is_big(m)) ? -1.0f : kRise;
   }
   auto turn = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
@@ -528,7 +538,8 @@ template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
 // along the keys: a tile has 32 rows, each wave takes every FW-th unit of 32 keys of its workgroup's share with a
 // ring of its own in LDS (whole 1 KB DMA loads, no barrier in the loop: a wave waits for its own loads only),
 // and gridDim.y workgroups share a tile's keys. The waves of a workgroup join through LDS, the workgroups through
-// float32 parts (each normalised, with its row's log2 of the sum) that join_kernel adds in order.
+// float32 parts (each normalised, with its row's log2 of the sum: maximum and sum in one float, exact to 2^-24 of the
+// maximum, as the scores themselves are) that join_kernel adds in order.
 // Measured: 64 caches of 4096 keys on average (32 heads of 128 over 8): 240 us, 5.0 TB/s, a large copy's rate on this card
 // (4.9); one cache of 4000: 6.5 us here and 3 in the join, both chains of latencies (lengths, keys, LDS, parts).
 // Short chunks of tokens over a long cache come here too, several tiles of 32 rows to a sequence (few_rows).
@@ -598,6 +609,7 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
 #pragma unroll
   for (int d = 0; d < DB; ++d) O[d] = v16f{};
   float m = kLow, l = 0.0f;
+  bool careful = false;  // some row's maximum is big
   const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
 
   int at = 0;
@@ -637,6 +649,13 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
+      careful = __any(is_big(m));
+    }
+    float pc = a.c, pm = m;  // a power is 2^(pc S - pm)
+    if (__builtin_expect(careful, 0)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[i] = S[i] * a.c - m;
+      pc = 1.0f, pm = 0.0f;
     }
     if (kmin < s.lk && u * 32 + 32 > kmin) {  // keys were loaded that some row does not see (the rows may be one token's)
       uint32_t odd = 0;
@@ -664,8 +683,8 @@ __global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, 
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i], a.c, -m));
-        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i + 1], a.c, -m));
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i], pc, -pm));
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i + 1], pc, -pm));
         sum += x + y;
         pk[i / 8][(i % 8) / 2] = pack_bf16x2(x, y);
       }

@@ -1,9 +1,11 @@
-"""ss_attn where a tile's rows share one token (32 query heads and more to a key head), for every form of the kernels:
-tiles of many rows, the keys in two parts, few rows in one workgroup and in several."""
+"""ss_attn where a tile's rows share one token (32 query heads and more to a key head) and where scores are large, for
+every form of the kernels: tiles of many rows, the keys in two parts, few rows in one workgroup and in several."""
+import numpy as np
 import pytest
 import torch
 
 from helpers import have_gpu
+from oracle.attention import attention
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
 
@@ -45,3 +47,54 @@ def test_infinities_and_nan_with_a_token_per_tile(ss, lq, lk, D, G):
         o = ss.attn(q, kb, v, lse=lse_k)
         assert torch.equal(o[~rows], clean[~rows]) and torch.equal(lse_k[:, ~rows], lse[:, ~rows])
         assert o[rows].isnan().all() and lse_k[:, rows].isnan().all()
+
+
+@pytest.mark.parametrize("top", [34, 60, 110, 121])
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [
+    (200, 333, 2, 1, 128), (90, 200, 3, 1, 64),  # tiles of many rows
+    (700, 900, 2, 2, 64), (600, 1100, 2, 2, 128),  # the keys in two parts
+    (6, 500, 4, 1, 128), (40, 2000, 2, 1, 64),  # few rows, one workgroup and several
+    (4, 5000, 7, 1, 72)])
+def test_finite_scores_of_any_size(ss, lq, lk, Hq, Hkv, D, top):
+    """Scores of up to 2^top, so far apart that a row is the value of its largest score, exactly. The scores are
+    exact: only the first value of q and k is not zero, q a power of two, k of 8 bits: 512 different values within 4
+    powers of two, the other keys alike at the end that loses. The closest two, scaled, are 2^(top - 11) / sqrt(D) apart,
+    2^19 or more, whose power is zero. With q > 0 the largest of large scores wins, with q < 0 the least far of
+    scores that are all far below zero. The logarithm: the scale, its product with log2 e, the maximum and its product
+    with ln 2 round by 2^-24 each, and so do the two constants."""
+    rng = np.random.default_rng(lk + D)
+    steps = np.array([(1 + m / 128) * 2.0 ** e for e in range(4) for m in range(128)])
+    seen = np.arange(lk)[None, :] <= (np.arange(lq) + lk - lq)[:, None]
+    for sign in (1.0, -1.0):
+        b = np.full(lk, 1.0 if sign > 0 else 16.0)
+        own = rng.permutation(lk)[: min(512, lk)]
+        b[own] = rng.permutation(steps)[: len(own)]
+        q, k = np.zeros((lq, Hq, D)), np.zeros((lk, Hkv, D))
+        q[:, :, 0] = sign * 2.0 ** (top // 2)
+        k[:, :, 0] = (b * 2.0 ** (top - 4 - top // 2))[:, None]
+        s = np.where(seen, q[:, :1, 0] * k[:, 0, 0], -np.inf)
+        assert ((s == s.max(1)[:, None]).sum(1) == 1).all()
+        qt, kt = (torch.from_numpy(x).to("cuda", torch.bfloat16) for x in (q, k))
+        v = torch.from_numpy(rng.standard_normal((lk, Hkv, D))).to("cuda", torch.bfloat16)
+        lse = torch.empty((Hq, lq), device="cuda")
+        o = ss.attn(qt, kt, v, lse=lse)
+        assert torch.equal(o, v[torch.from_numpy(s.argmax(1)).cuda()].repeat_interleave(Hq // Hkv, 1))
+        ref = s.max(1) * D ** -0.5
+        assert (np.abs(lse.double().cpu().numpy() - ref) <= np.abs(ref) * 6.1 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [(200, 333, 2, 1, 128), (700, 900, 2, 2, 64), (600, 1100, 2, 2, 128), (6, 500, 4, 1, 128), (4, 5000, 7, 1, 72)])
+def test_ordinary_rows_beside_large_scores(ss, lq, lk, Hq, Hkv, D):
+    """Every second token's scores are 2^40 times the others', in the same tiles. Tolerance of the others as in
+    test_gpu_attn.py: scores to 4e-5 of their magnitudes, probabilities and outputs rounded by 2^-8."""
+    g = torch.Generator(device="cuda").manual_seed(lk)
+    q = torch.randn((lq, Hq, D), generator=g, device="cuda")
+    q[0::2] *= 2.0 ** 40
+    q = q.to(torch.bfloat16)
+    k, v = (torch.randn((lk, Hkv, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    o = ss.attn(q, k, v).double().cpu().numpy()
+    assert np.isfinite(o).all() and (np.abs(o) <= float(v.abs().max())).all()
+    eo, _, mass, size = attention(*(t.float().cpu().numpy() for t in (q, k, v)), [0, lq], [0, lk])
+    tol = mass * (2.0 ** -8 + size.T[:, :, None] * 8e-5 + 6e-5)
+    tol = tol + 2.0 ** -8 * (np.abs(eo) + tol)
+    assert (np.abs(o - eo) <= tol)[1::2].all()
