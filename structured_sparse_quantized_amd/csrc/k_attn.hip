@@ -826,6 +826,7 @@ inline int64_t few_slots(int64_t Tq, int64_t B, int64_t G) { return Tq * G / FM 
 // us: below 512 keys a tile stays whole (9.8 in one, 9.7 in 3 at 384), below 1024 where it would be cut in few parts
 // (16 caches of 512: 12.8 whole, 13.5 in 4).
 inline int splits(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv, int64_t D) {
+  if (Tq * G * Hkv >= 1 << 24) return 1;  // join_kernel: 256 threads a row, fewer than 2^32 in a launch
   const int64_t tiles = std::max<int64_t>(B, Tq * G / FM) * Hkv, keys = Tk / B;
   int64_t n = std::min<int64_t>((D <= 64 ? 4 : 2) * (int64_t)num_cus_p() / tiles, kMaxParts);
   if (keys < (n < 8 ? 1024 : 512)) return 1;

@@ -98,3 +98,13 @@ def test_ordinary_rows_beside_large_scores(ss, lq, lk, Hq, Hkv, D):
     tol = mass * (2.0 ** -8 + size.T[:, :, None] * 8e-5 + 6e-5)
     tol = tol + 2.0 ** -8 * (np.abs(eo) + tol)
     assert (np.abs(o - eo) <= tol)[1::2].all()
+
+
+def test_more_rows_than_a_join_can_hold(ss):
+    """2^24 (token, head) rows over sequences long enough to be split: equal keys (stride 0), so the values come back."""
+    B, Hq, Hkv, D, n = 65536, 256, 8, 8, 2048
+    q = torch.randn((B, Hq, D), device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn((1, Hkv, D), device="cuda").to(torch.bfloat16).expand(B * n, Hkv, D) for _ in range(2))
+    cq = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    o = ss.attn(q, k, v, cq, cq * n)
+    assert torch.equal(o, v[:1].repeat_interleave(Hq // Hkv, 1).expand(B, Hq, D))
