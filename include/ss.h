@@ -275,15 +275,17 @@ ss_status ss_spgemm_tiled_ws(ss_side side, int64_t M, int64_t N, int64_t Kc, ss_
  * may be Y itself with ldr = ldy, and must not overlap Y otherwise. gated != 0
  * makes Y [M][N / 2] (N even): weight rows 2j and 2j + 1 hold the gate and the
  * value of column j (a caller interleaves the two matrices before the weight
- * preparation). Exponentials, where y_dt is BF16, are the chip's own (relative
- * error below 2^-19 for |z| < 16) and erf is good to 1.5e-7 absolute. A NaN of z
- * stays a NaN under every activation.
+ * preparation). Activations are good relative to their values: where y_dt is
+ * BF16, exponentials are the chip's own (2^-19 + |u| 2^-22, u the exponent: z, or
+ * 1.6 (z + 0.045 z^3) for GELU_TANH) and GELU's normal integral is good to 2^-16 +
+ * z^2 2^-22; values below about 2^-120 may come out as zero. A NaN of z stays a NaN
+ * under every activation.
  * Sides, operands, scales (both for I8 and FP8E4M3), workspace and errors as
  * ss_spgemm_tiled_ws; the workspace query is the same. */
 typedef enum {
   SS_ACT_NONE = 0,
   SS_ACT_RELU = 1,      /* max(z, 0) */
-  SS_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) */
+  SS_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) = z/2 erfc(-z / sqrt 2) */
   SS_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
   SS_ACT_SILU = 4       /* z / (1 + exp(-z)) */
 } ss_act;

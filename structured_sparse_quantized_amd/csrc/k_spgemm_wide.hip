@@ -426,8 +426,8 @@ __global__ __launch_bounds__(64 * W, occupancy<BN>()) void wide_kernel(
           // own lanes (4 channels of one token each; column by column of the tile, so that the activations stay
           // short unrolled runs), then rows of bf16 through the idle ring as below. The residuals of a column are
           // on their way while the column is finished.
-          // 4096 tokens, 28672 x 4096, FP8: 267 us without extras (the plain product 260-275), 269 with bias, 277 silu, 283
-          // gelu_tanh, 312 gelu (the whole erf), 302 residual (112 MB to read); gated 246, gated silu 255, for half the
+          // 4096 tokens, 28672 x 4096, FP8: 251 us without extras (the plain product 252), 254 with bias, 261 silu, 267
+          // gelu_tanh, 290 gelu, 291 residual (112 MB to read); gated 233, gated silu 239, gated gelu 253, for half the
           // output bytes.
           constexpr int STRIDE = 128 * 2 + 16;
           constexpr int UP = up_rows(TJ, META / NW / (16 * STRIDE)), NP = TJ / UP, RP = 16 * UP;
