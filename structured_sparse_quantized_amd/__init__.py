@@ -43,9 +43,16 @@ if not os.path.exists(_LIB_PATH):
 lib = ctypes.CDLL(_LIB_PATH)
 try:
     from . import _ssbind  # argument checks and marshalling of the calls between products (csrc/ss_bind.cpp)
-except ImportError as e:
-    raise ImportError(f"the binding _ssbind.so next to {_LIB_PATH} does not load ({e}): build it with "
-                      "structured_sparse_quantized_amd.build.build()") from e
+except ImportError as _e:  # built against one Python and one torch; the other calls go through ctypes alone
+    class _NoBinding:
+        def __init__(self, why):
+            self._why = why
+
+        def __getattr__(self, name):
+            raise ImportError(f"{name} needs the binding _ssbind.so, which does not load ({self._why}): build it with "
+                              "structured_sparse_quantized_amd.build.build()")
+
+    _ssbind = _NoBinding(_e)
 
 SS_OK, SS_ERR_NULL, SS_ERR_SHAPE, SS_ERR_ALIGN, SS_ERR_DTYPE, SS_ERR_PATTERN, SS_ERR_UNSUPPORTED, SS_ERR_HIP = range(8)
 SS_F32, SS_BF16, SS_I8, SS_FP8E4M3, SS_I32 = range(5)
@@ -124,7 +131,8 @@ class SSError(RuntimeError):
         super().__init__(f"{msg}: {detail}")
 
 
-_ssbind.set_error(SSError)
+if not hasattr(_ssbind, "_why"):
+    _ssbind.set_error(SSError)
 
 
 # Size checks made before a call reaches the C ABI: the library validates sizes, strides and alignment, but
