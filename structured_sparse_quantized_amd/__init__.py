@@ -410,7 +410,8 @@ def spgemm_tiled_epilogue(side: int, M: int, N: int, Kc: int, tvals: torch.Tenso
     """spgemm_tiled followed by + bias [N] (f32), the activation ("none", "relu", "gelu", "gelu_tanh", "silu") and
     + residual, all in the product's epilogue and rounded once. gated: weight rows 2j and 2j + 1 are the gate and
     the value of column j, y[:, j] = act(z[:, 2j]) * z[:, 2j + 1], so Y and residual are [M, N / 2]. residual has
-    the type of Y (bf16 or f32) and may be `out` itself. workspace: as spgemm_tiled (None takes one where needed)."""
+    the type of Y (bf16 or f32) and may be `out` itself. workspace: spgemm_tiled_workspace_bytes bytes, or None, which
+    takes one where it is needed (there is no form without, as spgemm_tiled has)."""
     code = ACTIVATIONS.get(act)
     if code is None:
         raise SSError(SS_ERR_UNSUPPORTED, f"act {act!r}: one of {', '.join(ACTIVATIONS)}")
