@@ -547,7 +547,7 @@ constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
 constexpr int kMaxParts = 32;           // workgroups that share a tile's keys
 
 template <int DP, bool SPLIT>
-__global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, int slots, float* __restrict__ part) {
+__global__ __launch_bounds__(64 * FW, 2) void few_kernel(AttnArgs a, float* __restrict__ part) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;
   constexpr int KB = 32 * DP * 2, UNIT = 2 * KB, RING = FR * UNIT;
   constexpr int LPU = KB / 1024;            // 1 KB loads per unit and operand
@@ -836,13 +836,12 @@ inline int splits(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv, int
 
 template <int DP> hipError_t launch_few(const AttnArgs& a, void* ws, hipStream_t st) {
   const int n = splits(a.Tq, a.Tk, a.B, a.G, a.Hkv, a.D);
-  const int64_t slots = few_slots(a.Tq, a.B, a.G);
   constexpr int lds = FW * FR * 2 * 32 * DP * 2;
-  const dim3 grid((unsigned)(slots * a.Hkv), (unsigned)n);
+  const dim3 grid((unsigned)(few_slots(a.Tq, a.B, a.G) * a.Hkv), (unsigned)n);
   auto go = [&](auto kern) -> hipError_t {
     const hipError_t e = lds_limit((const void*)kern, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, grid, dim3(64 * FW), lds, st, a, (int)slots, static_cast<float*>(ws));
+    hipLaunchKernelGGL(kern, grid, dim3(64 * FW), lds, st, a, static_cast<float*>(ws));
     return hipGetLastError();
   };
   if (n == 1) return go(few_kernel<DP, false>);

@@ -593,7 +593,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
   const int g0 = KS4 * wave / NW, g1 = KS4 * (wave + 1) / NW;  // this wave's 4-step groups
   float res[4];
   if constexpr (YT == 3) {  // under the product
-    if (wave < NCT) load_residual<false>(res, rb * 16 + 4 * jj, min(wave * 16 + r16, C - 1), R, ep);
+    if (wave < NCT) load_residual(res, rb * 16 + 4 * jj, min(wave * 16 + r16, C - 1), R, ep);
   }
   Acc acc[NCT];
 #pragma unroll
@@ -1071,7 +1071,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(int R, int C, int RP
   const int bc = (int)(idx / quads), ar = (int)(idx % quads) * 4;
   if (bc >= C || ar >= R) return;
   float y[4], res[4];
-  if constexpr (YT == 3) load_residual<false>(res, ar, bc, R, ep);
+  if constexpr (YT == 3) load_residual(res, ar, bc, R, ep);
   int32_t yi[4];
   if constexpr (AB == 0) {
     int4 s = make_int4(0, 0, 0, 0);

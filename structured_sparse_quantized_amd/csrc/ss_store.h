@@ -92,65 +92,48 @@ __device__ __forceinline__ void store_one(void* Y, int64_t at, float v, bool f32
   if (f32) static_cast<float*>(Y)[at] = v;
   else static_cast<uint16_t*>(Y)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
 }
-// store_out with the general epilogue, in steps: the residuals of a lane's 4 results (the loads of several tiles
-// are issued before the first store: the residual may be Y, so none could move over one); and, of finished results
-// (gated: y[0], y[1] on side W, the even lanes' on side X), the sum with the residual and the store.
-template <bool SIDE_X>
+// The few-token kernels (weight-sparse side): a lane's 4 results are channels ar .. ar+3 of token bc. Their residuals (of the
+// 4 columns, or with a gate the 2, clamped into the row) are loaded under the product, long before the stores: the
+// residual may be Y, so no load could move over one.
 __device__ __forceinline__ void load_residual(float* r, int64_t ar, int64_t bc, int64_t R, const Epilogue& e) {
   if (!e.res) return;
-  if constexpr (SIDE_X) {
-    const int64_t col = e.gated ? bc >> 1 : bc;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) r[q] = load_res(e, min(ar + q, R - 1) * e.ldr + col);
-  } else {
-    const int n = e.gated ? 2 : 4;
-    const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
-    if (n == 4 && !e.f32 && (e.ldr & 3) == 0 && col + 4 <= cols) {
-      const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.res) + bc * e.ldr + col);
-      r[0] = __uint_as_float(x.x << 16);
-      r[1] = __uint_as_float(x.x & 0xFFFF0000u);
-      r[2] = __uint_as_float(x.y << 16);
-      r[3] = __uint_as_float(x.y & 0xFFFF0000u);
-      return;
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < n) r[q] = load_res(e, bc * e.ldr + min(col + q, cols - 1));
+  const int n = e.gated ? 2 : 4;
+  const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
+  if (n == 4 && !e.f32 && (e.ldr & 3) == 0 && col + 4 <= cols) {
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.res) + bc * e.ldr + col);
+    r[0] = __uint_as_float(x.x << 16);
+    r[1] = __uint_as_float(x.x & 0xFFFF0000u);
+    r[2] = __uint_as_float(x.y << 16);
+    r[3] = __uint_as_float(x.y & 0xFFFF0000u);
+    return;
   }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (q < n) r[q] = load_res(e, bc * e.ldr + min(col + q, cols - 1));
 }
-template <bool SIDE_X>
+// The finished values (gated: y[0], y[1]) plus their residuals, stored.
 __device__ __forceinline__ void store_epilogue(void* Y, int64_t ldy, int64_t ar, int64_t bc, int64_t R, float* y,
                                                const float* r, const Epilogue& e) {
   if (e.res) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (SIDE_X || q < 2 || !e.gated) y[q] += r[q];
+      if (q < 2 || !e.gated) y[q] += r[q];
   }
-  if constexpr (SIDE_X) {
-    if (e.gated && (bc & 1)) return;
-    const int64_t col = e.gated ? bc >> 1 : bc;
+  const int n = e.gated ? 2 : 4;
+  const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
+  if (n == 4 && !e.f32 && (ldy & 3) == 0 && col + 4 <= cols) {  // 8-byte vectors
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + bc * ldy + col) =
+        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    return;
+  }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (ar + q >= R) break;
-      store_one(Y, (ar + q) * ldy + col, y[q], e.f32);
-    }
-  } else {
-    const int n = e.gated ? 2 : 4;
-    const int64_t col = e.gated ? ar >> 1 : ar, cols = e.gated ? R >> 1 : R;
-    if (n == 4 && !e.f32 && (ldy & 3) == 0 && col + 4 <= cols) {  // 8-byte vectors
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(Y) + bc * ldy + col) =
-          make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-      return;
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q >= n || col + q >= cols) break;
-      store_one(Y, bc * ldy + col + q, y[q], e.f32);
-    }
+  for (int q = 0; q < 4; ++q) {
+    if (q >= n || col + q >= cols) break;
+    store_one(Y, bc * ldy + col + q, y[q], e.f32);
   }
 }
 
-// The few-token kernels' epilogue: one lane, 4 channels ar..ar+3 of token bc, scaled.
+// Their epilogue, of the scaled sums.
 __device__ __forceinline__ void finish_and_store(void* Y, int64_t ldy, int64_t ar, int64_t bc, int64_t R, float* y,
                                                  const float* r, const Epilogue& e) {
   if (e.bias) {
@@ -165,7 +148,7 @@ __device__ __forceinline__ void finish_and_store(void* Y, int64_t ldy, int64_t a
   } else {
     activate_n<4>(y, e.act, e.f32);
   }
-  store_epilogue<false>(Y, ldy, ar, bc, R, y, r, e);
+  store_epilogue(Y, ldy, ar, bc, R, y, r, e);
 }
 
 // Whether rows of Y and of the residual start on 16 bytes (their pointers do).
