@@ -60,6 +60,7 @@ __device__ __forceinline__ v4s read_tr(const SS_LDS void* __restrict__ p) {
 }
 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float unif(float x) { return __int_as_float(uni(__float_as_int(x))); }
 
 // the value of this lane and of lane l ^ 32, combined
 __device__ __forceinline__ float pair_max(float x) {
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[d][i] *= f;
       const bool big = is_big(m);
-      rise = __any(big) ? -1.0f : kRise;
+      rise = unif(__any(big) ? -1.0f : kRise);
       sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     for (int i = 0; i < 16; ++i)
       if (8 * (i / 4) + i % 4 < left) mt = fmaxf(mt, S0[i]);
     m = fmaxf(m, ceilf(pair_max(mt) * a.c));
-    rise = __any(is_big(m)) ? -1.0f : kRise;
+    rise = unif(__any(is_big(m)) ? -1.0f : kRise);
   }
   auto turn = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
