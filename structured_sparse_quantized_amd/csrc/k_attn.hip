@@ -187,9 +187,9 @@ __device__ __forceinline__ void renew(uint32_t& x) { asm volatile("" : "+v"(x));
 //   that waits for them out of every stage (1-3% for heads of 128, 6% for 64); the first stage's maximum is found ahead.
 // So the matrix instructions have vector work of about the same length beside them that does not wait for
 // them, and fragments are read a stage ahead of their use.
-// Measured: one prompt of 8192 tokens, 32 heads of 128 over 8, causal: 475 us, 1.16 PFLOP/s of the seen pairs (matrix cores
-// busy 65% of the cycles, at the 1.8 GHz the card keeps under this load; its large bf16 product runs at 1.37); 9 packed
-// prompts, 8001 tokens, 28 heads over 4: 85 us, 0.70 PFLOP/s. What bounds it is the vector work beside the matrix
+// Measured: one prompt of 8192 tokens, 32 heads of 128 over 8, causal: 470-507 us by the card, 1.09-1.17 PFLOP/s of the seen
+// pairs (matrix cores busy 65% of the cycles, at the 1.8 GHz a card keeps under this load; its large bf16 product runs at
+// 1.37); 9 packed prompts, 8001 tokens, 28 heads over 4: 84-88 us, 0.68-0.71 PFLOP/s. What bounds it is the vector work beside the matrix
 // instructions, some 60 instructions per 16 scores a lane (the 16 powers at a quarter of the rate), about as long as
 // the products themselves. Tried and not kept: 64 rows a wave (608 us for the first prompt, when this form took 537,
 // the accumulators crowd the registers), 8 waves on one tile (561), stages not merged (557), deeper rings, the two
@@ -826,6 +826,10 @@ inline int64_t few_slots(int64_t Tq, int64_t B, int64_t G) { return Tq * G / FM 
 // of 1024 keys even out lengths: 64 caches of 1 to 8192 keys 213 in 4, 274 whole (all of 8192: 384 / 393). The join costs 3
 // us: below 512 keys a tile stays whole (9.8 in one, 9.7 in 3 at 384), below 1024 where it would be cut in few parts
 // (16 caches of 512: 12.8 whole, 13.5 in 4).
+// The lengths are in device memory, so both rules go by the mean of the room in k, and a call whose lengths are far from it
+// runs by another's plan: 64 caches of 1024 keys in room for 8192 take 51.7 us, without the room 45.0; of 256 28.9 / 14.9;
+// of 64 24.4 / 6.6; 16 tokens over 256 keys in room for 16384 19.3 / 8.6; one packed sequence of 8192 keys among 63 of 64
+// 101 us (alone 10.6), where the same in room for 8192 each takes 49.
 inline int splits(int64_t Tq, int64_t Tk, int64_t B, int64_t G, int64_t Hkv, int64_t D) {
   if (Tq * G * Hkv >= 1 << 24) return 1;  // join_kernel: 256 threads a row, fewer than 2^32 in a launch
   const int64_t tiles = std::max<int64_t>(B, Tq * G / FM) * Hkv, keys = Tk / B;

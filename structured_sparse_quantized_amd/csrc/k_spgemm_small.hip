@@ -9,8 +9,9 @@
 // S stages of one 128-position step each (4 KB of compressed values, their index words, the B rows), every
 // wave bringing the same number of pieces per stage by LDS DMA, so that "the next stage has landed" is a wait for a
 // constant count. The fragments of step j + 1 are read while step j multiplies, before its loads set out (after them: 5% slower);
-// one barrier a step. A step costs 0.14, 0.18 and 0.24 us at TJ = 1, 2 and 4: at TJ = 1 a CU takes in its 9 KB at 65 B/ns,
-// 17 TB/s over 256 of them, from the L2s. A barrier per two steps measured the same at TJ = 1 and lost at TJ = 2 and 4, whose
+// one barrier a step. A step costs 0.14, 0.18 and 0.24 us at TJ = 1, 2 and 4: at TJ = 1 a CU takes in its 9 KB at 65 B/ns, at
+// TJ = 2 and 4 at 74 and 90, so the L2s could give more: with 5 stages (46 KB) on their way it is the latency of 0.7 us that
+// counts. A barrier per two steps measured the same at TJ = 1 and lost at TJ = 2 and 4, whose
 // LDS holds too few stages for it. FP8, 4096 rows, 128 tokens: 8.6 us at K = 4096, 20.2 us at 14336, where the 256 x 128
 // tiles take 20.8 and 51.8.
 #include <type_traits>

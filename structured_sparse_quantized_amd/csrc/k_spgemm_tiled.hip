@@ -1197,7 +1197,7 @@ static int wide_bn(bool side_x, int64_t R, int64_t C, int64_t KS, int64_t ldb_by
 }
 // The small tiles of k_spgemm_small.hip (general epilogue): the smallest width, 32, 64 or 128, whose tiles fit one per
 // CU, else one of 32 or 64 at two per CU; 0 where the problem fills the chip with the large tiles. Against the 256 x 128
-// kernel (FP8, 4096 x 4096): 9.0 against 20.8 us at 128 tokens, 12.0 / 20.9 at 256, 17.0 / 22.1 at 512, where the next
+// kernel (FP8, 4096 x 4096): 8.6 against 20.8 us at 128 tokens, 12.0 / 20.9 at 256, 17.0 / 22.1 at 512, where the next
 // width down takes 17.7; at 768 tokens (more than 256 tiles of any width, 25.5 / 23.1) the large tiles win. At two per CU:
 // 28672 x 4096, 48 and 64 tokens, 18.1 / 22.6 and 18.8 / 24.0 against the split reduction; 128 tokens, 448 tiles of width
 // 128, 31.2 / 24.1, so that width stops at one per CU. Reductions of up to 8 steps take width 64 at three per CU: 3000

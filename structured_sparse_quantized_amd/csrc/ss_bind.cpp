@@ -2,9 +2,9 @@
 //
 // These run between products, often on one token, where a call's own time on the host is what counts: checking the
 // tensors and marshalling some twenty arguments in Python took 7-12 us a call, the kernels 4-11 us. Here both take
-// 1-2 us. Nothing is computed: sizes, strides, types and devices are checked (the C entry points cannot see how
-// large a tensor behind a pointer is), outputs and workspaces come from torch, the call goes to the C ABI on the
-// current stream of the tensors' GPU.
+// 0.4-0.6 us, an output from torch's allocator 0.7-1.1 more; the launch, 2.9 us, is the rest of a call's 4-5 us. Nothing is
+// computed: sizes, strides, types and devices are checked (the C entry points cannot see how large a tensor behind a
+// pointer is), outputs and workspaces come from torch, the call goes to the C ABI on the current stream of the tensors' GPU.
 //
 // No exception leaves a function: torch's become Python exceptions, a refused call raises the package's SSError.
 #include <Python.h>
