@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * NW, 2) void small_kernel(int R, int C, int KS,
 #pragma unroll
   for (int q = 0; q < TJ; ++q) {
     const int b = (wave + q * NW) * 8 + (lane >> 3);
-    pb[q] = bd + (int64_t)min(c0 + b, C - 1) * ldb + swz(lane & 7, b & 15) * 16;
+    pb[q] = bd + (int64_t)min(c0 + b, C - 1) * (uint32_t)ldb + swz(lane & 7, b & 15) * 16;
   }
   // stage k into its slot; steps past the end re-read the last one (in bounds, never used), so that every wave's
   // count of loads stays the same

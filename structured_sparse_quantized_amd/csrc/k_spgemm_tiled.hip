@@ -603,7 +603,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_kernel(int R, int C, int KS
     const uint8_t* pm = tm + (int64_t)rb * KS4 * MT::BLOCK + lane * (4 * MT::WB);
     const uint8_t* pb[NCT];
 #pragma unroll
-    for (int c = 0; c < NCT; ++c) pb[c] = bd + (int64_t)min(c * 16 + r16, C - 1) * ldb + 16 * jj;
+    for (int c = 0; c < NCT; ++c) pb[c] = bd + (int64_t)min(c * 16 + r16, C - 1) * (uint32_t)ldb + 16 * jj;  // (2^31 bytes and more: two rows)
     tiled::v4i A[4], B[4][NCT][2];
     MV mcur, mnxt;
     // padded steps (>= KS) hold zero values; their dense slices re-read step KS-1
