@@ -8,7 +8,8 @@
 // untouched on almost every tile. Scores, m, l and O are
 // float32; the powers are rounded to bf16 (nearest even) for the second product, because the matrix
 // instructions take bf16 there: with q, k, v in bf16 that adds one rounding of at most 2^-8 relative per
-// key, independent over the keys. l sums the powers before that rounding.
+// key, independent over the keys (in all 0.0022 of a row against 0.0016 with float32 probabilities; what the rounding leaves as
+// a second operand costs few_kernel 0-3% over long caches and up to 20% for chunks of tokens). l sums the powers before it.
 //
 // Rows. The query heads that share a key head read the same keys, so the rows of one (sequence, key head) are
 // all its (token, head) pairs, r = token * G + head-in-group: a tile of rows covers fewer tokens than rows,
