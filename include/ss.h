@@ -494,6 +494,74 @@ ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_
                   int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
                   const int32_t* k_len, float scale, int causal, void* workspace, int64_t ws_bytes, void* stream);
 
+/* ss_attn_window -- ss_attn under a sliding window whose first tokens stay visible: the row at position p of its sequence
+ * (row i of lq: p = i + lk - lq) sees the keys j <= p with j > p - window or j < sinks. window = 0: no window (ss_attn; sinks
+ * then says nothing); window > 0 needs causal = 1 (SS_ERR_UNSUPPORTED). Keys that no row of a call sees are
+ * not part of a result, whatever they hold. Everything else as ss_attn; the workspace is that of its own query (it serves
+ * calls with few query rows per sequence). */
+int64_t ss_attn_window_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                                       int64_t sinks);
+ss_status ss_attn_window(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                         int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
+                         int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
+                         const int32_t* k_len, float scale, int causal, int64_t window, int64_t sinks, void* workspace,
+                         int64_t ws_bytes, void* stream);
+
+/* ss_rmsnorm_act -- what stands before a layer's products: the residual's addition, the root-mean-square norm, and the
+ * preparation of the product's activations, in one pass.
+ *   r[m][k] = X[m][k] + residual[m][k], rounded to x_dt and written to sum; without a residual r = X
+ *   rs[m] = fl32(1 / sqrt(mean_k r^2 + eps)), the mean and the root in float64
+ *   z[m][k] = fl32(fl32(r rs) w[k]); w NULL: fl32(r rs)
+ * and of the row z: y_dt BF16: Y [M][K], rounded once (n must be 2, sx NULL; ss_prune24_act reads it); I8 or FP8E4M3: codes
+ * and scales sx[M] = fl32(a / Q), lifted to Y [M][Kc], Kc = ss_lifted_k(K, n), as ss_quant_lift_act(z, n) gives them but for
+ * inv = fl32(fl32(1 / a) Q), which is what a norm and a quantiser of elementwise tensor operations compute: the codes are
+ * theirs, and a step from ss_quant_lift_act's where a value lies within 2^-23 of a border. A row of zeros gives zeros.
+ * X, residual, sum [M][K] (F32 or BF16; ldx, ldr, lds elements); sum may be X or residual (the same leading dimension), and is
+ * required with a residual; otherwise sum and Y overlap nothing. w [K]: F32 or x_dt. eps finite and >= 0. */
+ss_status ss_rmsnorm_act(const void* X, ss_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                         void* sum, int64_t lds, const void* w, ss_dtype w_dt, double eps, int n, ss_dtype y_dt, void* Y,
+                         int64_t ldy, float* sx, void* stream);
+
+/* A paged key-value cache: pages of `page` keys in any order of the pool, k [pages][page][Hkv][D] and v likewise, BF16, with
+ * strides in elements (p: page, t: key, h: head; the values of a head are adjacent). Row b of the table names the pages of
+ * sequence b: its key j lies in page table[b][j / page], at j % page. Entries outside 0 .. pages - 1 name no page.
+ * Pointers and strides 16-byte aligned; page strides below 2^32, key strides below 2^24; sequences may share pages. */
+typedef struct {
+  void *k, *v;
+  int64_t pages, page;
+  int64_t skp, skt, skh, svp, svt, svh;
+  const int32_t* table;           /* [sequences][table_cols] */
+  int64_t table_cols, table_ld;   /* columns in use; elements from row to row */
+} ss_paged_kv;
+
+/* ss_paged_store -- new tokens into a paged cache: rotary positions on their queries and keys (as ss_rotary: steps, rot_dim,
+ * layout, mscale), and keys and values to their places, in one pass. Token t of sequence b goes to key pos[t] of b: page
+ * table[b][pos / page]. q [T][Hq][D], k, v [T][Hkv][D], BF16, any strides (t: token, h: head) and alignment of their elements; D % 8 == 0.
+ * Turned queries go to qo (may be q with the same strides); Hq = 0: keys and values alone. rot_dim = 0 (then Hq must be
+ * 0): keys as they are.
+ *   cu: B + 1 non-decreasing int32 bounds of the sequences' tokens, or NULL with B = T: one token a sequence. Tokens in no
+ * sequence leave qo and the cache untouched; a token whose pos is negative or behind the table, or whose entry names no page,
+ * is not stored (its queries are turned all the same). What two tokens with one place leave there is undefined. The cache's
+ * rows must not overlap each other nor an input. */
+ss_status ss_paged_store(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                         int64_t svt, int64_t svh, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* pos,
+                         const int32_t* cu, const uint64_t* steps, int64_t rot_dim, ss_rope_layout layout, float mscale,
+                         void* qo, int64_t sot, int64_t soh, const ss_paged_kv* cache, void* stream);
+
+/* ss_attn_paged -- attention over a paged cache: ss_attn_window of query rows q [Tq][Hq][D] over the keys 0 .. k_len[b] - 1
+ * that the table names for sequence b (k_len: B int32, the new tokens' keys among them; clamped to the table). cu_q: B + 1
+ * int32 bounds of the sequences' rows, or NULL: one row a sequence (B = Tq), or one sequence of all rows (B = 1). A key whose entry names no page is not
+ * seen by any row (pages behind a window may be given back, their entries set to -1). causal, window, sinks, lse, heads, D,
+ * rows without keys and rows in no sequence as in ss_attn and ss_attn_window; page sizes of any number of keys.
+ *   It is made for few rows per sequence: single tokens, drafts, short chunks (all are computed, in tiles of 32 rows of a key head).
+ *   workspace: ss_attn_paged_workspace_bytes bytes (room = table_cols * page), as for ss_attn. */
+int64_t ss_attn_paged_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                                      int64_t sinks);
+ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_kv* cache, void* o, int64_t sot, int64_t soh,
+                        float* lse, int64_t Tq, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q,
+                        const int32_t* k_len, float scale, int causal, int64_t window, int64_t sinks, void* workspace,
+                        int64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

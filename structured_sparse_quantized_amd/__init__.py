@@ -27,8 +27,11 @@ Functions keep the names of the C entry points:
         (the product with bias, activation, gate and residual; workspace as spgemm_tiled)
     rotary_steps(rot_dim, base, scaling, ...)   -> (steps, mscale)
     rotary(x, pos, steps, layout, mscale)       -> y [T, H, D]
-    attn(q, k, v, cu_q, cu_k, k_len, causal)    -> o [Tq, Hq, D]  (workspace from torch when ss_attn_workspace_bytes
-                                                   asks for one)
+    attn(q, k, v, cu_q, cu_k, k_len, causal, window, sinks) -> o [Tq, Hq, D]  (workspace from torch when the library asks
+                                                   for one)
+    rmsnorm_act(x, w, eps, residual, n, y_dtype) -> (y, sx | None, sum | None)  (norm, quantisation and lift)
+    paged_store(k, v, pos, k_pages, v_pages, table, cu, q, steps) -> turned q | None  (rotary and the cache's write)
+    attn_paged(q, k_pages, v_pages, table, k_len, cu_q, window, sinks) -> o [Tq, Hq, D]
 """
 from __future__ import annotations
 
@@ -105,12 +108,30 @@ lib.ss_rotary.argtypes = [_vp, _int, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i6
                           _i64, _vp]
 lib.ss_attn_workspace_bytes.argtypes = [_i64] * 6
 lib.ss_attn_workspace_bytes.restype = _i64
+class PagedKV(ctypes.Structure):
+    """ss_paged_kv: a paged cache and its table, for calls to `lib` itself."""
+    _fields_ = [("k", _vp), ("v", _vp)] + [(f, _i64) for f in ("pages", "page", "skp", "skt", "skh", "svp", "svt", "svh")] + [
+        ("table", _vp), ("table_cols", _i64), ("table_ld", _i64)]
+
+
+lib.ss_attn_window_workspace_bytes.argtypes = [_i64] * 8
+lib.ss_attn_window_workspace_bytes.restype = _i64
+lib.ss_attn_window.argtypes = [_vp, _i64, _i64] * 4 + [_fp] + [_i64] * 6 + [_vp, _vp, _vp, ctypes.c_float, _int, _i64, _i64, _vp,
+                                                                            _i64, _vp]
+lib.ss_rmsnorm_act.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _int, ctypes.c_double, _int, _int, _vp,
+                               _i64, _fp, _vp]
+lib.ss_paged_store.argtypes = [_vp, _i64, _i64] * 3 + [_i64] * 5 + [_vp, _vp, _vp, _i64, _int, ctypes.c_float, _vp, _i64, _i64,
+                                                                    ctypes.POINTER(PagedKV), _vp]
+lib.ss_attn_paged_workspace_bytes.argtypes = [_i64] * 8
+lib.ss_attn_paged_workspace_bytes.restype = _i64
+lib.ss_attn_paged.argtypes = [_vp, _i64, _i64, ctypes.POINTER(PagedKV), _vp, _i64, _i64, _fp] + [_i64] * 5 + [
+    _vp, _vp, ctypes.c_float, _int, _i64, _i64, _vp, _i64, _vp]
 lib.ss_attn.argtypes = [_vp, _i64, _i64] * 4 + [_fp] + [_i64] * 6 + [_vp, _vp, _vp, ctypes.c_float, _int, _vp, _i64, _vp]
 for _f in ("ss_prune24", "ss_slide_decompose", "ss_quant_lift_act", "ss_prune24_act", "ss_spgemm", "ss_pack_sparse",
            "ss_prune24_act_tiled", "ss_slide_decompose_tiled", "ss_spgemm_tiled", "ss_spgemm_tiled_ws",
            "ss_spgemm_tiled_noalloc", "ss_prune24_block", "ss_quant_group_act", "ss_spgemm_tiled_block",
            "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill", "ss_spgemm_tiled_epilogue",
-           "ss_rotary_steps", "ss_rotary", "ss_attn"):
+           "ss_rotary_steps", "ss_rotary", "ss_attn", "ss_attn_window", "ss_rmsnorm_act", "ss_paged_store", "ss_attn_paged"):
     getattr(lib, _f).restype = _int
 
 EXPORTS = ("ss_lifted_k", "ss_lifted_k_logical", "ss_status_string", "ss_last_error", "ss_version",
@@ -119,7 +140,9 @@ EXPORTS = ("ss_lifted_k", "ss_lifted_k_logical", "ss_status_string", "ss_last_er
            "ss_slide_decompose_tiled", "ss_spgemm_tiled", "ss_spgemm_tiled_workspace_bytes", "ss_spgemm_tiled_ws",
            "ss_spgemm_tiled_noalloc", "ss_prune24_block", "ss_quant_group_act", "ss_spgemm_tiled_block",
            "ss_quant_lift_spgemm_decode", "ss_spgemm_tiled_batched", "ss_quant_spgemm_prefill",
-           "ss_spgemm_tiled_epilogue", "ss_rotary_steps", "ss_rotary", "ss_attn_workspace_bytes", "ss_attn")
+           "ss_spgemm_tiled_epilogue", "ss_rotary_steps", "ss_rotary", "ss_attn_workspace_bytes", "ss_attn",
+           "ss_attn_window_workspace_bytes", "ss_attn_window", "ss_rmsnorm_act", "ss_paged_store",
+           "ss_attn_paged_workspace_bytes", "ss_attn_paged")
 
 
 class SSError(RuntimeError):
@@ -641,9 +664,50 @@ def attn_workspace_bytes(Tq: int, Tk: int, B: int, Hq: int, Hkv: int, D: int) ->
 
 
 def attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k=None, k_len=None, causal: bool = True,
-         scale=None, out=None, lse=None, workspace=None):
+         scale=None, out=None, lse=None, workspace=None, window=None, sinks: int = 0):
     """Attention of packed sequences: q [Tq, Hq, D], k and v [Tk, Hkv, D] bf16 (any 16-byte aligned token and head
     strides), cu_q / cu_k int32 [B + 1] row bounds (None: one sequence), k_len int32 [B] keys in use (caches with
     room). scale defaults to 1 / sqrt(D). lse: a float32 [Hq, Tq] tensor that receives the rows' log-sum-exp.
+    window (with causal): the row at position p sees the keys j <= p with j > p - window or j < sinks.
     Calls with few query rows per sequence take a workspace from torch's allocator unless one is passed."""
-    return _ssbind.attn(q, k, v, cu_q, cu_k, k_len, causal, scale, out, lse, workspace)
+    return _ssbind.attn(q, k, v, cu_q, cu_k, k_len, causal, scale, out, lse, workspace, window, sinks)
+
+
+def attn_window_workspace_bytes(Tq: int, Tk: int, B: int, Hq: int, Hkv: int, D: int, window: int, sinks: int = 0) -> int:
+    return int(lib.ss_attn_window_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, window, sinks))
+
+
+def rmsnorm_act(x: torch.Tensor, w=None, eps: float = 1e-6, residual=None, n: int = 2, y_dtype="bf16", sum_out=None, out=None,
+                scale_out=None):
+    """Root-mean-square norm of x [M, K] (bf16 or f32) with weights w [K] (x's type or f32; None: ones), of x + residual
+    where a residual of x's type is given, and the preparation of a product's activations from it. Returns (y, sx, sum):
+    y_dtype "bf16": y [M, K], sx None; "i8" / "fp8": codes [M, lifted_k(K, n)] and scales as quant_lift_act leaves them. sum:
+    x + residual in x's type (None without a residual); sum_out may be x or residual themselves."""
+    return _ssbind.rmsnorm_act(x, w, eps, residual, n, dtype_code(y_dtype), sum_out, out, scale_out)
+
+
+# ---- paged caches: k_pages and v_pages [pages, page, Hkv, D] bf16, table int32 [B, columns] of page numbers ----------
+
+
+def paged_store(k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                table: torch.Tensor, cu=None, q=None, steps=None, layout: str = "half", mscale: float = 1.0, q_out=None):
+    """New tokens into a paged cache: k and v [T, Hkv, D] bf16 go to key pos[t] (int32) of their sequence, keys turned by
+    rotary positions where `steps` (rotary_steps) is given; q [T, Hq, D] is turned in the same pass and returned (q_out: may be
+    q itself), else None. cu: int32 [B + 1] token bounds of the sequences, None: one token each."""
+    code = ROPE_LAYOUT.get(layout)
+    if code is None:
+        raise SSError(SS_ERR_UNSUPPORTED, f"layout {layout!r}: one of {', '.join(ROPE_LAYOUT)}")
+    return _ssbind.paged_store(k, v, pos, k_pages, v_pages, table, cu, q, steps, code, mscale, q_out)[0]
+
+
+def attn_paged_workspace_bytes(Tq: int, room: int, B: int, Hq: int, Hkv: int, D: int, window: int = 0, sinks: int = 0) -> int:
+    """Workspace of attn_paged for a table of `room` keys (columns * page) and a window (0: none)."""
+    return int(lib.ss_attn_paged_workspace_bytes(Tq, room, B, Hq, Hkv, D, window, sinks))
+
+
+def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, k_len: torch.Tensor,
+               cu_q=None, causal: bool = True, window=None, sinks: int = 0, scale=None, out=None, lse=None, workspace=None):
+    """Attention of q [Tq, Hq, D] bf16 over the first k_len[b] keys of each sequence's pages; cu_q int32 [B + 1] row bounds
+    (None: one row a sequence, or one sequence). Table entries that name no page hide their keys. window, sinks, scale,
+    lse and workspace as in attn."""
+    return _ssbind.attn_paged(q, k_pages, v_pages, table, k_len, cu_q, causal, window, sinks, scale, out, lse, workspace)

@@ -27,51 +27,10 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ss_device.h"
-#include "ss_kernels.h"
+#include "ss_attn.h"
 
 namespace ss {
 namespace attn {
-
-#define SS_LDS __attribute__((address_space(3)))
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-
-constexpr float kSlack = 8.0f;     // in powers of two
-constexpr float kRise = 256.0f;
-constexpr int vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }  // s_waitcnt vmcnt(n)
-constexpr float kLow = -3.402823466e38f;  // below every finite score's exponent, and finite: kLow - kLow = 0
-// From this size of a maximum m on, the power's argument is the rounded product c s less m. Below it both come out of one
-// fused step, whose exact product may pass the rounded maximum by half of a unit of m's last place: 2^7 at 2^31, a power that
-// overflows (or, below m, a largest score whose power is 0).
-constexpr float kBig = 16777216.0f;  // 2^24
-__device__ __forceinline__ bool is_big(float m) { return m != kLow && fabsf(m) >= kBig; }
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
-// The transposing LDS read, through a pointer that nothing else writes while it is read (the kernels' barriers and
-// waits see to that). Said without it, the compiler lets every such read wait for all loads to LDS in flight,
-// which exposed the latency of the next tile's load in every tile.
-__device__ __forceinline__ v4s read_tr(const SS_LDS void* __restrict__ p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((SS_LDS v4s*)p);
-}
-
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-__device__ __forceinline__ float unif(float x) { return __int_as_float(uni(__float_as_int(x))); }
-
-// the value of this lane and of lane l ^ 32, combined
-__device__ __forceinline__ float pair_max(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float pair_sum(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
 
 // One sequence's share of the call, all uniform. Bounds taken from device memory are clamped to the tensors,
 // so whatever cu_q, cu_k and k_len hold, no access leaves q, k, v or o.
@@ -139,43 +98,6 @@ template <int BM> __device__ __forceinline__ bool locate(const AttnArgs& a, int 
   return tile >= 0 && tile * BM < s.lq * a.G;
 }
 
-// LDS tiles are row-major (DP values a row, in 16-byte chunks) with the chunks of a row permuted by an XOR, so
-// that the fragment reads below spread over the banks: a K fragment reads one chunk column of 32 rows, a V
-// fragment 4 chunks of 4 rows (rows of 64 values lie two to a turn of the banks, so pairs of rows share a place).
-template <int DP> struct Lds {
-  __device__ static int swk(int row) { return DP >= 128 ? row & 15 : (row >> 1) & 7; }
-  __device__ static int swv(int row) { return DP >= 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
-};
-
-// Under a causal mask a tile's keys go past what some of its rows see, or all of them (rows of one token, with 32 query heads
-// and more to a key head: a tile is loaded up to the sequence's last key), and one product takes them all: a power of
-// zero keeps a finite value of an unseen key out of a row, not an infinity or a NaN. Where a tile's values hold one, it is
-// replaced by zero in the operand and added to the rows that see it by hand (its power is above zero, so the sum is v itself).
-__device__ __forceinline__ uint32_t odd_bf16x2(uint32_t w) {  // bits 31, 15: that half is infinite or NaN
-  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-}
-__device__ __forceinline__ uint32_t even_out(uint32_t w) {
-  asm volatile("" : "+v"(w));  // (computed anew: its parts are not kept from the test)
-  return w & ~((odd_bf16x2(w) >> 15) * 0xFFFFu);
-}
-// `vt`: 32 rows of values in LDS, of which row r of the lane sees the first `seen`
-template <int DP> __device__ __forceinline__ void add_odd(v16f* O, const SS_LDS uint8_t* vt, int seen, int h) {
-  asm volatile("" : "+v"(h), "+v"(seen));  // (nothing of this is kept in registers beside the loop that calls it)
-#pragma unroll 1
-  for (int k = 0; k < 32; ++k)
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const v2u w = *reinterpret_cast<const SS_LDS v2u*>(vt + k * DP * 2 + ((d * 4 + g) ^ Lds<DP>::swv(k)) * 16 + h * 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-          if (k < seen && !__builtin_isfinite(v)) O[d][4 * g + e] += v;
-        }
-      }
-}
-
 // What is computed from x is computed anew from here on (in the loops that have no registers to keep it in).
 __device__ __forceinline__ void renew(uint32_t& x) { asm volatile("" : "+v"(x)); }
 
@@ -200,7 +122,12 @@ __device__ __forceinline__ void renew(uint32_t& x) { asm volatile("" : "+v"(x));
 constexpr int NW = 4, BM = NW * 32;  // waves of a part, rows
 constexpr int BK = 64;               // keys per tile
 
-template <int DP, int NS>
+//
+// With WIN the rows of a workgroup see the tiles of the first tokens and, from the first row's window on, those behind: a
+// list of tiles without the ones between, walked as the whole range is without it. Tiles that some row of a wave sees in part
+// (the diagonal, the windows' lower edges, the end of the first tokens) are masked; the others branch over the masks. (Loops of
+// their own for the two kinds of tiles, in turn, took hundreds of registers to scratch.)
+template <int DP, int NS, bool WIN>
 __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int slots) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;  // chunks a row, 16-value steps, 32-value blocks
   constexpr int KB = BK * DP * 2;                          // bytes of a K or V tile
@@ -237,9 +164,20 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   }
   const int kend = uni(lim(min(tile * BM + BM, nr) - 1));  // keys of the workgroup
   const int wmin = uni(r0 < nr ? lim(r0) : 0), wmax = uni(r0 < nr ? lim(min(r0 + 32, nr) - 1) : 0);
-  const int all = (kend + BK - 1) / BK, nt = (all + NS - 1) / NS, t0 = part * nt;  // tiles; of a part; its first
-  // this wave's tiles; those every row sees whole
-  const int nw = min(max((wmax + BK - 1) / BK - t0, 0), nt), nfull = min(max(wmin / BK - t0, 0), nt);
+  // a window: row r sees the keys from low(r) on, and the first ones below `sinks`
+  auto low = [&](int r) {
+    const int p = r / a.G + s.lk - s.lq;
+    return WIN && p >= a.window ? p - a.window + 1 : 0;
+  };
+  const int row_low = low(row), sinks = WIN ? min(a.sinks, kend) : 0;
+  const int whigh = uni(r0 < nr ? low(min(r0 + 32, nr) - 1) : 0);  // of the wave's last row
+  // list of tiles: the first ns, then those from w0 on
+  const int ns = (sinks + BK - 1) / BK, w0 = WIN ? max(uni(low(tile * BM)) / BK, ns) : 0;
+  auto listed = [&](int end) { return max(min((end + BK - 1) / BK, ns), (end + BK - 1) / BK - (w0 - ns)); };  // tiles up to key `end`
+  const int all = WIN ? listed(kend) : (kend + BK - 1) / BK, nt = (all + NS - 1) / NS, t0 = part * nt;  // tiles; of a part; its first
+  auto key_of = [&](int i) { return (WIN && i >= ns ? i + (w0 - ns) : i) * BK; };  // first key of tile i of the list
+  // this wave's tiles; those every row sees whole (without a window, the first of them)
+  const int nw = min(max((WIN ? listed(wmax) : (wmax + BK - 1) / BK) - t0, 0), nt), nfull = min(max(wmin / BK - t0, 0), nt);
 
   // DMA of a tile: load i of a wave brings rows RPI i + .. to byte 1024 (NW i + wave) + 16 lane of its slot; the rows
   // of a lane differ by RPI, a multiple of 16, so they share one place in the swizzle and one lane offset. The
@@ -257,9 +195,11 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   const uint16_t* vp = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
   // the tiles that are being brought in: where they start, and the keys from there to the sequence's end
   const uint32_t kr2 = (uint32_t)a.skt * 2u, vr2 = (uint32_t)a.svt * 2u;  // bytes from row to row
-  const uint8_t *kb = reinterpret_cast<const uint8_t*>(kp) + (int64_t)t0 * BK * kr2,
-                *vb = reinterpret_cast<const uint8_t*>(vp) + (int64_t)t0 * BK * vr2;
-  int kleft = s.lk - t0 * BK, vleft = kleft;
+  const int from = WIN ? key_of(t0) : t0 * BK;
+  const uint8_t *kb = reinterpret_cast<const uint8_t*>(kp) + (int64_t)from * kr2,
+                *vb = reinterpret_cast<const uint8_t*>(vp) + (int64_t)from * vr2;
+  int kleft = s.lk - from, vleft = kleft;
+  int kat = t0, vat = t0;  // (a window: their places in the list)
   auto load_k = [&](int i, uint32_t to) __attribute__((always_inline)) {
     const int last = min(max(kleft, 0), BK) - 1;  // -1: nothing is left, a resource of no bytes
     const uint32_t n = ((uint32_t)last * kr2 + a.D * 2) & ~(uint32_t)(last >> 31);
@@ -272,8 +212,14 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(vb, n), (SS_LDS void*)((SS_LDS uint8_t*)smem + to + (NW * i + wave) * 1024), 16,
                                              ofv + (uint32_t)(i * RPI) * vr2, 0, 0, 0);
   };
-  auto next_k = [&]() __attribute__((always_inline)) { kb += (int64_t)BK * kr2, kleft -= BK; };
-  auto next_v = [&]() __attribute__((always_inline)) { vb += (int64_t)BK * vr2, vleft -= BK; };
+  auto next_k = [&]() __attribute__((always_inline)) {
+    const int n = WIN && ++kat == ns ? BK * (w0 - ns + 1) : BK;
+    kb += (int64_t)n * kr2, kleft -= n;
+  };
+  auto next_v = [&]() __attribute__((always_inline)) {
+    const int n = WIN && ++vat == ns ? BK * (w0 - ns + 1) : BK;
+    vb += (int64_t)n * vr2, vleft -= n;
+  };
 
   // this lane's places in a tile: K row l32 (chunk 2 i + h), V row 4 h + (lane % 16) / 4 of a 16-key step; the XOR
   // of the swizzle leaves KST addresses for K and DB for V, the rest are constant offsets
@@ -305,13 +251,25 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   };
   // one stage: `cur` holds its scores, `nxt` receives those of the next; kn: LDS offset of the keys of the stage after
   // the next, vc: of this stage's values; `side`: work beside it (loads)
+  bool masked = true;  // (a window: whether some row does not see the tile whole)
   auto stage = [&](v16f& cur, v16f& nxt, uint32_t kn, uint32_t vc, int first, auto side, auto maskc) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (decltype(maskc)::value) {
       const int left = row_lim - first - 4 * h;
+      if constexpr (WIN) {
+        if (masked) {
+          const int lo = row_low - first - 4 * h, sk = sinks - first - 4 * h;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (8 * (i / 4) + i % 4 >= left) cur[i] = -INFINITY;
+          for (int i = 0; i < 16; ++i) {
+            const int e = 8 * (i / 4) + i % 4;
+            if (e >= left || (e < lo && e >= sk)) cur[i] = -INFINITY;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (8 * (i / 4) + i % 4 >= left) cur[i] = -INFINITY;
+      }
     }
     side();
     nxt = v16f{};
@@ -364,7 +322,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     P[1] = __builtin_bit_cast(v8bf, pk[1]);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (decltype(maskc)::value) {
-      if (wmin < s.lk && first + 32 > wmin) {  // keys were loaded that some row does not see (its rows may be one token's)
+      if (WIN ? masked : wmin < s.lk && first + 32 > wmin) {  // keys were loaded that some row does not see (its rows may be one token's)
         uint32_t odd = 0;
 #pragma unroll
         for (int j = 0; j < 2 * DB; ++j) {
@@ -380,7 +338,8 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
             for (int i = 0; i < 4; ++i) w[i] = even_out(w[i]);
             vf[j / DB][j % DB] = __builtin_bit_cast(v8bf, w);
           }
-          add_odd<DP>(O, (const SS_LDS uint8_t*)smem + vc, row_lim - first, h);
+          if constexpr (WIN) add_odd_between<DP>(O, (const SS_LDS uint8_t*)smem + vc, row_low - first, row_lim - first, sinks - first, h);
+          else add_odd<DP>(O, (const SS_LDS uint8_t*)smem + vc, row_lim - first, h);
         }
       }
     }
@@ -409,11 +368,13 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     for (int i = 0; i < KST; ++i) S0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], qf[i], S0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < KST; ++i) read_k(i, KB / 2);
-    const int left = row_lim - t0 * BK - 4 * h;
+    const int left = row_lim - from - 4 * h, lo = row_low - from - 4 * h, sk = sinks - from - 4 * h;
     float mt = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (8 * (i / 4) + i % 4 < left) mt = fmaxf(mt, S0[i]);
+    for (int i = 0; i < 16; ++i) {
+      const int e = 8 * (i / 4) + i % 4;
+      if (e < left && (!WIN || e >= lo || e < sk)) mt = fmaxf(mt, S0[i]);
+    }
     m = fmaxf(m, ceilf(pair_max(mt) * a.c));
     rise = unif(__any(is_big(m)) ? -1.0f : kRise);
   }
@@ -433,19 +394,25 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   auto tile_of = [&](int t, auto maskc) __attribute__((always_inline)) {
     turn();
     if constexpr (decltype(maskc)::value) renew(ofk), renew(ofv);
-    stage(S0, S1, k1, v0, (t0 + t) * BK, [&]() __attribute__((always_inline)) {
+    const int key = WIN ? key_of(t0 + t) : (t0 + t) * BK;
+    if constexpr (WIN) masked = key + BK > wmin || (key < whigh && key + BK > sinks);
+    stage(S0, S1, k1, v0, key, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_v(i, v1);
     }, maskc);
-    stage(S1, S0, k1 + KB / 2, v0 + KB / 2, (t0 + t) * BK + 32, [&]() __attribute__((always_inline)) {
+    stage(S1, S0, k1 + KB / 2, v0 + KB / 2, key + 32, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_k(i, k0);
     }, maskc);
     rotate();
   };
   int t = 0;
-  for (; t < nfull; ++t) tile_of(t, std::false_type{});
-  for (; t < nw; ++t) tile_of(t, std::true_type{});
+  if constexpr (WIN) {
+    for (; t < nw; ++t) tile_of(t, std::true_type{});
+  } else {
+    for (; t < nfull; ++t) tile_of(t, std::false_type{});
+    for (; t < nw; ++t) tile_of(t, std::true_type{});
+  }
 #pragma unroll
   for (int j = 0; j < 2 * DB; ++j)  // the last stage's values
     O[j % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[j / DB][j % DB], P[j / DB], O[j % DB], 0, 0, 0);
@@ -531,8 +498,10 @@ template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
     return hipGetLastError();
   };
   const int64_t wgs = slots * a.Hkv, cus = num_cus_p();
-  const bool two = DP <= 64 ? wgs <= 2 * cus && a.Tk >= 512 * (int64_t)a.B : wgs <= cus && a.Tk >= 1024 * (int64_t)a.B;
-  return two ? go(prompt_kernel<DP, 2>, 2) : go(prompt_kernel<DP, 1>, 1);
+  const int64_t keys = a.window ? std::min<int64_t>(a.Tk, ((int64_t)a.window + a.sinks + BM / a.G) * a.B) : a.Tk;  // that a tile walks, at most
+  const bool two = DP <= 64 ? wgs <= 2 * cus && keys >= 512 * (int64_t)a.B : wgs <= cus && keys >= 1024 * (int64_t)a.B;
+  if (a.window) return two ? go(prompt_kernel<DP, 2, true>, 2) : go(prompt_kernel<DP, 1, true>, 1);
+  return two ? go(prompt_kernel<DP, 2, false>, 2) : go(prompt_kernel<DP, 1, false>, 1);
 }
 
 // ---- few rows per sequence: the keys split over waves and workgroups ---------------------------------------------
@@ -859,21 +828,36 @@ template <int DP> hipError_t launch_few(const AttnArgs& a, void* ws, hipStream_t
 
 }  // namespace attn
 
-int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+// Under a window a sequence's keys are those that a chunk of its rows sees.
+static int64_t attn_keys(int64_t Tq, int64_t Tk, int64_t B, int64_t window, int64_t sinks) {
+  return window ? std::min(Tk, (window + sinks + Tq / B) * B) : Tk;
+}
+
+int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   const int64_t G = Hq / Hkv;
-  if (!attn::few_rows(Tq, Tk, B, G, Hkv)) return 0;
+  if (!attn::few_rows(Tq, attn_keys(Tq, Tk, B, window, sinks), B, G, Hkv)) return 0;
+  if (window) return flat_workspace_bytes(Tq, (Tk + B - 1) / B, B, Hq, Hkv, D, window, sinks);
   const int64_t n = attn::splits(Tq, Tk, B, G, Hkv, D);
   return n == 1 ? 0 : n * Tq * Hq * (D + 1) * 4;
 }
 
 // a launch holds fewer than 2^32 threads
-bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv) {
-  const int64_t G = Hq / Hkv, few = attn::few_rows(Tq, Tk, B, G, Hkv);
+bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t window, int64_t sinks) {
+  const int64_t G = Hq / Hkv, few = attn::few_rows(Tq, attn_keys(Tq, Tk, B, window, sinks), B, G, Hkv);
+  if (few && window) return true;  // (as many workgroups as the chip holds)
   return (few ? attn::few_slots(Tq, B, G) * 64 * attn::FW : (Tq * G / attn::BM + B) * 64 * attn::NW) * Hkv <= 0xFFFFFFFFLL;
 }
 
 hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {
-  if (attn::few_rows(a.Tq, a.Tk, a.B, a.G, a.Hkv)) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
+  if (attn::few_rows(a.Tq, attn_keys(a.Tq, a.Tk, a.B, a.window, a.sinks), a.B, a.G, a.Hkv)) {
+    if (!a.window) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
+    FlatArgs f{};
+    f.q = a.q, f.k = a.k, f.v = a.v, f.o = a.o, f.lse = a.lse, f.cu_q = a.cu_q, f.cu_k = a.cu_k, f.k_len = a.k_len;
+    f.sqt = a.sqt, f.sqh = a.sqh, f.sot = a.sot, f.soh = a.soh, f.skt = a.skt, f.skh = a.skh, f.svt = a.svt, f.svh = a.svh;
+    f.Tq = a.Tq, f.Tk = a.Tk, f.B = a.B, f.Hkv = a.Hkv, f.G = a.G, f.D = a.D;
+    f.c = a.c, f.causal = a.causal, f.window = a.window, f.sinks = a.sinks;
+    return launch_flat(f, (a.Tk + a.B - 1) / a.B, ws, st);
+  }
   return a.D <= 64 ? attn::launch_prompt<64>(a, st) : attn::launch_prompt<128>(a, st);
 }
 

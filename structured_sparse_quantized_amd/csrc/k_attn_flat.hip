@@ -1,0 +1,508 @@
+// Attention of few query rows a sequence over a paged cache, or over contiguous keys under a sliding window (gfx950):
+//   o = softmax(scale q k^T + mask) v of the keys that a row sees: with position p (the last row of a sequence has its last
+//   key), j <= p and, under a window w with s first tokens, j > p - w or j < s.
+//
+// Mathematics, matrix instructions and LDS tiles are those of the packed attention (k_attn.hip): tiles of 32 rows, the (token,
+// head) pairs of a sequence that share a key head; units of 32 keys; one pass with a running maximum and sum.
+//
+// Split. Such calls read every seen key and value once for a handful of rows (HBM bound), and lengths differ from sequence to
+// sequence. So the work is laid out flat: the units of all tiles one after the other, and each of the launch's workgroups
+// (as many as the chip holds at once) takes an equal run of them, whatever tile that begins and ends in. The lengths are in
+// device memory, so the workgroups find their runs themselves, by a sum over the sequences. A tile that lies whole in a run is
+// finished there; of one that is cut, each workgroup leaves a part (float32, normalised, with its row's log2 of the sum),
+// a run's first tile in one place and its last in another, and join_kernel adds the parts in order.
+//
+// Loads. Units go to LDS by loads of 16 bytes a lane from addresses of its own, so that a unit's keys may lie anywhere: each of
+// 32 lanes looks up the page of one key, a unit ahead, and the lanes that load its row take it from there. What no row of the tile
+// sees (keys behind the end, outside the window, entries that name no page) is loaded from a line of zeros instead: no memory
+// behind it is read, and whatever it holds stays out of the product.
+#include <math.h>
+
+#include <algorithm>
+
+#include "ss_attn.h"
+
+namespace ss {
+namespace flat {
+
+using namespace attn;
+constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
+constexpr int kMinUnits = 4;            // a workgroup's run, at least
+constexpr int kJoin = 8;                // workgroups that share a cut tile's rows
+
+__device__ const uint4 kZeros = {0, 0, 0, 0};
+
+// Parts in the workspace: one record per workgroup, then log2 of the sums [workgroup][2][FM], then the parts
+// [workgroup][2][rows][D].
+struct Record {  // of the tile that begins in this workgroup's run and ends in a later one
+  int parts;     // 0: none
+  int slot, rows, kvh, r0, unused;
+  int64_t q0;
+};
+static_assert(sizeof(Record) == 32, "workspace layout");
+struct Parts {
+  Record* rec;
+  float* lg;
+  float* part;
+  int rows;  // room of a part
+};
+__host__ __device__ inline Parts parts_of(void* ws, int64_t wgs, int rows) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  return {reinterpret_cast<Record*>(p), reinterpret_cast<float*>(p + wgs * sizeof(Record)),
+          reinterpret_cast<float*>(p + wgs * (sizeof(Record) + 2 * FM * 4)), rows};
+}
+
+struct Seq {
+  int64_t q0, k0;  // first query row, first key row (contiguous keys)
+  int lq, lk;
+};
+__device__ __forceinline__ int64_t inside(int x, int64_t n) { return min(max((int64_t)x, (int64_t)0), n); }
+// Bounds from device memory are clamped to the tensors, so whatever they hold, no access leaves q, k, v or o.
+template <bool PAGED> __device__ __forceinline__ Seq load_seq(const FlatArgs& a, int b) {
+  Seq s;
+  int64_t q0 = 0, q1 = a.Tq, k0 = 0, k1 = a.Tk;
+  int len = 0x7FFFFFFF;
+  if (a.cu_q) {
+    q0 = inside(a.cu_q[b], a.Tq), q1 = inside(a.cu_q[b + 1], a.Tq);
+  } else if (a.B > 1) {  // one row a sequence
+    q0 = min((int64_t)b, a.Tq), q1 = min((int64_t)b + 1, a.Tq);
+  }
+  if (PAGED) {
+    k1 = min((int64_t)a.cols * a.page, (int64_t)0x7FFFFF00);
+    len = a.k_len[b];
+  } else {
+    if (a.cu_k) k0 = inside(a.cu_k[b], a.Tk), k1 = inside(a.cu_k[b + 1], a.Tk);
+    if (a.k_len) len = a.k_len[b];
+  }
+  s.q0 = q0;
+  s.k0 = k0;
+  s.lq = (int)(max(q1, q0) - q0);
+  s.lk = min(max(len, 0), (int)min(max(k1, k0) - k0, (int64_t)0x7FFFFF00));
+  return s;
+}
+__host__ __device__ inline int tiles_of(int lq, int G) { return (int)(((int64_t)lq * G + FM - 1) / FM); }
+// units of a tile of the sequence, at most (at least one, so that rows without keys are written)
+__host__ __device__ inline int units_of(int window, int sinks, int G, int lq, int lk) {
+  int64_t n = ((int64_t)lk + 31) / 32;
+  if (window) {  // the tile's tokens see window + tokens - 1 adjacent keys between them, and the first ones
+    const int64_t tok = (FM - 1 + G - 1) / G + 1, len = (int64_t)window + (tok < lq ? tok : lq) - 1;
+    const int64_t m = (len + 62) / 32 + ((int64_t)sinks + 31) / 32;
+    n = m < n ? m : n;
+  }
+  return n > 1 ? (int)n : 1;
+}
+
+template <int DP, bool PAGED>
+__global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) {
+  constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;
+  constexpr int KB = 32 * DP * 2, UNIT = 2 * KB, RING = FR * UNIT;
+  constexpr int LPU = KB / 1024;  // 1 KB loads per unit and operand
+  constexpr int RPL = 64 / CH;    // rows of a load
+  constexpr int OST = DP * 4 + 16;
+  static_assert(FM * OST <= RING, "a wave's results fit its ring");
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[FW][2][FM];
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+
+  // ---- this workgroup's run -------------------------------------------------------------------------------------
+  auto weight = [&](int i) -> int64_t {
+    if (i >= a.B) return 0;
+    const Seq s = load_seq<PAGED>(a, i);
+    const int n = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
+    return (int64_t)tiles_of(s.lq, a.G) * a.Hkv * n;
+  };
+  int64_t mine = weight(lane), total = mine;
+  for (int i = 64 + lane; i < ((a.B + 63) & ~63); i += 64) total += weight(i);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, 64);
+  const int64_t least = a.whole ? 1 : kMinUnits;
+  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, least);
+  int64_t s0 = blockIdx.x * run;
+  const int64_t s1 = min(s0 + run, total);
+  if (!a.whole && threadIdx.x == 0) ws.rec[blockIdx.x].parts = 0;
+  if (s0 >= total) return;
+  int b = 0;
+  int64_t before = 0;  // work before sequence b
+  for (int c = 0; c < a.B; c += 64) {
+    if (c > 0) mine = weight(c + lane);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t x = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += x;
+    }
+    const uint64_t past = __ballot(before + incl > s0);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      b = c + l;
+      before += __shfl(incl - mine, l, 64);
+      break;
+    }
+    before += __shfl(incl, 63, 64);
+  }
+  b = uni(b);
+  Seq s = load_seq<PAGED>(a, b);
+  int tiles = tiles_of(s.lq, a.G), un = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
+  int64_t th = (s0 - before) / un;  // tile and key head in the sequence, the head fastest
+  int j0 = (int)((s0 - before) - th * un);
+
+  const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
+  SS_LDS uint8_t* ring = (SS_LDS uint8_t*)smem + wave * RING;
+  bool first = true;
+#pragma unroll 1
+  while (true) {
+    const int take = (int)min((int64_t)(un - j0), s1 - s0);
+    const int tile = uni((int)(th / a.Hkv)), kvh = uni((int)(th - (int64_t)tile * a.Hkv));
+    const int nr = s.lq * a.G, r0 = tile * FM, rows = min(nr - r0, FM);
+    auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
+    auto low = [&](int r) {
+      const int p = r / a.G + s.lk - s.lq;
+      return a.window && p >= a.window ? p - a.window + 1 : 0;
+    };
+    const int r = min(r0 + l32, nr - 1), row_lim = lim(r), row_low = low(r);
+    const int kend = uni(lim(r0 + rows - 1)), kmin = uni(lim(r0)), klow = uni(low(r0)), khigh = uni(low(r0 + rows - 1));
+    const int sinks = a.window ? min(a.sinks, kend) : 0;
+    const bool tokens = r0 / a.G != (r0 + rows - 1) / a.G;  // more than one: rows that see different keys
+    // the units that some row sees: those of the first tokens, then those of the windows
+    const int su = (sinks + 31) / 32, wb = max(klow / 32, su), units = su + max((kend + 31) / 32 - wb, 0);
+    const int j1 = a.whole ? units : j0 + take, je = min(j1, units);
+    auto base = [&](int j) { return (j < su ? j : wb + j - su) * 32; };
+    auto wanted = [&](int key) { return key < kend && (key >= klow || key < sinks); };
+    // the page of this lane's key of unit j (a unit past the part: none)
+    auto look = [&](int j) -> int {
+      if (j >= je) return -1;
+      const int key = base(j) + l32;
+      if (!wanted(key)) return -1;
+      if constexpr (PAGED) return a.table[b * a.ldt + key / a.page];
+      return 0;
+    };
+    const uint16_t* kb = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
+    const uint16_t* vb = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
+    // unit j on its way into the ring; returns its keys that are there, a bit each
+    auto issue = [&](int j, int entry, int at) -> uint32_t {
+      const int key = base(j) + l32;
+      const bool ok = PAGED ? (uint32_t)entry < (uint32_t)a.pages : entry >= 0;
+      const uint32_t there = (uint32_t)__ballot(ok);
+      const int row = PAGED ? key - key / a.page * a.page : key;
+      const uint16_t *pk[LPU], *pv[LPU];
+#pragma unroll
+      for (int i = 0; i < LPU; ++i) {
+        const int x = i * RPL + lane / CH, ck = (lane % CH) ^ Lds<DP>::swk(x), cv = (lane % CH) ^ Lds<DP>::swv(x);
+        const uint32_t page = PAGED ? (uint32_t)__shfl(entry, x, 64) : 0, place = (uint32_t)__shfl(row, x, 64);
+        const bool in = there >> x & 1;
+        int64_t ofk = (uint64_t)place * (uint32_t)a.skt, ofv = (uint64_t)place * (uint32_t)a.svt;
+        if constexpr (PAGED) ofk += (uint64_t)page * (uint32_t)a.skp, ofv += (uint64_t)page * (uint32_t)a.svp;
+        pk[i] = in && ck * 8 < a.D ? kb + ofk + ck * 8 : reinterpret_cast<const uint16_t*>(&kZeros);
+        pv[i] = in && cv * 8 < a.D ? vb + ofv + cv * 8 : reinterpret_cast<const uint16_t*>(&kZeros);
+      }
+      typedef const __attribute__((address_space(1))) void* gp;
+#pragma unroll
+      for (int i = 0; i < LPU; ++i)
+        __builtin_amdgcn_global_load_lds((gp)pk[i], (SS_LDS void*)(ring + at + i * 1024), 16, 0, 0);
+#pragma unroll
+      for (int i = 0; i < LPU; ++i)
+        __builtin_amdgcn_global_load_lds((gp)pv[i], (SS_LDS void*)(ring + at + KB + i * 1024), 16, 0, 0);
+      return there;
+    };
+
+    int j = j0 + wave;
+    int entry = look(j), ahead = look(j + FW);
+    uint32_t there = 0, there_next = 0;
+    if (j < je) there = issue(j, entry, 0);
+    v8bf qf[KST];
+    {
+      const uint16_t* p = a.q + (s.q0 + r / a.G) * a.sqt + (int64_t)(kvh * a.G + r % a.G) * a.sqh;
+#pragma unroll
+      for (int i = 0; i < KST; ++i) {
+        const int c = 2 * i + h;
+        v4u x = {0, 0, 0, 0};
+        if (DP == a.D || c * 8 < a.D) x = *reinterpret_cast<const v4u*>(p + c * 8);
+        qf[i] = __builtin_bit_cast(v8bf, x);
+      }
+    }
+    v16f O[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) O[d] = v16f{};
+    float m = kLow, l = 0.0f;
+    bool careful = false;  // some row's maximum is big
+
+    int at = 0;
+#pragma unroll 1
+    for (; j < je; j += FW) {
+      entry = ahead;
+      ahead = look(j + 2 * FW);
+      if (j + FW < je) {
+        there_next = issue(j + FW, entry, RING / FR - at);
+        // unit j has landed when only the loads just issued are outstanding (loads complete in order)
+        __builtin_amdgcn_s_waitcnt(vm(2 * LPU));
+      } else {
+        __builtin_amdgcn_s_waitcnt(vm(0));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const SS_LDS uint8_t* kt = ring + at;
+      const SS_LDS uint8_t* vt = kt + KB;
+      const int vo = at + KB;
+      at = RING / FR - at;
+      v16f S = v16f{};
+#pragma unroll
+      for (int i = 0; i < KST; ++i) {
+        const v8bf kf = *reinterpret_cast<const SS_LDS v8bf*>(kt + l32 * DP * 2 + ((2 * i + h) ^ Lds<DP>::swk(l32)) * 16);
+        S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], S, 0, 0, 0);
+      }
+      const int k0 = base(j);
+      const bool seen = uni(there) == -1 && k0 + 32 <= kmin && (k0 >= khigh || k0 + 32 <= sinks);  // by every row, whole
+      if (!seen) {
+        const int hi = row_lim - k0 - 4 * h, lo = row_low - k0 - 4 * h, sk = sinks - k0 - 4 * h;
+        const uint32_t bits = there >> (4 * h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = 8 * (i / 4) + i % 4;
+          if (e >= hi || (e < lo && e >= sk) || !(bits >> e & 1)) S[i] = -INFINITY;
+        }
+      }
+      float mt = S[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) mt = fmaxf(mt, S[i]);
+      if (__any(mt * a.c > m + kSlack)) {
+        const float mn = fmaxf(m, pair_max(mt) * a.c), f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) O[d][i] *= f;
+        careful = __any(is_big(m));
+      }
+      float pc = a.c, pm = m;  // a power is 2^(pc S - pm)
+      if (__builtin_expect(careful, 0)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i] = S[i] * a.c - m;
+        pc = 1.0f, pm = 0.0f;
+      }
+      if (tokens && !seen) {  // keys were loaded that some row does not see
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < LPU; ++i) {
+          const v4u w = *reinterpret_cast<const SS_LDS v4u*>(vt + (i * 64 + lane) * 16);
+          odd |= odd_bf16x2(w[0]) | odd_bf16x2(w[1]) | odd_bf16x2(w[2]) | odd_bf16x2(w[3]);
+        }
+        if (__builtin_expect(__any(odd != 0), 0)) {
+          add_odd_between<DP>(O, vt, row_low - k0, row_lim - k0, sinks - k0, h);
+#pragma unroll 1
+          for (int i = 0; i < LPU; ++i) {
+            SS_LDS v4u* p = (SS_LDS v4u*)(ring + vo + (i * 64 + lane) * 16);
+            const v4u w = *p;
+            *p = v4u{even_out(w[0]), even_out(w[1]), even_out(w[2]), even_out(w[3])};
+          }
+          __builtin_amdgcn_s_waitcnt(0xC07F);
+          asm volatile("" ::: "memory");  // the reads below stay below
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      v8bf P[2];
+      {
+        v4u pk[2];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i], pc, -pm));
+          const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i + 1], pc, -pm));
+          sum += x + y;
+          pk[i / 8][(i % 8) / 2] = pack_bf16x2(x, y);
+        }
+        l += sum;
+        P[0] = __builtin_bit_cast(v8bf, pk[0]);
+        P[1] = __builtin_bit_cast(v8bf, pk[1]);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          const int ra = kk * 16 + vrow, rb = ra + 8, c = d * 4 + vcol;
+          const v4s x = read_tr((const SS_LDS uint8_t*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
+          const v4s y = read_tr((const SS_LDS uint8_t*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
+          const v8bf vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+          O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, P[kk], O[d], 0, 0, 0);
+        }
+      there = there_next;
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // this unit's LDS reads are done before its slot is filled again
+      __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // join the waves: a wave's O goes through its own ring, scaled to the workgroup's maximum
+    if (h == 0) red[wave][0][l32] = m;
+    const float lt = pair_sum(l);
+    if (h == 0) red[wave][1][l32] = lt;
+    __syncthreads();
+    float M = red[0][0][l32];
+#pragma unroll
+    for (int w = 1; w < FW; ++w) M = fmaxf(M, red[w][0][l32]);
+    if (l32 < rows) {
+      const float f = __builtin_amdgcn_exp2f(m - M);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          typedef float v4f __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<SS_LDS v4f*>(ring + l32 * OST + (d * 32 + 8 * g + 4 * h) * 4) =
+              v4f{O[d][4 * g] * f, O[d][4 * g + 1] * f, O[d][4 * g + 2] * f, O[d][4 * g + 3] * f};
+        }
+    }
+    __syncthreads();
+    const bool cut = !a.whole && take < un;
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (first ? 0 : 1);
+    if (cut && j0 == 0 && threadIdx.x == 0) {  // the tile begins here: who else has parts of it
+      Record& rec = ws.rec[blockIdx.x];
+      rec.slot = first ? 0 : 1;
+      rec.rows = rows;
+      rec.kvh = kvh;
+      rec.r0 = r0;
+      rec.q0 = s.q0;
+      rec.parts = 1 + (int)((un - take + run - 1) / run);
+    }
+    const int quads = a.D / 4;
+    for (int i = threadIdx.x; i < rows * quads; i += 64 * FW) {
+      const int row = i / quads, c = (i - row * quads) * 4;
+      float M2 = red[0][0][row], L = 0.0f;
+#pragma unroll
+      for (int w = 1; w < FW; ++w) M2 = fmaxf(M2, red[w][0][row]);
+#pragma unroll
+      for (int w = 0; w < FW; ++w) L += red[w][1][row] * __builtin_amdgcn_exp2f(red[w][0][row] - M2);
+      float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < FW; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(smem + w * RING + row * OST + c * 4);
+        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      const float lg = L == 0.0f ? -INFINITY : M2 + __builtin_amdgcn_logf(L);  // log2 of the row's sum
+      if (cut) {
+        *reinterpret_cast<float4*>(ws.part + (slot * ws.rows + row) * a.D + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (c == 0) ws.lg[slot * FM + row] = lg;
+      } else {
+        const int rr = r0 + row, head = kvh * a.G + rr % a.G;
+        const int64_t tok = s.q0 + rr / a.G;
+        *reinterpret_cast<uint2*>(a.o + tok * a.sot + head * a.soh + c) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (a.lse && c == 0) a.lse[head * a.Tq + tok] = lg * 0.69314718056f;
+      }
+    }
+
+    s0 += take;
+    if (s0 >= s1) break;
+    __syncthreads();  // the rings and sums are free again
+    first = false;
+    j0 = 0;
+    if (++th == (int64_t)tiles * a.Hkv) {
+      th = 0;
+      do {
+        if (++b >= a.B) return;
+        s = load_seq<PAGED>(a, b);
+        tiles = tiles_of(s.lq, a.G);
+      } while (tiles == 0);
+      un = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
+    }
+  }
+}
+
+// o = sum_s w_s part_s, w_s = 2^(lg_s - max) / sum of them, for the tile that begins in workgroup blockIdx.x's run and
+// ends in a later one: part 0 lies in the record's place, the others in the first places of the workgroups behind it. 16 bytes a
+// thread, the parts dealt over groups of threads, in flight together, and added in LDS in a fixed order.
+__global__ __launch_bounds__(256) void join_kernel(FlatArgs a, Parts ws) {
+  constexpr int kPre = 4;
+  __shared__ float4 acc[256];
+  const Record rec = ws.rec[blockIdx.x];
+  if (rec.parts == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int quads = a.D / 4, groups = 256 / quads, g = threadIdx.x / quads, c = threadIdx.x % quads;
+  auto slot = [&](int s) { return s == 0 ? (int64_t)blockIdx.x * 2 + rec.slot : ((int64_t)blockIdx.x + s) * 2; };
+  for (int row = blockIdx.y; row < rec.rows; row += gridDim.y) {
+    float M = -INFINITY;
+    for (int s = lane; s < rec.parts; s += 64) M = fmaxf(M, ws.lg[slot(s) * FM + row]);
+    M = wave_max(M);
+    auto power = [&](float l) { return l == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(l - M); };  // (of a NaN: NaN)
+    float sum = 0.0f;
+    for (int s = lane; s < rec.parts; s += 64) sum += power(ws.lg[slot(s) * FM + row]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    float4 o = make_float4(0, 0, 0, 0);
+    if (g < groups) {
+      for (int s0 = g; s0 < rec.parts; s0 += kPre * groups) {
+        float lp[kPre];
+        float4 xp[kPre];
+#pragma unroll
+        for (int i = 0; i < kPre; ++i) {
+          const int64_t at = slot(min(s0 + i * groups, rec.parts - 1));
+          lp[i] = ws.lg[at * FM + row];
+          xp[i] = *reinterpret_cast<const float4*>(ws.part + (at * ws.rows + row) * a.D + c * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < kPre; ++i) {
+          if (s0 + i * groups >= rec.parts) break;
+          const float w = power(lp[i]) * inv;
+          o.x += w * xp[i].x; o.y += w * xp[i].y; o.z += w * xp[i].z; o.w += w * xp[i].w;
+        }
+      }
+    }
+    acc[threadIdx.x] = o;
+    __syncthreads();
+    const int rr = rec.r0 + row, head = rec.kvh * a.G + rr % a.G;
+    const int64_t tok = rec.q0 + rr / a.G;
+    if (threadIdx.x < quads) {
+      for (int k = 1; k < groups; ++k) {
+        const float4 x = acc[k * quads + threadIdx.x];
+        o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+      }
+      *reinterpret_cast<uint2*>(a.o + tok * a.sot + head * a.soh + threadIdx.x * 4) =
+          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    }
+    if (a.lse && threadIdx.x == 0)
+      a.lse[head * a.Tq + tok] = sum == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(sum)) * 0.69314718056f;
+    __syncthreads();
+  }
+}
+
+// Workgroups of a call, and whether it leaves its tiles whole (then no workspace and one launch): rows over so few keys that
+// a workgroup's least run holds them. The lengths are not known here: the rule goes by the room for keys.
+struct Plan {
+  int64_t wgs;
+  bool whole;
+  int rows;
+};
+inline Plan plan(int64_t Tq, int64_t room, int64_t B, int64_t G, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
+  const int64_t units = units_of((int)window, (int)sinks, (int)G, (int)Tq, (int)std::min<int64_t>(room, 0x7FFFFF00));
+  const int64_t tiles = (Tq * G / FM + B) * Hkv, fits = (D <= 64 ? 4 : 2) * (int64_t)num_cus_p();
+  const bool whole = units <= kMinUnits;
+  const int64_t wgs = whole ? std::min<int64_t>(tiles, 4 * fits)
+                            : std::min<int64_t>(fits, (int64_t)std::min<double>((double)tiles * units / kMinUnits + 1, 1e9));
+  return {std::max<int64_t>(wgs, 1), whole, (int)std::min<int64_t>(FM, Tq * G)};
+}
+
+template <int DP, bool PAGED> hipError_t launch(FlatArgs a, int64_t room, void* ws, hipStream_t st) {
+  const Plan p = plan(a.Tq, room, a.B, a.G, a.Hkv, a.D, a.window, a.sinks);
+  constexpr int lds = FW * FR * 2 * 32 * DP * 2;
+  const hipError_t e = lds_limit((const void*)flat_kernel<DP, PAGED>, lds);
+  if (e != hipSuccess) return e;
+  a.whole = p.whole;
+  const Parts parts = parts_of(ws, p.wgs, p.rows);
+  hipLaunchKernelGGL((flat_kernel<DP, PAGED>), dim3((unsigned)p.wgs), dim3(64 * FW), lds, st, a, parts);
+  if (const hipError_t f = hipGetLastError(); f != hipSuccess || p.whole) return f;
+  hipLaunchKernelGGL(join_kernel, dim3((unsigned)p.wgs, (unsigned)std::min(p.rows, kJoin)), dim3(256), 0, st, a, parts);
+  return hipGetLastError();
+}
+
+}  // namespace flat
+
+int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
+  const flat::Plan p = flat::plan(Tq, room, B, Hq / Hkv, Hkv, D, window, sinks);
+  return p.whole ? 0 : p.wgs * ((int64_t)sizeof(flat::Record) + 2 * flat::FM * 4 + 2 * p.rows * D * 4);
+}
+
+hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st) {
+  if (a.paged) return a.D <= 64 ? flat::launch<64, true>(a, room, ws, st) : flat::launch<128, true>(a, room, ws, st);
+  return a.D <= 64 ? flat::launch<64, false>(a, room, ws, st) : flat::launch<128, false>(a, room, ws, st);
+}
+
+}  // namespace ss

@@ -631,26 +631,59 @@ ss_status ss_rotary(const void* x, ss_dtype x_dt, int64_t T, int64_t H, int64_t 
   return hip_status(ss::launch_rotary(x_dt == SS_BF16, a, (hipStream_t)stream), "ss_rotary launch");
 }
 
-int64_t ss_attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+namespace {
+
+constexpr int64_t kMostWindow = 1 << 30;  // wider windows, and more first tokens, than any sequence has keys
+
+int64_t attn_workspace(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   if (Tq < 0 || Tk < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || (Hkv > 0 && Hq % Hkv != 0)) return -1;
   if (Tq == 0 || Tk == 0 || B == 0 || Hq == 0 || Hkv == 0 || D == 0) return 0;
   if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || B > 0x7FFFFFFF || Hq > 0xFFFF || D > 128 || Tq * (Hq / Hkv) > 0x7FFFFF00LL)
     return -1;
-  return ss::attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
+  return ss::attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, window, sinks);
 }
 
-ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
-                  int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
-                  int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
-                  const int32_t* k_len, float scale, int causal, void* workspace, int64_t ws_bytes, void* stream) {
-  if (Tq < 0 || Tk < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ws_bytes < 0) return fail(SS_ERR_SHAPE, "negative size");
-  if (Tq == 0 || B == 0 || Hq == 0) return ok();
+// What every attention call asks of its heads, scale and window (window and sinks are clamped).
+ss_status check_heads(int64_t Hq, int64_t Hkv, int64_t D, float scale, int causal, int64_t* window, int64_t* sinks) {
   if (Hkv == 0 || Hq % Hkv != 0)
     return fail(SS_ERR_SHAPE, "%lld query heads do not divide into %lld key heads", (long long)Hq, (long long)Hkv);
   if (D < 8 || D > 128 || D % 8 != 0) return fail(SS_ERR_UNSUPPORTED, "D=%lld must be a multiple of 8 within 8..128", (long long)D);
   if (!(scale > 0) || !std::isfinite(scale * 1.5f)) return fail(SS_ERR_SHAPE, "scale must be positive and finite");
+  if (*window < 0 || *sinks < 0) return fail(SS_ERR_SHAPE, "window and sinks must not be negative");
+  if (*window > 0 && !causal) return fail(SS_ERR_UNSUPPORTED, "a window needs the causal mask");
+  *window = *window < kMostWindow ? *window : kMostWindow;
+  *sinks = *window == 0 ? 0 : *sinks < kMostWindow ? *sinks : kMostWindow;
+  return SS_OK;
+}
+
+struct Op { const char* name; const void* p; int64_t st, sh; bool used; };
+ss_status check_rows(const Op& t) {
+  if (!t.used) return SS_OK;
+  if (!t.p) return fail(SS_ERR_NULL, "%s is NULL", t.name);
+  if (t.st < 0 || t.sh < 0) return fail(SS_ERR_SHAPE, "%s: negative stride", t.name);
+  if (!aligned16(t.p) || t.st % 8 || t.sh % 8)
+    return fail(SS_ERR_ALIGN, "%s: pointer and strides must be 16-byte aligned", t.name);
+  return SS_OK;
+}
+
+ss_status check_workspace(const void* workspace, int64_t ws_bytes, int64_t need) {
+  if (need <= 0) return SS_OK;
+  if (!workspace) return fail(SS_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+  if (!aligned16(workspace)) return fail(SS_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (ws_bytes < need) return fail(SS_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  return SS_OK;
+}
+
+ss_status attn_call(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                    int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
+                    int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
+                    const int32_t* k_len, float scale, int causal, int64_t window, int64_t sinks, void* workspace,
+                    int64_t ws_bytes, void* stream) {
+  if (Tq < 0 || Tk < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ws_bytes < 0) return fail(SS_ERR_SHAPE, "negative size");
+  if (Tq == 0 || B == 0 || Hq == 0) return ok();
+  if (const ss_status s = check_heads(Hq, Hkv, D, scale, causal, &window, &sinks); s != SS_OK) return s;
   if (Tq > 0x7FFFFFFF || Tk > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL ||
-      !ss::attn_fits(Tq, Tk, B, Hq, Hkv))
+      !ss::attn_fits(Tq, Tk, B, Hq, Hkv, window, sinks))
     return fail(SS_ERR_SHAPE, "too large");
   if ((!cu_q || !cu_k) && B != 1) return fail(SS_ERR_NULL, "cu_q and cu_k are required with %lld sequences", (long long)B);
   // the stride of a single token or head is never taken
@@ -658,26 +691,16 @@ ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_
   if (Tk <= 1) skt = svt = D;
   if (Hq <= 1) sqh = soh = D;
   if (Hkv <= 1) skh = svh = D;
-  struct Op { const char* name; const void* p; int64_t st, sh; bool used; };
   for (const Op& t : {Op{"q", q, sqt, sqh, true}, Op{"k", k, skt, skh, Tk > 0}, Op{"v", v, svt, svh, Tk > 0},
-                      Op{"o", o, sot, soh, true}}) {
-    if (!t.used) continue;
-    if (!t.p) return fail(SS_ERR_NULL, "%s is NULL", t.name);
-    if (t.st < 0 || t.sh < 0) return fail(SS_ERR_SHAPE, "%s: negative stride", t.name);
-    if (!aligned16(t.p) || t.st % 8 || t.sh % 8)
-      return fail(SS_ERR_ALIGN, "%s: pointer and strides must be 16-byte aligned", t.name);
-  }
+                      Op{"o", o, sot, soh, true}})
+    if (const ss_status s = check_rows(t); s != SS_OK) return s;
   if (sot < D || soh < D) return fail(SS_ERR_SHAPE, "o: strides below D=%lld", (long long)D);
   // a tile's lane offsets are 32-bit
   if (Tk > 0 && (skt >= (1 << 24) || svt >= (1 << 24))) return fail(SS_ERR_UNSUPPORTED, "token strides of k and v must be below 2^24");
   if ((uintptr_t)cu_q % 4 || (uintptr_t)cu_k % 4 || (uintptr_t)k_len % 4 || (uintptr_t)lse % 4)
     return fail(SS_ERR_ALIGN, "a pointer is not aligned to its elements");
-  const int64_t need = ss::attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
-  if (need > 0) {
-    if (!workspace) return fail(SS_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
-    if (!aligned16(workspace)) return fail(SS_ERR_ALIGN, "workspace is not 16-byte aligned");
-    if (ws_bytes < need) return fail(SS_ERR_SHAPE, "workspace of %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
-  }
+  const int64_t need = ss::attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, window, sinks);
+  if (const ss_status s = check_workspace(workspace, ws_bytes, need); s != SS_OK) return s;
   ss::AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -696,7 +719,205 @@ ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_
   a.D = (int)D;
   a.c = scale * 1.44269504088896340736f;
   a.causal = causal != 0;
+  a.window = (int)window;
+  a.sinks = (int)sinks;
   return hip_status(ss::launch_attn(a, need > 0 ? workspace : nullptr, (hipStream_t)stream), "ss_attn launch");
+}
+
+// A paged cache and its table for B sequences; `s`: the strides as the kernels take them (of a single page, key or head,
+// which are never taken, those of adjacent rows). `write`: its rows must not overlap.
+ss_status check_paged(const ss_paged_kv* kv, int64_t Hkv, int64_t D, int64_t B, bool write, ss_paged_kv* s) {
+  if (!kv) return fail(SS_ERR_NULL, "the cache is NULL");
+  *s = *kv;
+  if (s->pages < 0 || s->page < 1 || s->table_cols < 0) return fail(SS_ERR_SHAPE, "cache: pages, page or table_cols is out of range");
+  if (s->pages > 0x7FFFFFFF || s->page > 0x7FFFFFFF || s->table_cols > 0x7FFFFFFF) return fail(SS_ERR_SHAPE, "cache: too large");
+  if (Hkv <= 1) s->skh = s->svh = D;
+  if (s->page <= 1) s->skt = s->svt = D;
+  if (s->pages <= 1) s->skp = s->svp = D;
+  for (const Op& t : {Op{"k pages", s->k, s->skt, s->skh, s->pages > 0}, Op{"v pages", s->v, s->svt, s->svh, s->pages > 0},
+                      Op{"k pages", s->k, s->skp, s->skh, s->pages > 0}, Op{"v pages", s->v, s->svp, s->svh, s->pages > 0}})
+    if (const ss_status e = check_rows(t); e != SS_OK) return e;
+  for (int64_t x : {s->skp, s->svp}) if (x > 0xFFFFFFFFLL) return fail(SS_ERR_UNSUPPORTED, "cache: page strides must be below 2^32");
+  for (int64_t x : {s->skt, s->svt}) if (x >= (1 << 24)) return fail(SS_ERR_UNSUPPORTED, "cache: key strides must be below 2^24");
+  if (write && s->pages > 0)
+    for (int64_t x : {s->skp, s->svp, s->skt, s->svt, s->skh, s->svh})
+      if (x < D) return fail(SS_ERR_SHAPE, "cache: a stride below D=%lld", (long long)D);
+  if (s->table_cols > 0) {
+    if (!s->table) return fail(SS_ERR_NULL, "table is NULL");
+    if ((uintptr_t)s->table % 4) return fail(SS_ERR_ALIGN, "table is not aligned to its elements");
+    if (B > 1 && s->table_ld < s->table_cols)
+      return fail(SS_ERR_SHAPE, "table: leading dimension %lld < %lld columns", (long long)s->table_ld, (long long)s->table_cols);
+  }
+  if (B <= 1) s->table_ld = s->table_cols;
+  return SS_OK;
+}
+
+}  // namespace
+
+int64_t ss_attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  return attn_workspace(Tq, Tk, B, Hq, Hkv, D, 0, 0);
+}
+
+ss_status ss_attn(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                  int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
+                  int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
+                  const int32_t* k_len, float scale, int causal, void* workspace, int64_t ws_bytes, void* stream) {
+  return attn_call(q, sqt, sqh, k, skt, skh, v, svt, svh, o, sot, soh, lse, Tq, Tk, B, Hq, Hkv, D, cu_q, cu_k, k_len, scale,
+                   causal, 0, 0, workspace, ws_bytes, stream);
+}
+
+int64_t ss_attn_window_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                                       int64_t sinks) {
+  if (window < 0 || sinks < 0) return -1;
+  window = window < kMostWindow ? window : kMostWindow;
+  return attn_workspace(Tq, Tk, B, Hq, Hkv, D, window, window == 0 ? 0 : sinks < kMostWindow ? sinks : kMostWindow);
+}
+
+ss_status ss_attn_window(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                         int64_t svt, int64_t svh, void* o, int64_t sot, int64_t soh, float* lse, int64_t Tq, int64_t Tk,
+                         int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q, const int32_t* cu_k,
+                         const int32_t* k_len, float scale, int causal, int64_t window, int64_t sinks, void* workspace,
+                         int64_t ws_bytes, void* stream) {
+  return attn_call(q, sqt, sqh, k, skt, skh, v, svt, svh, o, sot, soh, lse, Tq, Tk, B, Hq, Hkv, D, cu_q, cu_k, k_len, scale,
+                   causal, window, sinks, workspace, ws_bytes, stream);
+}
+
+ss_status ss_rmsnorm_act(const void* X, ss_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                         void* sum, int64_t lds, const void* w, ss_dtype w_dt, double eps, int n, ss_dtype y_dt, void* Y,
+                         int64_t ldy, float* sx, void* stream) {
+  if (n < 2 || n > 8) return fail(SS_ERR_PATTERN, "n=%d outside 2..8", n);
+  if (x_dt != SS_F32 && x_dt != SS_BF16) return fail(SS_ERR_DTYPE, "input must be F32 or BF16");
+  if (y_dt != SS_BF16 && y_dt != SS_I8 && y_dt != SS_FP8E4M3) return fail(SS_ERR_DTYPE, "output must be BF16, I8 or FP8E4M3");
+  if (w && w_dt != SS_F32 && w_dt != x_dt) return fail(SS_ERR_DTYPE, "weights must be F32 or of the input's type");
+  if (y_dt == SS_BF16 && n != 2) return fail(SS_ERR_PATTERN, "a BF16 output has no lift (n=%d)", n);
+  if (y_dt == SS_BF16 && sx) return fail(SS_ERR_DTYPE, "a BF16 output has no scales");
+  if (!(eps >= 0) || !std::isfinite(eps)) return fail(SS_ERR_SHAPE, "eps must be finite and not negative");
+  if (M < 0 || K < 0) return fail(SS_ERR_SHAPE, "negative size");
+  if (M > 0x7FFFFFFF || K > 0x7FFFFFF) return fail(SS_ERR_SHAPE, "too large");
+  if (M == 0 || K == 0) return ok();
+  const int64_t Kc = y_dt == SS_BF16 ? K : ss_lifted_k(K, n);
+  const int es = esize(x_dt);
+  ss_status s;
+  if ((s = check_mat("X", X, M, K, ldx, es)) != SS_OK) return s;
+  if (residual) {
+    if ((s = check_mat("residual", residual, M, K, ldr, es)) != SS_OK) return s;
+    if ((s = check_mat("sum", sum, M, K, lds, es)) != SS_OK) return s;
+    if ((sum == X && lds != ldx) || (sum == residual && lds != ldr))
+      return fail(SS_ERR_SHAPE, "sum: in place needs the input's leading dimension");
+  } else if (sum) {
+    return fail(SS_ERR_UNSUPPORTED, "sum without a residual");
+  }
+  if ((s = check_mat("Y", Y, M, Kc, ldy, esize(y_dt))) != SS_OK) return s;
+  if (Y == X || (residual && (Y == residual || Y == sum))) return fail(SS_ERR_UNSUPPORTED, "Y must not overlap another operand");
+  if (y_dt != SS_BF16 && !sx) return fail(SS_ERR_NULL, "sx is NULL");
+  if (w && !aligned16(w)) return fail(SS_ERR_ALIGN, "w is not 16-byte aligned");
+  ss::NormArgs a{};
+  a.x = X; a.res = residual; a.w = w; a.sum = sum; a.y = Y; a.sx = sx;
+  a.M = M; a.K = K; a.Kc = Kc; a.ldx = ldx; a.ldr = ldr; a.lds = lds; a.ldy = ldy;
+  a.eps = eps;
+  a.n = n;
+  return hip_status(ss::launch_rmsnorm(x_dt == SS_BF16, w && w_dt == SS_BF16, out_code(y_dt), a, (hipStream_t)stream),
+                    "ss_rmsnorm_act launch");
+}
+
+ss_status ss_paged_store(const void* q, int64_t sqt, int64_t sqh, const void* k, int64_t skt, int64_t skh, const void* v,
+                         int64_t svt, int64_t svh, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* pos,
+                         const int32_t* cu, const uint64_t* steps, int64_t rot_dim, ss_rope_layout layout, float mscale,
+                         void* qo, int64_t sot, int64_t soh, const ss_paged_kv* cache, void* stream) {
+  if (T < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0) return fail(SS_ERR_SHAPE, "negative size");
+  if (layout != SS_ROPE_HALF && layout != SS_ROPE_INTERLEAVED) return fail(SS_ERR_UNSUPPORTED, "unknown layout %d", (int)layout);
+  if (T == 0 || B == 0 || Hkv == 0 || D == 0) return ok();
+  if (D % 8 != 0) return fail(SS_ERR_UNSUPPORTED, "D=%lld must be a multiple of 8", (long long)D);
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0)
+    return fail(SS_ERR_SHAPE, "rot_dim=%lld must be even and within 0..%lld", (long long)rot_dim, (long long)D);
+  if (rot_dim == 0 && Hq > 0) return fail(SS_ERR_UNSUPPORTED, "query heads without a turn");
+  if (!std::isfinite(mscale)) return fail(SS_ERR_SHAPE, "mscale must be finite");
+  if (!cu && B != T) return fail(SS_ERR_NULL, "cu is required unless every sequence has one token");
+  if (T > 0x7FFFFFFF || B > 0x7FFFFFF || D > 0xFFFF || Hq > 0xFFFF || Hkv > 0xFFFF || (Hq + 2 * Hkv) * D > 0x7FFFFFF)
+    return fail(SS_ERR_SHAPE, "too large");
+  // the stride of a single token or head is never taken
+  if (T == 1) sqt = skt = svt = sot = D;
+  if (Hq <= 1) sqh = soh = D;
+  if (Hkv == 1) skh = svh = D;
+  for (const Op& t : {Op{"q", q, sqt, sqh, Hq > 0}, Op{"k", k, skt, skh, true}, Op{"v", v, svt, svh, true},
+                      Op{"the turned queries", qo, sot, soh, Hq > 0}}) {
+    if (!t.used) continue;
+    if (!t.p) return fail(SS_ERR_NULL, "%s: NULL", t.name);
+    if (t.st < 0 || t.sh < 0) return fail(SS_ERR_SHAPE, "%s: negative stride", t.name);
+    if ((uintptr_t)t.p % 2) return fail(SS_ERR_ALIGN, "%s: not aligned to its elements", t.name);
+  }
+  if (Hq > 0 && (sot < D || soh < D)) return fail(SS_ERR_SHAPE, "the turned queries: strides below D=%lld", (long long)D);
+  if (Hq > 0 && q == qo && (sqt != sot || sqh != soh)) return fail(SS_ERR_SHAPE, "in place needs equal strides");
+  if (!pos || (rot_dim > 0 && !steps)) return fail(SS_ERR_NULL, "pos and steps are required");
+  if ((uintptr_t)pos % 4 || (uintptr_t)cu % 4 || (uintptr_t)steps % 8) return fail(SS_ERR_ALIGN, "a pointer is not aligned to its elements");
+  ss_paged_kv c;
+  if (const ss_status s = check_paged(cache, Hkv, D, B, true, &c); s != SS_OK) return s;
+  ss::StoreArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.qo = static_cast<uint16_t*>(qo);
+  a.kc = static_cast<uint16_t*>(c.k);
+  a.vc = static_cast<uint16_t*>(c.v);
+  a.pos = pos; a.cu = cu; a.table = c.table; a.steps = steps;
+  a.T = T; a.B = B; a.ldt = c.table_ld;
+  a.sqt = sqt; a.sqh = sqh; a.skt = skt; a.skh = skh; a.svt = svt; a.svh = svh; a.sot = sot; a.soh = soh;
+  a.kp = c.skp; a.kt = c.skt; a.kh = c.skh; a.vp = c.svp; a.vt = c.svt; a.vh = c.svh;
+  a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.D = (int)D; a.rot = (int)rot_dim; a.half = layout == SS_ROPE_HALF;
+  a.cols = (int)c.table_cols; a.pages = (int)c.pages; a.page = (int)c.page;
+  a.mscale = mscale;
+  return hip_status(ss::launch_paged_store(a, (hipStream_t)stream), "ss_paged_store launch");
+}
+
+int64_t ss_attn_paged_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                                      int64_t sinks) {
+  if (Tq < 0 || room < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || (Hkv > 0 && Hq % Hkv != 0) || window < 0 || sinks < 0) return -1;
+  if (Tq == 0 || B == 0 || Hq == 0 || Hkv == 0 || D == 0) return 0;
+  if (Tq > 0x7FFFFFFF || B > 0x7FFFFFFF || Hq > 0xFFFF || D > 128 || Tq * (Hq / Hkv) > 0x7FFFFF00LL) return -1;
+  window = window < kMostWindow ? window : kMostWindow;
+  return ss::flat_workspace_bytes(Tq, room, B, Hq, Hkv, D, window, window == 0 ? 0 : sinks < kMostWindow ? sinks : kMostWindow);
+}
+
+ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_kv* cache, void* o, int64_t sot, int64_t soh,
+                        float* lse, int64_t Tq, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, const int32_t* cu_q,
+                        const int32_t* k_len, float scale, int causal, int64_t window, int64_t sinks, void* workspace,
+                        int64_t ws_bytes, void* stream) {
+  if (Tq < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0 || ws_bytes < 0) return fail(SS_ERR_SHAPE, "negative size");
+  if (Tq == 0 || B == 0 || Hq == 0) return ok();
+  ss_status s;
+  if ((s = check_heads(Hq, Hkv, D, scale, causal, &window, &sinks)) != SS_OK) return s;
+  if (Tq > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL) return fail(SS_ERR_SHAPE, "too large");
+  if (!cu_q && B != Tq && B != 1) return fail(SS_ERR_NULL, "cu_q is required unless every sequence has one token");
+  if (Tq == 1) sqt = sot = D;
+  if (Hq == 1) sqh = soh = D;
+  for (const Op& t : {Op{"q", q, sqt, sqh, true}, Op{"o", o, sot, soh, true}})
+    if ((s = check_rows(t)) != SS_OK) return s;
+  if (sot < D || soh < D) return fail(SS_ERR_SHAPE, "o: strides below D=%lld", (long long)D);
+  if (!k_len) return fail(SS_ERR_NULL, "k_len is NULL");
+  if ((uintptr_t)cu_q % 4 || (uintptr_t)k_len % 4 || (uintptr_t)lse % 4) return fail(SS_ERR_ALIGN, "a pointer is not aligned to its elements");
+  ss_paged_kv c;
+  if ((s = check_paged(cache, Hkv, D, B, false, &c)) != SS_OK) return s;
+  const int64_t room = c.table_cols * c.page;
+  const int64_t need = ss::flat_workspace_bytes(Tq, room, B, Hq, Hkv, D, window, sinks);
+  if ((s = check_workspace(workspace, ws_bytes, need)) != SS_OK) return s;
+  ss::FlatArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(c.k);
+  a.v = static_cast<const uint16_t*>(c.v);
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.cu_q = cu_q; a.k_len = k_len; a.table = c.table;
+  a.sqt = sqt; a.sqh = sqh; a.sot = sot; a.soh = soh;
+  a.skp = c.skp; a.skt = c.skt; a.skh = c.skh; a.svp = c.svp; a.svt = c.svt; a.svh = c.svh;
+  a.Tq = Tq; a.ldt = c.table_ld;
+  a.B = (int)B; a.Hkv = (int)Hkv; a.G = (int)(Hq / Hkv); a.D = (int)D;
+  a.pages = (int)c.pages; a.page = (int)c.page; a.cols = (int)c.table_cols;
+  a.c = scale * 1.44269504088896340736f;
+  a.causal = causal != 0;
+  a.window = (int)window;
+  a.sinks = (int)sinks;
+  a.paged = 1;
+  return hip_status(ss::launch_flat(a, room, need > 0 ? workspace : nullptr, (hipStream_t)stream), "ss_attn_paged launch");
 }
 
 }  // extern "C"

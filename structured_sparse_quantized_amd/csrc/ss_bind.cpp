@@ -1,4 +1,5 @@
-// Python binding of the calls around a layer's products: spgemm_tiled_epilogue, rotary, attn.
+// Python binding of the calls around a layer's products: spgemm_tiled_epilogue, rmsnorm_act, rotary, paged_store, attn,
+// attn_paged.
 //
 // These run between products, often on one token, where a call's own time on the host is what counts: checking the
 // tensors and marshalling some twenty arguments in Python took 7-12 us a call, the kernels 4-11 us. Here both take
@@ -15,7 +16,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <string>
+#include <utility>
 
 #include "ss.h"
 
@@ -162,10 +165,27 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (q, k, v, cu_q, cu_k, k_len, causal, scale or None, out, lse, workspace)
+// a window's width: None is none, which the C ABI writes 0
+int64_t window_of(PyObject* o) {
+  if (o == Py_None) return 0;
+  const int64_t w = integer(o);
+  if (w < 1) refuse(SS_ERR_SHAPE, "window must be None or at least 1");
+  return w;
+}
+void need_lse(const at::Tensor* lse, int64_t Hq, int64_t Tq) {
+  if (!lse) return;
+  need_type(lse, at::kFloat, "lse");
+  if (lse->dim() != 2 || lse->size(0) != Hq || lse->size(1) != Tq || !lse->is_contiguous())
+    refuse(SS_ERR_SHAPE, "lse: needs contiguous [" + std::to_string(Hq) + ", " + std::to_string(Tq) + "], has " + shape(*lse));
+}
+float scale_of(PyObject* o, int64_t D) {
+  return o == Py_None ? (float)(1.0 / std::sqrt((double)std::max<int64_t>(D, 1))) : (float)number(o);
+}
+
+// (q, k, v, cu_q, cu_k, k_len, causal, scale or None, out, lse, workspace, window or None, sinks)
 PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> at::Tensor {
-    count(n, 11);
+    count(n, 13);
     const at::Tensor *q = tensor(a[0], "q"), *k = tensor(a[1], "k"), *v = tensor(a[2], "v"),
                      *cu_q = tensor(a[3], "cu_q", true), *cu_k = tensor(a[4], "cu_k", true),
                      *k_len = tensor(a[5], "k_len", true), *out = tensor(a[8], "out", true),
@@ -180,32 +200,30 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need_type(k, at::kBFloat16, "k");
     need_type(v, at::kBFloat16, "v");
     need_type(out, at::kBFloat16, "out");
-    if (lse) {
-      need_type(lse, at::kFloat, "lse");
-      if (lse->dim() != 2 || lse->size(0) != Hq || lse->size(1) != Tq || !lse->is_contiguous())
-        refuse(SS_ERR_SHAPE, "lse: needs contiguous [" + std::to_string(Hq) + ", " + std::to_string(Tq) + "], has " + shape(*lse));
-    }
+    need_lse(lse, Hq, Tq);
     const int64_t B = cu_q ? cu_q->numel() - 1 : cu_k ? cu_k->numel() - 1 : 1;
     if (B < 0) refuse(SS_ERR_SHAPE, "cu_q and cu_k hold one value more than there are sequences");
     need_vec(cu_q, B + 1, at::kInt, "cu_q", true);
     need_vec(cu_k, B + 1, at::kInt, "cu_k", true);
     need_vec(k_len, B, at::kInt, "k_len", true);
     need_bytes(ws, 0, "workspace");
+    const float scale = scale_of(a[7], D);
+    const int64_t window = window_of(a[11]), sinks = integer(a[12]);
+    if (sinks < 0) refuse(SS_ERR_SHAPE, "sinks must not be negative");
     same_gpu(q->device(), {k, v, cu_q, cu_k, k_len, out, lse, ws});
-    const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)std::max<int64_t>(D, 1))) : (float)number(a[7]);
     const Place at(q->device());
     at::Tensor o = out ? *out : at::empty({Tq, Hq, D}, q->options());
     at::Tensor own;
     if (!ws) {
-      const int64_t need = ss_attn_workspace_bytes(Tq, Tk, B, Hq, Hkv, D);
+      const int64_t need = ss_attn_window_workspace_bytes(Tq, Tk, B, Hq, Hkv, D, window, sinks);
       if (need > 0) {
         own = at::empty({need}, q->options().dtype(at::kByte));
         ws = &own;
       }
     }
-    check(ss_attn(ptr<void>(q), q->stride(0), q->stride(1), ptr<void>(k), k->stride(0), k->stride(1), ptr<void>(v),
+    check(ss_attn_window(ptr<void>(q), q->stride(0), q->stride(1), ptr<void>(k), k->stride(0), k->stride(1), ptr<void>(v),
                   v->stride(0), v->stride(1), o.data_ptr(), o.stride(0), o.stride(1), ptr<float>(lse), Tq, Tk, B, Hq, Hkv,
-                  D, ptr<int32_t>(cu_q), ptr<int32_t>(cu_k), ptr<int32_t>(k_len), scale, truth(a[6]), ptr<void>(ws),
+                  D, ptr<int32_t>(cu_q), ptr<int32_t>(cu_k), ptr<int32_t>(k_len), scale, truth(a[6]), window, sinks, ptr<void>(ws),
                   ws ? (int64_t)ws->nbytes() : 0, at.stream));
     return o;
   });
@@ -265,6 +283,183 @@ PyObject* spgemm_tiled_epilogue(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A call's results in a tuple (None where there is none), or the exception that ended it.
+template <typename F> PyObject* guarded_tuple(F&& f) {
+  HANDLE_TH_ERRORS
+  try {
+    const auto r = f();
+    PyObject* t = PyTuple_New((Py_ssize_t)r.size());
+    if (!t) return nullptr;
+    for (size_t i = 0; i < r.size(); ++i) {
+      PyObject* x = nullptr;
+      if (r[i].defined()) {
+        x = THPVariable_Wrap(r[i]);
+      } else {
+        Py_INCREF(Py_None);
+        x = Py_None;
+      }
+      if (!x) {
+        Py_DECREF(t);
+        return nullptr;
+      }
+      PyTuple_SET_ITEM(t, (Py_ssize_t)i, x);
+    }
+    return t;
+  } catch (const Refused&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, w, eps, residual, n, y_dt, sum_out, out, scale_out) -> (y, sx or None, sum or None)
+PyObject* rmsnorm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded_tuple([&]() -> std::array<at::Tensor, 3> {
+    count(n, 9);
+    const at::Tensor *x = tensor(a[0], "x"), *w = tensor(a[1], "w", true), *res = tensor(a[3], "residual", true),
+                     *sum = tensor(a[6], "sum_out", true), *out = tensor(a[7], "out", true), *sx = tensor(a[8], "scale_out", true);
+    const int pattern = (int)std::min<int64_t>(std::max<int64_t>(integer(a[4]), -1), 99);
+    const int64_t y_code = integer(a[5]);
+    if (y_code != SS_BF16 && y_code != SS_I8 && y_code != SS_FP8E4M3) refuse(SS_ERR_DTYPE, "the output must be bf16, i8 or fp8");
+    const at::ScalarType y_type = y_code == SS_BF16 ? at::kBFloat16 : y_code == SS_I8 ? at::kChar : at::kFloat8_e4m3fn;
+    if (x->dim() != 2) refuse(SS_ERR_SHAPE, "x: needs [rows, values], has " + shape(*x));
+    const int64_t M = x->size(0), K = x->size(1);
+    const at::ScalarType type = x->scalar_type();
+    if (type != at::kBFloat16) need_type(x, at::kFloat, "x (or bf16)");
+    const ss_dtype x_dt = type == at::kBFloat16 ? SS_BF16 : SS_F32;
+    const ss_dtype w_dt = w && w->scalar_type() == at::kBFloat16 ? SS_BF16 : SS_F32;
+    if (w_dt == SS_F32) need_vec(w, K, at::kFloat, "w", true);
+    else need_vec(w, K, at::kBFloat16, "w", true);
+    const int64_t Kc = y_code == SS_BF16 ? K : ss_lifted_k(K, pattern);
+    if (Kc < 0) refuse(SS_ERR_PATTERN, "n=" + std::to_string(pattern) + " outside 2..8");
+    need_mat(x, M, K, "x");
+    for (const auto& [t, name] : {std::pair<const at::Tensor*, const char*>{res, "residual"}, {sum, "sum_out"}}) {
+      need_type(t, type, name);
+      if (t && (t->dim() != 2 || t->size(0) != M || t->size(1) != K))
+        refuse(SS_ERR_SHAPE, std::string(name) + ": needs " + shape(*x) + ", has " + shape(*t));
+      need_mat(t, M, K, name);
+    }
+    if (sum && !res) refuse(SS_ERR_UNSUPPORTED, "sum_out without a residual");
+    if (sx && y_code == SS_BF16) refuse(SS_ERR_DTYPE, "a bf16 output has no scales");
+    need_type(out, y_type, "out");
+    need_mat(out, M, Kc, "out");
+    need_vec(sx, M, at::kFloat, "scale_out");
+    same_gpu(x->device(), {w, res, sum, out, sx});
+    const Place at(x->device());
+    // rows of new tensors start on 16 bytes
+    auto rows = [&](int64_t cols, at::ScalarType t) {
+      const int64_t per = 16 / (int64_t)at::elementSize(t), ld = (cols + per - 1) / per * per;
+      const at::Tensor m = at::empty({M, ld}, x->options().dtype(t));
+      return ld == cols ? m : m.narrow(1, 0, cols);
+    };
+    at::Tensor y = out ? *out : rows(Kc, y_type), scales, total;
+    if (y_code != SS_BF16) scales = sx ? *sx : at::empty({M}, x->options().dtype(at::kFloat));
+    if (res) total = sum ? *sum : rows(K, type);
+    check(ss_rmsnorm_act(ptr<void>(x), x_dt, M, K, x->stride(0), ptr<void>(res), res ? res->stride(0) : 0,
+                         res ? total.data_ptr() : nullptr, res ? total.stride(0) : 0, ptr<void>(w), w_dt, number(a[2]), pattern,
+                         (ss_dtype)y_code, y.data_ptr(), y.stride(0),
+                         scales.defined() ? static_cast<float*>(scales.data_ptr()) : nullptr, at.stream));
+    return {y, scales, total};
+  });
+}
+
+// k_pages, v_pages [pages, page, Hkv, D], the values of a head adjacent, and table [B, columns]
+ss_paged_kv paged(const at::Tensor* k, const at::Tensor* v, const at::Tensor* table, int64_t Hkv, int64_t D, int64_t B) {
+  for (const auto& [t, name] : {std::pair<const at::Tensor*, const char*>{k, "k_pages"}, {v, "v_pages"}}) {
+    need_type(t, at::kBFloat16, name);
+    if (t->dim() != 4 || t->size(0) != k->size(0) || t->size(1) != k->size(1) || t->size(1) < 1 || t->size(2) != Hkv ||
+        t->size(3) != D || (t->stride(3) != 1 && D > 1 && t->numel() > 0))
+      refuse(SS_ERR_SHAPE, std::string(name) + ": needs [pages, page, " + std::to_string(Hkv) + ", " + std::to_string(D) +
+                               "] with unit stride along the last dimension, k_pages and v_pages alike, has " + shape(*t));
+  }
+  need_type(table, at::kInt, "table");
+  if (table->dim() != 2 || table->size(0) != B || (table->size(1) > 1 && table->numel() > 0 && table->stride(1) != 1))
+    refuse(SS_ERR_SHAPE, "table: needs a row-major [" + std::to_string(B) + ", columns], has " + shape(*table));
+  return {k->data_ptr(), v->data_ptr(), k->size(0), k->size(1), k->stride(0), k->stride(1), k->stride(2), v->stride(0), v->stride(1),
+          v->stride(2), ptr<int32_t>(table), table->size(1), table->stride(0)};
+}
+
+// (k, v, pos, k_pages, v_pages, table, cu, q, steps, layout, mscale, q_out) -> (the turned queries or None,)
+PyObject* paged_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded_tuple([&]() -> std::array<at::Tensor, 1> {
+    count(n, 12);
+    const at::Tensor *k = tensor(a[0], "k"), *v = tensor(a[1], "v"), *pos = tensor(a[2], "pos"), *kp = tensor(a[3], "k_pages"),
+                     *vp = tensor(a[4], "v_pages"), *table = tensor(a[5], "table"), *cu = tensor(a[6], "cu", true),
+                     *q = tensor(a[7], "q", true), *steps = tensor(a[8], "steps", true), *out = tensor(a[11], "q_out", true);
+    need_heads(k, "k");
+    const int64_t T = k->size(0), Hkv = k->size(1), D = k->size(2);
+    need_heads(v, T, Hkv, D, "v");
+    need_type(k, at::kBFloat16, "k");
+    need_type(v, at::kBFloat16, "v");
+    int64_t Hq = 0;
+    if (q) {
+      if (q->dim() == 3) Hq = q->size(1);
+      need_heads(q, T, Hq, D, "q");
+      need_type(q, at::kBFloat16, "q");
+      if (!steps) refuse(SS_ERR_NULL, "steps is None: q is there to be turned");
+    }
+    if (out) {
+      if (!q) refuse(SS_ERR_UNSUPPORTED, "q_out without q");
+      need_heads(out, T, Hq, D, "q_out");
+      need_type(out, at::kBFloat16, "q_out");
+    }
+    need_vec(pos, T, at::kInt, "pos", true);
+    const int64_t B = cu ? cu->numel() - 1 : T;
+    if (B < 0) refuse(SS_ERR_SHAPE, "cu holds one value more than there are sequences");
+    need_vec(cu, B + 1, at::kInt, "cu", true);
+    if (steps) need_vec(steps, steps->numel(), at::kLong, "steps", true);
+    const ss_paged_kv cache = paged(kp, vp, table, Hkv, D, B);
+    same_gpu(k->device(), {v, pos, kp, vp, table, cu, q, steps, out});
+    const Place at(k->device());
+    at::Tensor y;
+    if (q) y = out ? *out : at::empty({T, Hq, D}, q->options());
+    check(ss_paged_store(ptr<void>(q), q ? q->stride(0) : 0, q ? q->stride(1) : 0, ptr<void>(k), k->stride(0), k->stride(1),
+                         ptr<void>(v), v->stride(0), v->stride(1), T, B, Hq, Hkv, D, ptr<int32_t>(pos), ptr<int32_t>(cu),
+                         ptr<uint64_t>(steps), steps ? 2 * steps->numel() : 0, (ss_rope_layout)integer(a[9]),
+                         (float)number(a[10]), q ? y.data_ptr() : nullptr, q ? y.stride(0) : 0, q ? y.stride(1) : 0, &cache,
+                         at.stream));
+    return {y};
+  });
+}
+
+// (q, k_pages, v_pages, table, k_len, cu_q, causal, window or None, sinks, scale or None, out, lse, workspace)
+PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> at::Tensor {
+    count(n, 13);
+    const at::Tensor *q = tensor(a[0], "q"), *kp = tensor(a[1], "k_pages"), *vp = tensor(a[2], "v_pages"),
+                     *table = tensor(a[3], "table"), *k_len = tensor(a[4], "k_len"), *cu_q = tensor(a[5], "cu_q", true),
+                     *out = tensor(a[10], "out", true), *lse = tensor(a[11], "lse", true), *ws = tensor(a[12], "workspace", true);
+    need_heads(q, "q");
+    const int64_t Tq = q->size(0), Hq = q->size(1), D = q->size(2);
+    need_type(q, at::kBFloat16, "q");
+    if (kp->dim() != 4) refuse(SS_ERR_SHAPE, "k_pages: needs [pages, page, heads, values], has " + shape(*kp));
+    const int64_t Hkv = kp->size(2), B = k_len->numel();
+    need_vec(k_len, B, at::kInt, "k_len", true);
+    need_vec(cu_q, B + 1, at::kInt, "cu_q", true);
+    const ss_paged_kv cache = paged(kp, vp, table, Hkv, D, B);
+    if (out) need_heads(out, Tq, Hq, D, "out");
+    need_type(out, at::kBFloat16, "out");
+    need_lse(lse, Hq, Tq);
+    need_bytes(ws, 0, "workspace");
+    const int64_t window = window_of(a[7]), sinks = integer(a[8]);
+    if (sinks < 0) refuse(SS_ERR_SHAPE, "sinks must not be negative");
+    same_gpu(q->device(), {kp, vp, table, k_len, cu_q, out, lse, ws});
+    const Place at(q->device());
+    at::Tensor o = out ? *out : at::empty({Tq, Hq, D}, q->options());
+    at::Tensor own;
+    if (!ws) {
+      const int64_t need = ss_attn_paged_workspace_bytes(Tq, cache.table_cols * cache.page, B, Hq, Hkv, D, window, sinks);
+      if (need > 0) {
+        own = at::empty({need}, q->options().dtype(at::kByte));
+        ws = &own;
+      }
+    }
+    check(ss_attn_paged(ptr<void>(q), q->stride(0), q->stride(1), &cache, o.data_ptr(), o.stride(0), o.stride(1), ptr<float>(lse),
+                        Tq, B, Hq, Hkv, D, ptr<int32_t>(cu_q), ptr<int32_t>(k_len), scale_of(a[9], D), truth(a[6]), window, sinks,
+                        ptr<void>(ws), ws ? (int64_t)ws->nbytes() : 0, at.stream));
+    return o;
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XDECREF(g_error);
@@ -278,6 +473,9 @@ PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
 PyMethodDef methods[] = {{"rotary", fast(rotary), METH_FASTCALL, nullptr},
                          {"attn", fast(attn), METH_FASTCALL, nullptr},
                          {"spgemm_tiled_epilogue", fast(spgemm_tiled_epilogue), METH_FASTCALL, nullptr},
+                         {"rmsnorm_act", fast(rmsnorm_act), METH_FASTCALL, nullptr},
+                         {"paged_store", fast(paged_store), METH_FASTCALL, nullptr},
+                         {"attn_paged", fast(attn_paged), METH_FASTCALL, nullptr},
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ssbind", nullptr, -1, methods};

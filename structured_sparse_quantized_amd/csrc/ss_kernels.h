@@ -114,10 +114,10 @@ struct AttnArgs {
   int64_t Tq, Tk;
   int B, Hkv, G, D;  // G = query heads per key head
   float c;           // scale * log2 e
-  int causal;
+  int causal, window, sinks;  // window 0: none
 };
-int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
-bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv);  // (a launch's threads)
+int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks);
+bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t window, int64_t sinks);  // (a launch's threads)
 hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st);
 
 // Rotary positions on [T][H][D] views (strides in elements, t: token, h: head); y may be x (same strides).
@@ -132,5 +132,48 @@ struct RotaryArgs {
   float cscale, sscale;
 };
 hipError_t launch_rotary(bool bf16, const RotaryArgs& a, hipStream_t st);
+
+// Norm of token rows with the residual's addition; out: 0 = int8, 1 = fp8 (codes lifted by n, scales sx), 2 = bf16.
+struct NormArgs {
+  const void *x, *res, *w;  // res, w: or NULL
+  void *sum, *y;            // sum: where res is given
+  float* sx;
+  int64_t M, first, K, Kc, ldx, ldr, lds, ldy;  // first: of the launch's rows
+  double eps;
+  int n;
+};
+hipError_t launch_rmsnorm(bool x_bf16, bool w_bf16, int out, const NormArgs& a, hipStream_t st);
+
+// Rotary positions on queries and keys, keys and values into the pages of a cache (bf16; strides in elements).
+struct StoreArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t *qo, *kc, *vc;
+  const int32_t *pos, *cu, *table;  // cu: or NULL (one token a sequence)
+  const uint64_t* steps;
+  int64_t T, first, B, ldt;  // first: of the launch's tokens
+  int64_t sqt, sqh, skt, skh, svt, svh, sot, soh;
+  int64_t kp, kt, kh, vp, vt, vh;  // cache: page, row, head
+  int Hq, Hkv, D, rot, half, cols, pages, page;
+  float mscale;
+};
+hipError_t launch_paged_store(const StoreArgs& a, hipStream_t st);
+
+// Attention of few rows a sequence over a paged cache, or over contiguous keys under a window.
+struct FlatArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  float* lse;  // [Hq][Tq] or NULL
+  const int32_t *cu_q, *cu_k, *k_len, *table;  // table: paged; cu_k: contiguous keys
+  int64_t sqt, sqh, sot, soh;
+  int64_t skp, skt, skh, svp, svt, svh;  // page, key, head
+  int64_t Tq, Tk, ldt;
+  int B, Hkv, G, D, pages, page, cols;
+  float c;  // scale * log2 e
+  int causal, window, sinks;  // window 0: none
+  int paged;  // by table, else contiguous keys
+  int whole;  // (set by the launch)
+};
+int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks);
+hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st);
 
 }  // namespace ss
