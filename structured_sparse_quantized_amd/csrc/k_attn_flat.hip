@@ -12,10 +12,12 @@
 // finished there; of one that is cut, each workgroup leaves a part (float32, normalised, with its row's log2 of the sum),
 // a run's first tile in one place and its last in another, and join_kernel adds the parts in order.
 //
-// Loads. Units go to LDS by loads of 16 bytes a lane from addresses of its own, so that a unit's keys may lie anywhere: each of
-// 32 lanes looks up the page of one key, a unit ahead, and the lanes that load its row take it from there. What no row of the tile
-// sees (keys behind the end, outside the window, entries that name no page) is loaded from a line of zeros instead: no memory
-// behind it is read, and whatever it holds stays out of the product.
+// Loads. A unit is loaded to registers, 16 bytes a lane from addresses of its own, so that its keys may lie anywhere, while the
+// unit before it is computed, and goes to LDS when that is done: each of 32 lanes looks up the page of one key, a unit ahead,
+// and the lanes that load its row take it from there. (Loads to LDS without registers, by the same addresses, left a wave's own
+// LDS reads incomplete behind their wait while they were in flight.) What no row of the tile sees (keys
+// behind the end, outside the window, entries that name no page) is loaded from a line of zeros instead: no memory behind it is
+// read, and whatever it holds stays out of the product.
 #include <math.h>
 
 #include <algorithm>
@@ -26,7 +28,7 @@ namespace ss {
 namespace flat {
 
 using namespace attn;
-constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
+constexpr int FW = 2, FM = 32;          // waves, rows
 constexpr int kMinUnits = 4;            // a workgroup's run, at least
 constexpr int kJoin = 8;                // workgroups that share a cut tile's rows
 
@@ -92,68 +94,85 @@ __host__ __device__ inline int units_of(int window, int sinks, int G, int lq, in
   return n > 1 ? (int)n : 1;
 }
 
+// Sum over this lane and those below it, by the lanes' own exchange: each step adds what lies so many lanes down.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);   // 1 down, within rows of 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);   // 2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);   // 4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);   // 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // a row's last lane to rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // lane 31 to the upper half
+  return x;
+}
+
+// The transposing LDS read of what the wave itself has written: LDS serves a wave in order.
+__device__ __forceinline__ v4s read_columns(SS_LDS uint8_t* p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16((SS_LDS v4s*)p); }
+
+// The address, or that of zeros, without a branch over what computes it.
+__device__ __forceinline__ const uint16_t* pick(bool take, const uint16_t* p) {
+  const uint64_t mask = take ? ~0ull : 0ull;
+  return reinterpret_cast<const uint16_t*>(((uint64_t)p & mask) | ((uint64_t)&kZeros & ~mask));
+}
+
+// a wave's room in LDS holds a unit's keys and values, and at the end its rows' results
+constexpr int lds_bytes(int DP) { return FW * (2 * 32 * DP * 2 > FM * (DP * 4 + 16) ? 2 * 32 * DP * 2 : FM * (DP * 4 + 16)); }
+
 template <int DP, bool PAGED>
 __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;
-  constexpr int KB = 32 * DP * 2, UNIT = 2 * KB, RING = FR * UNIT;
-  constexpr int LPU = KB / 1024;  // 1 KB loads per unit and operand
-  constexpr int RPL = 64 / CH;    // rows of a load
-  constexpr int OST = DP * 4 + 16;
-  static_assert(FM * OST <= RING, "a wave's results fit its ring");
+  constexpr int KB = 32 * DP * 2;    // bytes of a unit's keys, and of its values
+  constexpr int LPU = KB / 1024;     // 1 KB loads per unit and operand
+  constexpr int RPL = 64 / CH;       // rows of a load
+  constexpr int OST = DP * 4 + 16;   // bytes of a joined row, padded
+  constexpr int RING = lds_bytes(DP) / FW;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[FW][2][FM];
   const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
   const int l32 = lane & 31, h = lane >> 5;
 
-  // ---- this workgroup's run -------------------------------------------------------------------------------------
-  auto weight = [&](int i) -> int64_t {
+  // ---- this workgroup's run: 64 sequences at a time, one a lane ---------------------------------------------------
+  Seq mine;
+  auto weight = [&](int i) -> int {  // units of sequence i's tiles (the host has seen to it that all fit 31 bits)
+    mine = Seq{0, 0, 0, 0};
     if (i >= a.B) return 0;
-    const Seq s = load_seq<PAGED>(a, i);
-    const int n = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
-    return (int64_t)tiles_of(s.lq, a.G) * a.Hkv * n;
+    mine = load_seq<PAGED>(a, i);
+    return tiles_of(mine.lq, a.G) * a.Hkv * (a.whole ? 1 : units_of(a.window, a.sinks, a.G, mine.lq, mine.lk));
   };
-  int64_t mine = weight(lane), total = mine;
-  for (int i = 64 + lane; i < ((a.B + 63) & ~63); i += 64) total += weight(i);
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, 64);
-  const int64_t least = a.whole ? 1 : kMinUnits;
-  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, least);
-  int64_t s0 = blockIdx.x * run;
-  const int64_t s1 = min(s0 + run, total);
+  int upto = wave_scan(weight(lane)), total = __builtin_amdgcn_readlane(upto, 63);
+  for (int c = 64; c < a.B; c += 64) total += __builtin_amdgcn_readlane(wave_scan(weight(c + lane)), 63);
+  const int run = (int)max(((uint32_t)total + gridDim.x - 1) / gridDim.x, (uint32_t)(a.whole ? 1 : kMinUnits));
+  int s0 = (int)min((int64_t)blockIdx.x * run, (int64_t)0x7FFFFFFF);
+  const int s1 = (int)min((int64_t)s0 + run, (int64_t)total);
   if (!a.whole && threadIdx.x == 0) ws.rec[blockIdx.x].parts = 0;
   if (s0 >= total) return;
-  int b = 0;
-  int64_t before = 0;  // work before sequence b
-  for (int c = 0; c < a.B; c += 64) {
-    if (c > 0) mine = weight(c + lane);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t x = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += x;
-    }
-    const uint64_t past = __ballot(before + incl > s0);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
+  int b = 0, before = 0;  // the sequence, and the work before it
+  Seq s;
+  for (int c = 0;; c += 64) {  // (ends: the work of all sequences passes s0)
+    if (a.B > 64) upto = wave_scan(weight(c + lane));
+    const uint64_t past = __ballot(before + upto > s0);
+    if (past || c + 64 >= a.B) {
+      const int l = past ? __ffsll((unsigned long long)past) - 1 : 0;
       b = c + l;
-      before += __shfl(incl - mine, l, 64);
+      if (l > 0) before += __builtin_amdgcn_readlane(upto, l - 1);
+      auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+      auto of64 = [&](int64_t x) { return (int64_t)((uint64_t)(uint32_t)of((int)(x >> 32)) << 32 | (uint32_t)of((int)x)); };
+      s = Seq{of64(mine.q0), of64(mine.k0), of(mine.lq), of(mine.lk)};
       break;
     }
-    before += __shfl(incl, 63, 64);
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
-  b = uni(b);
-  Seq s = load_seq<PAGED>(a, b);
   int tiles = tiles_of(s.lq, a.G), un = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
-  int64_t th = (s0 - before) / un;  // tile and key head in the sequence, the head fastest
-  int j0 = (int)((s0 - before) - th * un);
+  int th = (s0 - before) / un;  // tile and key head in the sequence, the head fastest
+  int j0 = (s0 - before) - th * un;
+  if ((uint32_t)th >= (uint32_t)(tiles * a.Hkv)) return;  // (bounds that decrease may overlap: more work than the host knows)
 
   const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
   SS_LDS uint8_t* ring = (SS_LDS uint8_t*)smem + wave * RING;
   bool first = true;
 #pragma unroll 1
   while (true) {
-    const int take = (int)min((int64_t)(un - j0), s1 - s0);
-    const int tile = uni((int)(th / a.Hkv)), kvh = uni((int)(th - (int64_t)tile * a.Hkv));
+    const int take = min(un - j0, s1 - s0);
+    const int tile = uni(th / a.Hkv), kvh = uni(th - tile * a.Hkv);
     const int nr = s.lq * a.G, r0 = tile * FM, rows = min(nr - r0, FM);
     auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
     auto low = [&](int r) {
@@ -179,37 +198,30 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     };
     const uint16_t* kb = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
     const uint16_t* vb = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
-    // unit j on its way into the ring; returns its keys that are there, a bit each
-    auto issue = [&](int j, int entry, int at) -> uint32_t {
+    // unit j on its way to registers; returns its keys that are there, a bit each
+    v4u kr[LPU], vr[LPU];
+    auto issue = [&](int j, int entry) __attribute__((always_inline)) -> uint32_t {
       const int key = base(j) + l32;
       const bool ok = PAGED ? (uint32_t)entry < (uint32_t)a.pages : entry >= 0;
       const uint32_t there = (uint32_t)__ballot(ok);
       const int row = PAGED ? key - key / a.page * a.page : key;
-      const uint16_t *pk[LPU], *pv[LPU];
 #pragma unroll
       for (int i = 0; i < LPU; ++i) {
         const int x = i * RPL + lane / CH, ck = (lane % CH) ^ Lds<DP>::swk(x), cv = (lane % CH) ^ Lds<DP>::swv(x);
         const uint32_t page = PAGED ? (uint32_t)__shfl(entry, x, 64) : 0, place = (uint32_t)__shfl(row, x, 64);
-        const bool in = there >> x & 1;
-        int64_t ofk = (uint64_t)place * (uint32_t)a.skt, ofv = (uint64_t)place * (uint32_t)a.svt;
+        uint64_t ofk = (uint64_t)place * (uint32_t)a.skt, ofv = (uint64_t)place * (uint32_t)a.svt;
         if constexpr (PAGED) ofk += (uint64_t)page * (uint32_t)a.skp, ofv += (uint64_t)page * (uint32_t)a.svp;
-        pk[i] = in && ck * 8 < a.D ? kb + ofk + ck * 8 : reinterpret_cast<const uint16_t*>(&kZeros);
-        pv[i] = in && cv * 8 < a.D ? vb + ofv + cv * 8 : reinterpret_cast<const uint16_t*>(&kZeros);
+        const bool in = there >> x & 1;
+        kr[i] = *reinterpret_cast<const v4u*>(pick(in && ck * 8 < a.D, kb + ofk + ck * 8));
+        vr[i] = *reinterpret_cast<const v4u*>(pick(in && cv * 8 < a.D, vb + ofv + cv * 8));
       }
-      typedef const __attribute__((address_space(1))) void* gp;
-#pragma unroll
-      for (int i = 0; i < LPU; ++i)
-        __builtin_amdgcn_global_load_lds((gp)pk[i], (SS_LDS void*)(ring + at + i * 1024), 16, 0, 0);
-#pragma unroll
-      for (int i = 0; i < LPU; ++i)
-        __builtin_amdgcn_global_load_lds((gp)pv[i], (SS_LDS void*)(ring + at + KB + i * 1024), 16, 0, 0);
       return there;
     };
 
     int j = j0 + wave;
     int entry = look(j), ahead = look(j + FW);
     uint32_t there = 0, there_next = 0;
-    if (j < je) there = issue(j, entry, 0);
+    if (j < je) there = issue(j, entry);
     v8bf qf[KST];
     {
       const uint16_t* p = a.q + (s.q0 + r / a.G) * a.sqt + (int64_t)(kvh * a.G + r % a.G) * a.sqh;
@@ -227,23 +239,17 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     float m = kLow, l = 0.0f;
     bool careful = false;  // some row's maximum is big
 
-    int at = 0;
+    SS_LDS uint8_t *kt = ring, *vt = ring + KB;
 #pragma unroll 1
     for (; j < je; j += FW) {
+#pragma unroll
+      for (int i = 0; i < LPU; ++i) {
+        *(SS_LDS v4u*)(ring + (i * 64 + lane) * 16) = kr[i];
+        *(SS_LDS v4u*)(ring + KB + (i * 64 + lane) * 16) = vr[i];
+      }
       entry = ahead;
       ahead = look(j + 2 * FW);
-      if (j + FW < je) {
-        there_next = issue(j + FW, entry, RING / FR - at);
-        // unit j has landed when only the loads just issued are outstanding (loads complete in order)
-        __builtin_amdgcn_s_waitcnt(vm(2 * LPU));
-      } else {
-        __builtin_amdgcn_s_waitcnt(vm(0));
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      const SS_LDS uint8_t* kt = ring + at;
-      const SS_LDS uint8_t* vt = kt + KB;
-      const int vo = at + KB;
-      at = RING / FR - at;
+      if (j + FW < je) there_next = issue(j + FW, entry);
       v16f S = v16f{};
 #pragma unroll
       for (int i = 0; i < KST; ++i) {
@@ -291,13 +297,10 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
           add_odd_between<DP>(O, vt, row_low - k0, row_lim - k0, sinks - k0, h);
 #pragma unroll 1
           for (int i = 0; i < LPU; ++i) {
-            SS_LDS v4u* p = (SS_LDS v4u*)(ring + vo + (i * 64 + lane) * 16);
+            SS_LDS v4u* p = (SS_LDS v4u*)(ring + KB + (i * 64 + lane) * 16);
             const v4u w = *p;
             *p = v4u{even_out(w[0]), even_out(w[1]), even_out(w[2]), even_out(w[3])};
           }
-          __builtin_amdgcn_s_waitcnt(0xC07F);
-          asm volatile("" ::: "memory");  // the reads below stay below
-          __builtin_amdgcn_sched_barrier(0);
         }
       }
       v8bf P[2];
@@ -320,14 +323,12 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
           const int ra = kk * 16 + vrow, rb = ra + 8, c = d * 4 + vcol;
-          const v4s x = read_tr((const SS_LDS uint8_t*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
-          const v4s y = read_tr((const SS_LDS uint8_t*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
+          const v4s x = read_columns((SS_LDS uint8_t*)(vt + ra * DP * 2 + (c ^ Lds<DP>::swv(ra)) * 16 + vsub));
+          const v4s y = read_columns((SS_LDS uint8_t*)(vt + rb * DP * 2 + (c ^ Lds<DP>::swv(rb)) * 16 + vsub));
           const v8bf vf = __builtin_bit_cast(v8bf, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
           O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, P[kk], O[d], 0, 0, 0);
         }
       there = there_next;
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // this unit's LDS reads are done before its slot is filled again
-      __builtin_amdgcn_sched_barrier(0);
     }
 
     // join the waves: a wave's O goes through its own ring, scaled to the workgroup's maximum
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       rec.kvh = kvh;
       rec.r0 = r0;
       rec.q0 = s.q0;
-      rec.parts = 1 + (int)((un - take + run - 1) / run);
+      rec.parts = min(1 + (un - take + run - 1) / run, (int)(gridDim.x - blockIdx.x));
     }
     const int quads = a.D / 4;
     for (int i = threadIdx.x; i < rows * quads; i += 64 * FW) {
@@ -394,7 +395,7 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     __syncthreads();  // the rings and sums are free again
     first = false;
     j0 = 0;
-    if (++th == (int64_t)tiles * a.Hkv) {
+    if (++th == tiles * a.Hkv) {
       th = 0;
       do {
         if (++b >= a.B) return;
@@ -418,26 +419,31 @@ __global__ __launch_bounds__(256) void join_kernel(FlatArgs a, Parts ws) {
   const int quads = a.D / 4, groups = 256 / quads, g = threadIdx.x / quads, c = threadIdx.x % quads;
   auto slot = [&](int s) { return s == 0 ? (int64_t)blockIdx.x * 2 + rec.slot : ((int64_t)blockIdx.x + s) * 2; };
   for (int row = blockIdx.y; row < rec.rows; row += gridDim.y) {
-    float M = -INFINITY;
-    for (int s = lane; s < rec.parts; s += 64) M = fmaxf(M, ws.lg[slot(s) * FM + row]);
+    float lp[kPre];
+    float4 xp[kPre];
+    auto fetch = [&](int s0) {  // (behind the last part: that one again)
+#pragma unroll
+      for (int i = 0; i < kPre; ++i) {
+        const int64_t at = slot(min(s0 + i * groups, rec.parts - 1));
+        lp[i] = ws.lg[at * FM + row];
+        xp[i] = *reinterpret_cast<const float4*>(ws.part + (at * ws.rows + row) * a.D + c * 4);
+      }
+    };
+    const float l0 = ws.lg[slot(min(lane, rec.parts - 1)) * FM + row];
+    fetch(g);
+    float M = l0;
+    for (int s = 64 + lane; s < rec.parts; s += 64) M = fmaxf(M, ws.lg[slot(s) * FM + row]);
     M = wave_max(M);
     auto power = [&](float l) { return l == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(l - M); };  // (of a NaN: NaN)
-    float sum = 0.0f;
-    for (int s = lane; s < rec.parts; s += 64) sum += power(ws.lg[slot(s) * FM + row]);
+    float sum = lane < rec.parts ? power(l0) : 0.0f;
+    for (int s = 64 + lane; s < rec.parts; s += 64) sum += power(ws.lg[slot(s) * FM + row]);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     float4 o = make_float4(0, 0, 0, 0);
     if (g < groups) {
       for (int s0 = g; s0 < rec.parts; s0 += kPre * groups) {
-        float lp[kPre];
-        float4 xp[kPre];
-#pragma unroll
-        for (int i = 0; i < kPre; ++i) {
-          const int64_t at = slot(min(s0 + i * groups, rec.parts - 1));
-          lp[i] = ws.lg[at * FM + row];
-          xp[i] = *reinterpret_cast<const float4*>(ws.part + (at * ws.rows + row) * a.D + c * 4);
-        }
+        if (s0 != g) fetch(s0);
 #pragma unroll
         for (int i = 0; i < kPre; ++i) {
           if (s0 + i * groups >= rec.parts) break;
@@ -465,7 +471,8 @@ __global__ __launch_bounds__(256) void join_kernel(FlatArgs a, Parts ws) {
 }
 
 // Workgroups of a call, and whether it leaves its tiles whole (then no workspace and one launch): rows over so few keys that
-// a workgroup's least run holds them. The lengths are not known here: the rule goes by the room for keys.
+// a workgroup's least run holds them (or so many rows and keys that their units may pass 31 bits). The lengths are not known
+// here: the rule goes by the room for keys.
 struct Plan {
   int64_t wgs;
   bool whole;
@@ -473,8 +480,8 @@ struct Plan {
 };
 inline Plan plan(int64_t Tq, int64_t room, int64_t B, int64_t G, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   const int64_t units = units_of((int)window, (int)sinks, (int)G, (int)Tq, (int)std::min<int64_t>(room, 0x7FFFFF00));
-  const int64_t tiles = (Tq * G / FM + B) * Hkv, fits = (D <= 64 ? 4 : 2) * (int64_t)num_cus_p();
-  const bool whole = units <= kMinUnits;
+  const int64_t tiles = (Tq * G / FM + B) * Hkv, fits = 4 * (int64_t)num_cus_p();
+  const bool whole = units <= kMinUnits || (double)tiles * units >= 0x7FFFFFFF;
   const int64_t wgs = whole ? std::min<int64_t>(tiles, 4 * fits)
                             : std::min<int64_t>(fits, (int64_t)std::min<double>((double)tiles * units / kMinUnits + 1, 1e9));
   return {std::max<int64_t>(wgs, 1), whole, (int)std::min<int64_t>(FM, Tq * G)};
@@ -482,7 +489,7 @@ inline Plan plan(int64_t Tq, int64_t room, int64_t B, int64_t G, int64_t Hkv, in
 
 template <int DP, bool PAGED> hipError_t launch(FlatArgs a, int64_t room, void* ws, hipStream_t st) {
   const Plan p = plan(a.Tq, room, a.B, a.G, a.Hkv, a.D, a.window, a.sinks);
-  constexpr int lds = FW * FR * 2 * 32 * DP * 2;
+  constexpr int lds = lds_bytes(DP);
   const hipError_t e = lds_limit((const void*)flat_kernel<DP, PAGED>, lds);
   if (e != hipSuccess) return e;
   a.whole = p.whole;

@@ -58,14 +58,17 @@ template <bool HALF, bool VEC> __global__ __launch_bounds__(256) void store_kern
   __shared__ int2 place[258];  // a workgroup's items belong to 256 / per + 2 tokens at most
   const int per = groups * chunks, heads = a.Hq + 2 * a.Hkv;
   const int64_t first = (int64_t)blockIdx.x * 256, items = a.T * per, t0 = first / per;  // (tokens of this launch)
-  const int tokens = (int)(min(first + 255, items - 1) / per - t0) + 1;
-  for (int i = threadIdx.x; i < tokens; i += 256) place[i] = place_of(a, a.first + t0 + i);
-  __syncthreads();
+  if (a.cu) {
+    const int tokens = (int)(min(first + 255, items - 1) / per - t0) + 1;
+    for (int i = threadIdx.x; i < tokens; i += 256) place[i] = place_of(a, a.first + t0 + i);
+    __syncthreads();
+  }
   const int64_t it = first + threadIdx.x;
   if (it >= items) return;
   const int64_t in = it / per, tok = a.first + in;
   const int rest = (int)(it - in * per), hg = rest / chunks, ch = rest - hg * chunks;
-  const int2 at = place[in - t0];
+  // (without a search for the sequence every thread looks its token's place up, under the loads of the values)
+  const int2 at = a.cu ? place[in - t0] : place_of(a, tok);
   if (at.x == kNoSequence) return;
   const bool pair = ch < pairs;
   const int second = !pair ? 0 : HALF ? a.rot / 2 : VEC ? 0 : 1;  // from a chunk's first part to its second; 0: one part

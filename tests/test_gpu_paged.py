@@ -148,6 +148,18 @@ def test_runs_cut_anywhere(ss, lens, Hq, Hkv, D):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_calls_give_the_same_bits(ss, D):
+    """Chunks whose tiles end inside a unit, cut into parts: loads of very different latency beside each other."""
+    c = Cache([1000, 777], 32, 2, D, 1)
+    q = torch.randn((129 + 50, 64, D), device="cuda").to(torch.bfloat16)
+    cu, n = _i32([0, 129, 179]), _i32([1000, 777])
+    first = ss.attn_paged(q, c.k, c.v, c.dev, n, cu_q=cu)
+    compare(first, None, c.expect(q, [1000, 777], [0, 129, 179]))
+    for _ in range(100):
+        assert torch.equal(ss.attn_paged(q, c.k, c.v, c.dev, n, cu_q=cu), first)
+
+
 def test_head_major_pages_and_strided_rows(ss):
     """Pages with the heads outside the keys, keys and values side by side in one pool, query and output rows inside wider ones."""
     _run(ss, [2, 1], [333, 40], 4, 2, 64, 16, head_major=True)
