@@ -853,7 +853,7 @@ hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {
     if (!a.window) return a.D <= 64 ? attn::launch_few<64>(a, ws, st) : attn::launch_few<128>(a, ws, st);
     FlatArgs f{};
     f.q = a.q, f.k = a.k, f.v = a.v, f.o = a.o, f.lse = a.lse, f.cu_q = a.cu_q, f.cu_k = a.cu_k, f.k_len = a.k_len;
-    f.sqt = a.sqt, f.sqh = a.sqh, f.sot = a.sot, f.soh = a.soh, f.skt = a.skt, f.skh = a.skh, f.svt = a.svt, f.svh = a.svh;
+    f.sqt = a.sqt, f.sqh = a.sqh, f.sot = a.sot, f.soh = a.soh, f.skt = (uint32_t)a.skt, f.skh = a.skh, f.svt = (uint32_t)a.svt, f.svh = a.svh;
     f.Tq = a.Tq, f.Tk = a.Tk, f.B = a.B, f.Hkv = a.Hkv, f.G = a.G, f.D = a.D;
     f.c = a.c, f.causal = a.causal, f.window = a.window, f.sinks = a.sinks;
     return launch_flat(f, (a.Tk + a.B - 1) / a.B, ws, st);

@@ -12,15 +12,16 @@
 // finished there; of one that is cut, each workgroup leaves a part (float32, normalised, with its row's log2 of the sum),
 // a run's first tile in one place and its last in another, and join_kernel adds the parts in order.
 //
-// Loads. A unit is loaded to registers, 16 bytes a lane from addresses of its own, so that its keys may lie anywhere, while the
-// unit before it is computed, and goes to LDS when that is done: each of 32 lanes looks up the page of one key, a unit ahead,
-// and the lanes that load its row take it from there. (Loads to LDS without registers, by the same addresses, left a wave's own
-// LDS reads incomplete behind their wait while they were in flight.) What no row of the tile sees (keys
-// behind the end, outside the window, entries that name no page) is loaded from a line of zeros instead: no memory behind it is
-// read, and whatever it holds stays out of the product.
+// Loads. A unit is loaded to registers while the unit before it is computed, and goes to LDS when that is done (loads to LDS
+// without registers, from addresses of each lane, left a wave's own LDS reads incomplete behind their wait while they were in
+// flight). Each of 32 lanes looks up the page of one key, a unit ahead. A load covers 4 rows of heads of 128, or 8 of 64:
+// where page sizes are multiples of that, its address is a scalar; other sizes take addresses of each lane (16 times 30
+// instructions a unit more). Values of keys that no row of the tile sees (behind the end, outside the window, of entries that
+// name no page) are replaced by zeros, so whatever they hold stays out of the product.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ss_attn.h"
 
@@ -54,13 +55,16 @@ __host__ __device__ inline Parts parts_of(void* ws, int64_t wgs, int rows) {
           reinterpret_cast<float*>(p + wgs * (sizeof(Record) + 2 * FM * 4)), rows};
 }
 
+// Where a unit's keys lie: rows of one tensor; pages that each load's rows share (their size is a multiple of them); any pages.
+constexpr int kRows = 0, kPages = 1, kAnyPages = 2;
+
 struct Seq {
   int64_t q0, k0;  // first query row, first key row (contiguous keys)
   int lq, lk;
 };
 __device__ __forceinline__ int64_t inside(int x, int64_t n) { return min(max((int64_t)x, (int64_t)0), n); }
 // Bounds from device memory are clamped to the tensors, so whatever they hold, no access leaves q, k, v or o.
-template <bool PAGED> __device__ __forceinline__ Seq load_seq(const FlatArgs& a, int b) {
+template <int KEYS> __device__ __forceinline__ Seq load_seq(const FlatArgs& a, int b) {
   Seq s;
   int64_t q0 = 0, q1 = a.Tq, k0 = 0, k1 = a.Tk;
   int len = 0x7FFFFFFF;
@@ -69,7 +73,7 @@ template <bool PAGED> __device__ __forceinline__ Seq load_seq(const FlatArgs& a,
   } else if (a.B > 1) {  // one row a sequence
     q0 = min((int64_t)b, a.Tq), q1 = min((int64_t)b + 1, a.Tq);
   }
-  if (PAGED) {
+  if (KEYS != kRows) {
     k1 = min((int64_t)a.cols * a.page, (int64_t)0x7FFFFF00);
     len = a.k_len[b];
   } else {
@@ -82,17 +86,18 @@ template <bool PAGED> __device__ __forceinline__ Seq load_seq(const FlatArgs& a,
   s.lk = min(max(len, 0), (int)min(max(k1, k0) - k0, (int64_t)0x7FFFFF00));
   return s;
 }
-__host__ __device__ inline int tiles_of(int lq, int G) { return (int)(((int64_t)lq * G + FM - 1) / FM); }
+__host__ __device__ inline int tiles_of(int lq, int G) { return (int)(((uint32_t)lq * (uint32_t)G + (FM - 1)) / FM); }
 // units of a tile of the sequence, at most (at least one, so that rows without keys are written)
-__host__ __device__ inline int units_of(int window, int sinks, int G, int lq, int lk) {
-  int64_t n = ((int64_t)lk + 31) / 32;
+__host__ __device__ inline int units_of(int window, int sinks, int tokens, int lq, int lk) {
+  uint32_t n = ((uint32_t)lk + 31) / 32;
   if (window) {  // the tile's tokens see window + tokens - 1 adjacent keys between them, and the first ones
-    const int64_t tok = (FM - 1 + G - 1) / G + 1, len = (int64_t)window + (tok < lq ? tok : lq) - 1;
-    const int64_t m = (len + 62) / 32 + ((int64_t)sinks + 31) / 32;
+    const uint32_t len = (uint32_t)window + (uint32_t)(tokens < lq ? tokens : lq) - 1;
+    const uint32_t m = (len + 62) / 32 + ((uint32_t)sinks + 31) / 32;
     n = m < n ? m : n;
   }
   return n > 1 ? (int)n : 1;
 }
+__host__ __device__ inline int tokens_of(int G) { return (FM - 1 + G - 1) / G + 1; }  // of a tile, at most
 
 // Sum over this lane and those below it, by the lanes' own exchange: each step adds what lies so many lanes down.
 __device__ __forceinline__ int wave_scan(int x) {
@@ -117,7 +122,7 @@ __device__ __forceinline__ const uint16_t* pick(bool take, const uint16_t* p) {
 // a wave's room in LDS holds a unit's keys and values, and at the end its rows' results
 constexpr int lds_bytes(int DP) { return FW * (2 * 32 * DP * 2 > FM * (DP * 4 + 16) ? 2 * 32 * DP * 2 : FM * (DP * 4 + 16)); }
 
-template <int DP, bool PAGED>
+template <int DP, int KEYS>
 __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;
   constexpr int KB = 32 * DP * 2;    // bytes of a unit's keys, and of its values
@@ -135,12 +140,12 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
   auto weight = [&](int i) -> int {  // units of sequence i's tiles (the host has seen to it that all fit 31 bits)
     mine = Seq{0, 0, 0, 0};
     if (i >= a.B) return 0;
-    mine = load_seq<PAGED>(a, i);
-    return tiles_of(mine.lq, a.G) * a.Hkv * (a.whole ? 1 : units_of(a.window, a.sinks, a.G, mine.lq, mine.lk));
+    mine = load_seq<KEYS>(a, i);
+    return tiles_of(mine.lq, a.G) * a.Hkv * (a.whole ? 1 : units_of(a.window, a.sinks, a.tokens, mine.lq, mine.lk));
   };
   int upto = wave_scan(weight(lane)), total = __builtin_amdgcn_readlane(upto, 63);
   for (int c = 64; c < a.B; c += 64) total += __builtin_amdgcn_readlane(wave_scan(weight(c + lane)), 63);
-  const int run = (int)max(((uint32_t)total + gridDim.x - 1) / gridDim.x, (uint32_t)(a.whole ? 1 : kMinUnits));
+  const int run = (int)max(a.by_wgs((uint32_t)total + gridDim.x - 1), (uint32_t)(a.whole ? 1 : kMinUnits));
   int s0 = (int)min((int64_t)blockIdx.x * run, (int64_t)0x7FFFFFFF);
   const int s1 = (int)min((int64_t)s0 + run, (int64_t)total);
   if (!a.whole && threadIdx.x == 0) ws.rec[blockIdx.x].parts = 0;
@@ -161,28 +166,42 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     }
     before += __builtin_amdgcn_readlane(upto, 63);
   }
-  int tiles = tiles_of(s.lq, a.G), un = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
+  int tiles = tiles_of(s.lq, a.G), un = a.whole ? 1 : units_of(a.window, a.sinks, a.tokens, s.lq, s.lk);
   int th = (s0 - before) / un;  // tile and key head in the sequence, the head fastest
   int j0 = (s0 - before) - th * un;
   if ((uint32_t)th >= (uint32_t)(tiles * a.Hkv)) return;  // (bounds that decrease may overlap: more work than the host knows)
 
   const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
   SS_LDS uint8_t* ring = (SS_LDS uint8_t*)smem + wave * RING;
+  // this lane's bytes of a load of RPL adjacent rows, whose chunks go to their places in LDS (the places repeat after NK loads)
+  constexpr int NK = DP >= 128 ? 4 : 2;
+  uint32_t lane_k[NK], lane_v;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int x = i * RPL + lane / CH, c = (lane % CH) ^ Lds<DP>::swk(x);
+    lane_k[i] = c * 8 < a.D ? (uint32_t)(lane / CH) * a.skt * 2u + c * 16 : 0x80000000u;  // (past every resource)
+  }
+  {
+    const int c = (lane % CH) ^ Lds<DP>::swv(lane / CH);
+    lane_v = c * 8 < a.D ? (uint32_t)(lane / CH) * a.svt * 2u + c * 16 : 0x80000000u;
+  }
   bool first = true;
 #pragma unroll 1
   while (true) {
     const int take = min(un - j0, s1 - s0);
-    const int tile = uni(th / a.Hkv), kvh = uni(th - tile * a.Hkv);
+    const int tile = uni((int)a.by_Hkv(th)), kvh = uni(th - tile * a.Hkv);
     const int nr = s.lq * a.G, r0 = tile * FM, rows = min(nr - r0, FM);
-    auto lim = [&](int r) { return a.causal ? min(max(r / a.G + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
-    auto low = [&](int r) {
-      const int p = r / a.G + s.lk - s.lq;
+    // what the rows of token t of the sequence see
+    auto lim = [&](int t) { return a.causal ? min(max(t + s.lk - s.lq + 1, 0), s.lk) : s.lk; };
+    auto low = [&](int t) {
+      const int p = t + s.lk - s.lq;
       return a.window && p >= a.window ? p - a.window + 1 : 0;
     };
-    const int r = min(r0 + l32, nr - 1), row_lim = lim(r), row_low = low(r);
-    const int kend = uni(lim(r0 + rows - 1)), kmin = uni(lim(r0)), klow = uni(low(r0)), khigh = uni(low(r0 + rows - 1));
+    const int t0 = uni((int)a.by_G(r0)), t1 = uni((int)a.by_G(r0 + rows - 1));  // tokens of the tile
+    const int r = min(r0 + l32, nr - 1), t = (int)a.by_G(r), row_lim = lim(t), row_low = low(t);
+    const int kend = uni(lim(t1)), kmin = uni(lim(t0)), klow = uni(low(t0)), khigh = uni(low(t1));
     const int sinks = a.window ? min(a.sinks, kend) : 0;
-    const bool tokens = r0 / a.G != (r0 + rows - 1) / a.G;  // more than one: rows that see different keys
+    const bool tokens = t0 != t1;  // more than one: rows that see different keys
     // the units that some row sees: those of the first tokens, then those of the windows
     const int su = (sinks + 31) / 32, wb = max(klow / 32, su), units = su + max((kend + 31) / 32 - wb, 0);
     const int j1 = a.whole ? units : j0 + take, je = min(j1, units);
@@ -193,27 +212,57 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       if (j >= je) return -1;
       const int key = base(j) + l32;
       if (!wanted(key)) return -1;
-      if constexpr (PAGED) return a.table[b * a.ldt + key / a.page];
+      if constexpr (KEYS != kRows) return a.table[b * a.ldt + a.by_page(key)];
       return 0;
     };
-    const uint16_t* kb = a.k + s.k0 * a.skt + (int64_t)kvh * a.skh;
-    const uint16_t* vb = a.v + s.k0 * a.svt + (int64_t)kvh * a.svh;
+    const uint16_t* kb = a.k + s.k0 * (int64_t)a.skt + (int64_t)kvh * a.skh;
+    const uint16_t* vb = a.v + s.k0 * (int64_t)a.svt + (int64_t)kvh * a.svh;
     // unit j on its way to registers; returns its keys that are there, a bit each
     v4u kr[LPU], vr[LPU];
     auto issue = [&](int j, int entry) __attribute__((always_inline)) -> uint32_t {
-      const int key = base(j) + l32;
-      const bool ok = PAGED ? (uint32_t)entry < (uint32_t)a.pages : entry >= 0;
+      const int first = base(j), key = first + l32;
+      const bool ok = KEYS == kRows ? entry >= 0 : (uint32_t)entry < (uint32_t)a.pages;
       const uint32_t there = (uint32_t)__ballot(ok);
-      const int row = PAGED ? key - key / a.page * a.page : key;
+      const int row = KEYS == kRows ? key : key - (int)a.by_page(key) * a.page;
+      if constexpr (KEYS == kAnyPages) {
 #pragma unroll
-      for (int i = 0; i < LPU; ++i) {
-        const int x = i * RPL + lane / CH, ck = (lane % CH) ^ Lds<DP>::swk(x), cv = (lane % CH) ^ Lds<DP>::swv(x);
-        const uint32_t page = PAGED ? (uint32_t)__shfl(entry, x, 64) : 0, place = (uint32_t)__shfl(row, x, 64);
-        uint64_t ofk = (uint64_t)place * (uint32_t)a.skt, ofv = (uint64_t)place * (uint32_t)a.svt;
-        if constexpr (PAGED) ofk += (uint64_t)page * (uint32_t)a.skp, ofv += (uint64_t)page * (uint32_t)a.svp;
-        const bool in = there >> x & 1;
-        kr[i] = *reinterpret_cast<const v4u*>(pick(in && ck * 8 < a.D, kb + ofk + ck * 8));
-        vr[i] = *reinterpret_cast<const v4u*>(pick(in && cv * 8 < a.D, vb + ofv + cv * 8));
+        for (int i = 0; i < LPU; ++i) {
+          const int x = i * RPL + lane / CH, ck = (lane % CH) ^ Lds<DP>::swk(x), cv = (lane % CH) ^ Lds<DP>::swv(x);
+          const uint32_t page = (uint32_t)__shfl(entry, x, 64), place = (uint32_t)__shfl(row, x, 64);
+          const uint64_t ofk = (uint64_t)page * a.skp + (uint64_t)place * a.skt;
+          const uint64_t ofv = (uint64_t)page * a.svp + (uint64_t)place * a.svt;
+          const bool in = there >> x & 1;
+          kr[i] = *reinterpret_cast<const v4u*>(pick(in && ck * 8 < a.D, kb + ofk + ck * 8));
+          vr[i] = *reinterpret_cast<const v4u*>(pick(in && cv * 8 < a.D, vb + ofv + cv * 8));
+        }
+      } else if (KEYS == kRows || a.page % 32 == 0) {
+        // the unit's rows are adjacent: one resource each for keys and values, which ends behind the sequence's last key or, of
+        // pages, behind the unit's last row (a page's other rows are memory of the pool; an entry that names none leaves no bytes)
+        const int at = KEYS == kRows ? first : __builtin_amdgcn_readfirstlane(row);
+        uint64_t ofk = (uint64_t)(uint32_t)at * a.skt, ofv = (uint64_t)(uint32_t)at * a.svt;
+        int n = 32;
+        if constexpr (KEYS == kPages) {
+          const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, there ? __ffs(there) - 1 : 0);
+          ofk += (uint64_t)page * a.skp, ofv += (uint64_t)page * a.svp;
+          n = there ? 32 : 0;
+        } else {
+          n = min(max(s.lk - first, 0), 32);
+        }
+        const auto rk = rsrc(kb + ofk, n ? (uint32_t)(n - 1) * a.skt * 2u + a.D * 2 : 0), rv = rsrc(vb + ofv, n ? (uint32_t)(n - 1) * a.svt * 2u + a.D * 2 : 0);
+#pragma unroll
+        for (int i = 0; i < LPU; ++i) {
+          kr[i] = __builtin_amdgcn_raw_buffer_load_b128(rk, lane_k[i % NK] + (uint32_t)(i * RPL) * a.skt * 2u, 0, 0);
+          vr[i] = __builtin_amdgcn_raw_buffer_load_b128(rv, lane_v + (uint32_t)(i * RPL) * a.svt * 2u, 0, 0);
+        }
+      } else {  // pages inside a unit: a resource for each load
+#pragma unroll
+        for (int i = 0; i < LPU; ++i) {
+          const uint32_t place = (uint32_t)__builtin_amdgcn_readlane(row, i * RPL), some = there >> (i * RPL) & ((1u << RPL) - 1);
+          const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, i * RPL + (some ? __ffs(some) - 1 : 0));
+          const uint64_t ofk = (uint64_t)page * a.skp + (uint64_t)place * a.skt, ofv = (uint64_t)page * a.svp + (uint64_t)place * a.svt;
+          kr[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(kb + ofk, some ? (RPL - 1) * a.skt * 2u + a.D * 2 : 0), lane_k[i % NK], 0, 0);
+          vr[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(vb + ofv, some ? (RPL - 1) * a.svt * 2u + a.D * 2 : 0), lane_v, 0, 0);
+        }
       }
       return there;
     };
@@ -224,7 +273,7 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     if (j < je) there = issue(j, entry);
     v8bf qf[KST];
     {
-      const uint16_t* p = a.q + (s.q0 + r / a.G) * a.sqt + (int64_t)(kvh * a.G + r % a.G) * a.sqh;
+      const uint16_t* p = a.q + (s.q0 + t) * a.sqt + (int64_t)(kvh * a.G + r - t * a.G) * a.sqh;
 #pragma unroll
       for (int i = 0; i < KST; ++i) {
         const int c = 2 * i + h;
@@ -246,6 +295,11 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       for (int i = 0; i < LPU; ++i) {
         *(SS_LDS v4u*)(ring + (i * 64 + lane) * 16) = kr[i];
         *(SS_LDS v4u*)(ring + KB + (i * 64 + lane) * 16) = vr[i];
+      }
+      if (KEYS != kAnyPages && uni(there) != -1) {  // values of keys that no row sees (their scores are replaced below)
+#pragma unroll
+        for (int i = 0; i < LPU; ++i)
+          if (!(there >> (i * RPL + lane / CH) & 1)) *(SS_LDS v4u*)(ring + KB + (i * 64 + lane) * 16) = v4u{0, 0, 0, 0};
       }
       entry = ahead;
       ahead = look(j + 2 * FW);
@@ -382,8 +436,8 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
         *reinterpret_cast<float4*>(ws.part + (slot * ws.rows + row) * a.D + c) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (c == 0) ws.lg[slot * FM + row] = lg;
       } else {
-        const int rr = r0 + row, head = kvh * a.G + rr % a.G;
-        const int64_t tok = s.q0 + rr / a.G;
+        const int rr = r0 + row, tr = (int)a.by_G(rr), head = kvh * a.G + rr - tr * a.G;
+        const int64_t tok = s.q0 + tr;
         *reinterpret_cast<uint2*>(a.o + tok * a.sot + head * a.soh + c) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (a.lse && c == 0) a.lse[head * a.Tq + tok] = lg * 0.69314718056f;
@@ -399,10 +453,10 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       th = 0;
       do {
         if (++b >= a.B) return;
-        s = load_seq<PAGED>(a, b);
+        s = load_seq<KEYS>(a, b);
         tiles = tiles_of(s.lq, a.G);
       } while (tiles == 0);
-      un = a.whole ? 1 : units_of(a.window, a.sinks, a.G, s.lq, s.lk);
+      un = a.whole ? 1 : units_of(a.window, a.sinks, a.tokens, s.lq, s.lk);
     }
   }
 }
@@ -454,8 +508,8 @@ __global__ __launch_bounds__(256) void join_kernel(FlatArgs a, Parts ws) {
     }
     acc[threadIdx.x] = o;
     __syncthreads();
-    const int rr = rec.r0 + row, head = rec.kvh * a.G + rr % a.G;
-    const int64_t tok = rec.q0 + rr / a.G;
+    const int rr = rec.r0 + row, tr = (int)a.by_G(rr), head = rec.kvh * a.G + rr - tr * a.G;
+    const int64_t tok = rec.q0 + tr;
     if (threadIdx.x < quads) {
       for (int k = 1; k < groups; ++k) {
         const float4 x = acc[k * quads + threadIdx.x];
@@ -479,22 +533,25 @@ struct Plan {
   int rows;
 };
 inline Plan plan(int64_t Tq, int64_t room, int64_t B, int64_t G, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
-  const int64_t units = units_of((int)window, (int)sinks, (int)G, (int)Tq, (int)std::min<int64_t>(room, 0x7FFFFF00));
+  const int64_t units = units_of((int)window, (int)sinks, tokens_of((int)G), (int)Tq, (int)std::min<int64_t>(room, 0x7FFFFF00));
   const int64_t tiles = (Tq * G / FM + B) * Hkv, fits = 4 * (int64_t)num_cus_p();
-  const bool whole = units <= kMinUnits || (double)tiles * units >= 0x7FFFFFFF;
+  const bool whole = units <= kMinUnits || (double)tiles * units >= 0x7FFF0000;
   const int64_t wgs = whole ? std::min<int64_t>(tiles, 4 * fits)
                             : std::min<int64_t>(fits, (int64_t)std::min<double>((double)tiles * units / kMinUnits + 1, 1e9));
   return {std::max<int64_t>(wgs, 1), whole, (int)std::min<int64_t>(FM, Tq * G)};
 }
 
-template <int DP, bool PAGED> hipError_t launch(FlatArgs a, int64_t room, void* ws, hipStream_t st) {
+template <int DP, int KEYS> hipError_t launch(FlatArgs a, int64_t room, void* ws, hipStream_t st) {
   const Plan p = plan(a.Tq, room, a.B, a.G, a.Hkv, a.D, a.window, a.sinks);
   constexpr int lds = lds_bytes(DP);
-  const hipError_t e = lds_limit((const void*)flat_kernel<DP, PAGED>, lds);
+  const hipError_t e = lds_limit((const void*)flat_kernel<DP, KEYS>, lds);
   if (e != hipSuccess) return e;
   a.whole = p.whole;
+  a.tokens = tokens_of(a.G);
+  a.by_G = FastDiv((uint32_t)a.G), a.by_Hkv = FastDiv((uint32_t)a.Hkv), a.by_wgs = FastDiv((uint32_t)p.wgs);
+  a.by_page = FastDiv((uint32_t)std::max(a.page, 1));
   const Parts parts = parts_of(ws, p.wgs, p.rows);
-  hipLaunchKernelGGL((flat_kernel<DP, PAGED>), dim3((unsigned)p.wgs), dim3(64 * FW), lds, st, a, parts);
+  hipLaunchKernelGGL((flat_kernel<DP, KEYS>), dim3((unsigned)p.wgs), dim3(64 * FW), lds, st, a, parts);
   if (const hipError_t f = hipGetLastError(); f != hipSuccess || p.whole) return f;
   hipLaunchKernelGGL(join_kernel, dim3((unsigned)p.wgs, (unsigned)std::min(p.rows, kJoin)), dim3(256), 0, st, a, parts);
   return hipGetLastError();
@@ -508,8 +565,12 @@ int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, in
 }
 
 hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st) {
-  if (a.paged) return a.D <= 64 ? flat::launch<64, true>(a, room, ws, st) : flat::launch<128, true>(a, room, ws, st);
-  return a.D <= 64 ? flat::launch<64, false>(a, room, ws, st) : flat::launch<128, false>(a, room, ws, st);
+  auto go = [&](auto dp) {
+    constexpr int DP = decltype(dp)::value;
+    if (!a.paged) return flat::launch<DP, flat::kRows>(a, room, ws, st);
+    return a.page % (512 / DP) == 0 ? flat::launch<DP, flat::kPages>(a, room, ws, st) : flat::launch<DP, flat::kAnyPages>(a, room, ws, st);
+  };
+  return a.D <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
 
 }  // namespace ss

@@ -908,7 +908,7 @@ ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_
   a.lse = lse;
   a.cu_q = cu_q; a.k_len = k_len; a.table = c.table;
   a.sqt = sqt; a.sqh = sqh; a.sot = sot; a.soh = soh;
-  a.skp = c.skp; a.skt = c.skt; a.skh = c.skh; a.svp = c.svp; a.svt = c.svt; a.svh = c.svh;
+  a.skp = (uint32_t)c.skp; a.skt = (uint32_t)c.skt; a.skh = c.skh; a.svp = (uint32_t)c.svp; a.svt = (uint32_t)c.svt; a.svh = c.svh;
   a.Tq = Tq; a.ldt = c.table_ld;
   a.B = (int)B; a.Hkv = (int)Hkv; a.G = (int)(Hq / Hkv); a.D = (int)D;
   a.pages = (int)c.pages; a.page = (int)c.page; a.cols = (int)c.table_cols;

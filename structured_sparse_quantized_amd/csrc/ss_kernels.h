@@ -158,20 +158,35 @@ struct StoreArgs {
 };
 hipError_t launch_paged_store(const StoreArgs& a, hipStream_t st);
 
+// Division of 0 .. 2^31 - 1 by a number known on the host: with 2^s the next power of two from d on, m = floor(2^(31+s) / d) + 1
+// is (2^(31+s) + e) / d with 0 < e <= 2^s, so n m / 2^(31+s) passes n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    for (s = 0; (1ull << s) < d; ++s) {}
+    m = (uint32_t)((1ull << (31 + s)) / d + 1);
+  }
+#ifdef __HIPCC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return __umulhi(n << 1, m) >> s; }
+#endif
+};
+
 // Attention of few rows a sequence over a paged cache, or over contiguous keys under a window.
 struct FlatArgs {
   const uint16_t *q, *k, *v;
   uint16_t* o;
   float* lse;  // [Hq][Tq] or NULL
   const int32_t *cu_q, *cu_k, *k_len, *table;  // table: paged; cu_k: contiguous keys
-  int64_t sqt, sqh, sot, soh;
-  int64_t skp, skt, skh, svp, svt, svh;  // page, key, head
+  int64_t sqt, sqh, sot, soh, skh, svh;
+  uint32_t skp, skt, svp, svt;  // page, key
   int64_t Tq, Tk, ldt;
   int B, Hkv, G, D, pages, page, cols;
+  FastDiv by_G, by_Hkv, by_page, by_wgs;  // (set by the launch)
   float c;  // scale * log2 e
   int causal, window, sinks;  // window 0: none
   int paged;  // by table, else contiguous keys
-  int whole;  // (set by the launch)
+  int whole, tokens;  // (set by the launch)
 };
 int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks);
 hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st);
