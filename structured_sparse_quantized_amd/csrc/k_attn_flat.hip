@@ -15,8 +15,8 @@
 // Loads. A unit is loaded to registers while the unit before it is computed, and goes to LDS when that is done (loads to LDS
 // without registers, from addresses of each lane, left a wave's own LDS reads incomplete behind their wait while they were in
 // flight). Each of 32 lanes looks up the page of one key, a unit ahead. A load covers 4 rows of heads of 128, or 8 of 64:
-// where page sizes are multiples of that, its address is a scalar; other sizes take addresses of each lane (16 times 30
-// instructions a unit more). Values of keys that no row of the tile sees (behind the end, outside the window, of entries that
+// where page sizes are multiples of that, its address is a scalar, where 32 divides them one for the unit; other sizes take
+// addresses of each lane (16 times 30 instructions a unit more). Values of keys that no row of the tile sees (behind the end, outside the window, of entries that
 // name no page) are replaced by zeros, so whatever they hold stays out of the product.
 #include <math.h>
 
@@ -55,8 +55,9 @@ __host__ __device__ inline Parts parts_of(void* ws, int64_t wgs, int rows) {
           reinterpret_cast<float*>(p + wgs * (sizeof(Record) + 2 * FM * 4)), rows};
 }
 
-// Where a unit's keys lie: rows of one tensor; pages that each load's rows share (their size is a multiple of them); any pages.
-constexpr int kRows = 0, kPages = 1, kAnyPages = 2;
+// Where a unit's keys lie: rows of one tensor; one page (sizes that 32 divides); pages that each load's rows share (sizes that
+// the rows of a load divide); any pages.
+constexpr int kRows = 0, kPage = 1, kPages = 2, kAnyPages = 3;
 
 struct Seq {
   int64_t q0, k0;  // first query row, first key row (contiguous keys)
@@ -143,8 +144,12 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     mine = load_seq<KEYS>(a, i);
     return tiles_of(mine.lq, a.G) * a.Hkv * (a.whole ? 1 : units_of(a.window, a.sinks, a.tokens, mine.lq, mine.lk));
   };
-  int upto = wave_scan(weight(lane)), total = __builtin_amdgcn_readlane(upto, 63);
-  for (int c = 64; c < a.B; c += 64) total += __builtin_amdgcn_readlane(wave_scan(weight(c + lane)), 63);
+  int upto = 0, total = 0;
+#pragma unroll 1
+  for (int c = 0; c < a.B; c += 64) {
+    upto = wave_scan(weight(c + lane));
+    total += __builtin_amdgcn_readlane(upto, 63);
+  }
   const int run = (int)max(a.by_wgs((uint32_t)total + gridDim.x - 1), (uint32_t)(a.whole ? 1 : kMinUnits));
   int s0 = (int)min((int64_t)blockIdx.x * run, (int64_t)0x7FFFFFFF);
   const int s1 = (int)min((int64_t)s0 + run, (int64_t)total);
@@ -152,6 +157,7 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
   if (s0 >= total) return;
   int b = 0, before = 0;  // the sequence, and the work before it
   Seq s;
+#pragma unroll 1
   for (int c = 0;; c += 64) {  // (ends: the work of all sequences passes s0)
     if (a.B > 64) upto = wave_scan(weight(c + lane));
     const uint64_t past = __ballot(before + upto > s0);
@@ -235,18 +241,18 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
           kr[i] = *reinterpret_cast<const v4u*>(pick(in && ck * 8 < a.D, kb + ofk + ck * 8));
           vr[i] = *reinterpret_cast<const v4u*>(pick(in && cv * 8 < a.D, vb + ofv + cv * 8));
         }
-      } else if (KEYS == kRows || a.page % 32 == 0) {
+      } else if constexpr (KEYS == kRows || KEYS == kPage) {
         // the unit's rows are adjacent: one resource each for keys and values, which ends behind the sequence's last key or, of
         // pages, behind the unit's last row (a page's other rows are memory of the pool; an entry that names none leaves no bytes)
         const int at = KEYS == kRows ? first : __builtin_amdgcn_readfirstlane(row);
         uint64_t ofk = (uint64_t)(uint32_t)at * a.skt, ofv = (uint64_t)(uint32_t)at * a.svt;
         int n = 32;
-        if constexpr (KEYS == kPages) {
+        if constexpr (KEYS == kPage) {
           const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, there ? __ffs(there) - 1 : 0);
           ofk += (uint64_t)page * a.skp, ofv += (uint64_t)page * a.svp;
           n = there ? 32 : 0;
         } else {
-          n = min(max(s.lk - first, 0), 32);
+          n = there ? min(s.lk - first, 32) : 0;
         }
         const auto rk = rsrc(kb + ofk, n ? (uint32_t)(n - 1) * a.skt * 2u + a.D * 2 : 0), rv = rsrc(vb + ofv, n ? (uint32_t)(n - 1) * a.svt * 2u + a.D * 2 : 0);
 #pragma unroll
@@ -269,17 +275,15 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
 
     int j = j0 + wave;
     int entry = look(j), ahead = look(j + FW);
-    uint32_t there = 0, there_next = 0;
-    if (j < je) there = issue(j, entry);
+    uint32_t there;
+    there = issue(j, entry);  // (a unit past the part: no bytes)
     v8bf qf[KST];
     {
       const uint16_t* p = a.q + (s.q0 + t) * a.sqt + (int64_t)(kvh * a.G + r - t * a.G) * a.sqh;
 #pragma unroll
       for (int i = 0; i < KST; ++i) {
         const int c = 2 * i + h;
-        v4u x = {0, 0, 0, 0};
-        if (DP == a.D || c * 8 < a.D) x = *reinterpret_cast<const v4u*>(p + c * 8);
-        qf[i] = __builtin_bit_cast(v8bf, x);
+        qf[i] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(pick(c * 8 < a.D, p + c * 8)));
       }
     }
     v16f O[DB];
@@ -303,7 +307,7 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       }
       entry = ahead;
       ahead = look(j + 2 * FW);
-      if (j + FW < je) there_next = issue(j + FW, entry);
+      const uint32_t there_next = issue(j + FW, entry);
       v16f S = v16f{};
 #pragma unroll
       for (int i = 0; i < KST; ++i) {
@@ -568,6 +572,7 @@ hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st
   auto go = [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     if (!a.paged) return flat::launch<DP, flat::kRows>(a, room, ws, st);
+    if (a.page % 32 == 0) return flat::launch<DP, flat::kPage>(a, room, ws, st);
     return a.page % (512 / DP) == 0 ? flat::launch<DP, flat::kPages>(a, room, ws, st) : flat::launch<DP, flat::kAnyPages>(a, room, ws, st);
   };
   return a.D <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
