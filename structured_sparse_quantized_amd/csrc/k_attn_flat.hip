@@ -55,9 +55,9 @@ __host__ __device__ inline Parts parts_of(void* ws, int64_t wgs, int rows) {
           reinterpret_cast<float*>(p + wgs * (sizeof(Record) + 2 * FM * 4)), rows};
 }
 
-// Where a unit's keys lie: rows of one tensor; one page (sizes that 32 divides); pages that each load's rows share (sizes that
-// the rows of a load divide); any pages.
-constexpr int kRows = 0, kPage = 1, kPages = 2, kAnyPages = 3;
+// Where a unit's keys lie: rows of one tensor; pages, of sizes that 32, 16 or 8 divides (so many adjacent rows share a page); any
+// pages.
+constexpr int kRows = 0, kAnyPages = 1;  // and 32, 16, 8
 
 struct Seq {
   int64_t q0, k0;  // first query row, first key row (contiguous keys)
@@ -177,7 +177,6 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
   int j0 = (s0 - before) - th * un;
   if ((uint32_t)th >= (uint32_t)(tiles * a.Hkv)) return;  // (bounds that decrease may overlap: more work than the host knows)
 
-  const int vrow = 4 * h + ((lane & 15) >> 2), vcol = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), vsub = (lane & 1) * 8;
   SS_LDS uint8_t* ring = (SS_LDS uint8_t*)smem + wave * RING;
   // this lane's bytes of a load of RPL adjacent rows, whose chunks go to their places in LDS (the places repeat after NK loads)
   constexpr int NK = DP >= 128 ? 4 : 2;
@@ -241,33 +240,32 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
           kr[i] = *reinterpret_cast<const v4u*>(pick(in && ck * 8 < a.D, kb + ofk + ck * 8));
           vr[i] = *reinterpret_cast<const v4u*>(pick(in && cv * 8 < a.D, vb + ofv + cv * 8));
         }
-      } else if constexpr (KEYS == kRows || KEYS == kPage) {
-        // the unit's rows are adjacent: one resource each for keys and values, which ends behind the sequence's last key or, of
-        // pages, behind the unit's last row (a page's other rows are memory of the pool; an entry that names none leaves no bytes)
-        const int at = KEYS == kRows ? first : __builtin_amdgcn_readfirstlane(row);
-        uint64_t ofk = (uint64_t)(uint32_t)at * a.skt, ofv = (uint64_t)(uint32_t)at * a.svt;
-        int n = 32;
-        if constexpr (KEYS == kPage) {
-          const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, there ? __ffs(there) - 1 : 0);
-          ofk += (uint64_t)page * a.skp, ofv += (uint64_t)page * a.svp;
-          n = there ? 32 : 0;
-        } else {
-          n = there ? min(s.lk - first, 32) : 0;
-        }
-        const auto rk = rsrc(kb + ofk, n ? (uint32_t)(n - 1) * a.skt * 2u + a.D * 2 : 0), rv = rsrc(vb + ofv, n ? (uint32_t)(n - 1) * a.svt * 2u + a.D * 2 : 0);
+      } else {
+        // rows that share a page are adjacent: one resource each for their keys and values, which ends behind the sequence's last
+        // key or, of pages, behind the last of them (a page's other rows are memory of the pool; an entry that names none leaves
+        // no bytes)
+        constexpr int PG = KEYS == kRows ? 32 : KEYS;
 #pragma unroll
-        for (int i = 0; i < LPU; ++i) {
-          kr[i] = __builtin_amdgcn_raw_buffer_load_b128(rk, lane_k[i % NK] + (uint32_t)(i * RPL) * a.skt * 2u, 0, 0);
-          vr[i] = __builtin_amdgcn_raw_buffer_load_b128(rv, lane_v + (uint32_t)(i * RPL) * a.svt * 2u, 0, 0);
-        }
-      } else {  // pages inside a unit: a resource for each load
+        for (int g = 0; g < 32 / PG; ++g) {
+          uint64_t ofk, ofv;
+          int n;
+          if constexpr (KEYS == kRows) {
+            ofk = (uint64_t)(uint32_t)first * a.skt, ofv = (uint64_t)(uint32_t)first * a.svt;
+            n = there ? min(s.lk - first, 32) : 0;
+          } else {
+            const uint32_t some = PG == 32 ? there : there >> (g * PG) & ((1u << (PG & 31)) - 1);
+            const uint32_t place = (uint32_t)__builtin_amdgcn_readlane(row, g * PG);
+            const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, g * PG + (some ? __ffs(some) - 1 : 0));
+            ofk = (uint64_t)page * a.skp + (uint64_t)place * a.skt, ofv = (uint64_t)page * a.svp + (uint64_t)place * a.svt;
+            n = some ? PG : 0;
+          }
+          const auto rk = rsrc(kb + ofk, n ? (uint32_t)(n - 1) * a.skt * 2u + a.D * 2 : 0), rv = rsrc(vb + ofv, n ? (uint32_t)(n - 1) * a.svt * 2u + a.D * 2 : 0);
 #pragma unroll
-        for (int i = 0; i < LPU; ++i) {
-          const uint32_t place = (uint32_t)__builtin_amdgcn_readlane(row, i * RPL), some = there >> (i * RPL) & ((1u << RPL) - 1);
-          const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, i * RPL + (some ? __ffs(some) - 1 : 0));
-          const uint64_t ofk = (uint64_t)page * a.skp + (uint64_t)place * a.skt, ofv = (uint64_t)page * a.svp + (uint64_t)place * a.svt;
-          kr[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(kb + ofk, some ? (RPL - 1) * a.skt * 2u + a.D * 2 : 0), lane_k[i % NK], 0, 0);
-          vr[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(vb + ofv, some ? (RPL - 1) * a.svt * 2u + a.D * 2 : 0), lane_v, 0, 0);
+          for (int i = 0; i < PG / RPL; ++i) {
+            const int x = g * (PG / RPL) + i;
+            kr[x] = __builtin_amdgcn_raw_buffer_load_b128(rk, lane_k[x % NK] + (uint32_t)(i * RPL) * a.skt * 2u, 0, 0);
+            vr[x] = __builtin_amdgcn_raw_buffer_load_b128(rv, lane_v + (uint32_t)(i * RPL) * a.svt * 2u, 0, 0);
+          }
         }
       }
       return there;
@@ -293,6 +291,12 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     bool careful = false;  // some row's maximum is big
 
     SS_LDS uint8_t *kt = ring, *vt = ring + KB;
+    // this lane's places in LDS, computed here, under the first loads (a call of few keys is a chain of latencies, and the
+    // instructions themselves, each read once, are among them)
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int ll = ln & 31, hh = ln >> 5;
+    const int vrow = 4 * hh + ((ln & 15) >> 2), vcol = ((ln >> 4) & 1) * 2 + ((ln & 3) >> 1), vsub = (ln & 1) * 8;
 #pragma unroll 1
     for (; j < je; j += FW) {
 #pragma unroll
@@ -311,19 +315,17 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       v16f S = v16f{};
 #pragma unroll
       for (int i = 0; i < KST; ++i) {
-        const v8bf kf = *reinterpret_cast<const SS_LDS v8bf*>(kt + l32 * DP * 2 + ((2 * i + h) ^ Lds<DP>::swk(l32)) * 16);
+        const v8bf kf = *reinterpret_cast<const SS_LDS v8bf*>(kt + ll * DP * 2 + ((2 * i + hh) ^ Lds<DP>::swk(ll)) * 16);
         S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], S, 0, 0, 0);
       }
       const int k0 = base(j);
       const bool seen = uni(there) == -1 && k0 + 32 <= kmin && (k0 >= khigh || k0 + 32 <= sinks);  // by every row, whole
       if (!seen) {
-        const int hi = row_lim - k0 - 4 * h, lo = row_low - k0 - 4 * h, sk = sinks - k0 - 4 * h;
-        const uint32_t bits = there >> (4 * h);
+        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; };
+        const uint32_t bits = (there & below(row_lim - k0) & (~below(row_low - k0) | below(sinks - k0))) >> (4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 8 * (i / 4) + i % 4;
-          if (e >= hi || (e < lo && e >= sk) || !(bits >> e & 1)) S[i] = -INFINITY;
-        }
+        for (int i = 0; i < 16; ++i)
+          if (!(bits >> (8 * (i / 4) + i % 4) & 1)) S[i] = -INFINITY;
       }
       float mt = S[0];
 #pragma unroll
@@ -572,8 +574,9 @@ hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st
   auto go = [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     if (!a.paged) return flat::launch<DP, flat::kRows>(a, room, ws, st);
-    if (a.page % 32 == 0) return flat::launch<DP, flat::kPage>(a, room, ws, st);
-    return a.page % (512 / DP) == 0 ? flat::launch<DP, flat::kPages>(a, room, ws, st) : flat::launch<DP, flat::kAnyPages>(a, room, ws, st);
+    if (a.page % 32 == 0) return flat::launch<DP, 32>(a, room, ws, st);
+    if (a.page % 16 == 0) return flat::launch<DP, 16>(a, room, ws, st);
+    return a.page % 8 == 0 ? flat::launch<DP, 8>(a, room, ws, st) : flat::launch<DP, flat::kAnyPages>(a, room, ws, st);
   };
   return a.D <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
