@@ -124,7 +124,7 @@ constexpr int BK = 64;               // keys per tile
 
 //
 // With WIN the rows of a workgroup see the tiles of the first tokens and, from the first row's window on, those behind: a
-// list of tiles without the ones between, walked as the whole range is without it. Tiles that some row of a wave sees in part
+// list of tiles without the ones between, walked as the whole range is without it. Stages that some row of a wave does not see whole
 // (the diagonal, the windows' lower edges, the end of the first tokens) are masked; the others branch over the masks. (Loops of
 // their own for the two kinds of tiles, in turn, took hundreds of registers to scratch.)
 template <int DP, int NS, bool WIN>
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   };
   // one stage: `cur` holds its scores, `nxt` receives those of the next; kn: LDS offset of the keys of the stage after
   // the next, vc: of this stage's values; `side`: work beside it (loads)
-  bool masked = true;  // (a window: whether some row does not see the tile whole)
+  bool masked = true;  // (a window: whether some row of the wave does not see the stage whole)
   auto stage = [&](v16f& cur, v16f& nxt, uint32_t kn, uint32_t vc, int first, auto side, auto maskc) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (decltype(maskc)::value) {
@@ -348,36 +348,6 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   // Iteration t reads K tile t + 1 and V tile t and brings in K tile t + 2 and V tile t + 1, into the slots of K tile t
   // and V tile t - 1, which were read in iteration t - 1: one wait and one barrier a tile.
   uint32_t k0 = 0, k1 = KB, v0 = VRING, v1 = VRING + KB;  // slots of tiles t, t + 1
-  if (nt > 0) {
-#pragma unroll
-    for (int i = 0; i < LPW; ++i) load_k(i, k0);
-    next_k();
-#pragma unroll
-    for (int i = 0; i < LPW; ++i) load_k(i, k1);
-    next_k();
-#pragma unroll
-    for (int i = 0; i < LPW; ++i) load_v(i, v0);
-    next_v();
-    __builtin_amdgcn_s_waitcnt(vm(2 * LPW));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < KST; ++i) read_k(i, 0);
-    S0 = v16f{};
-#pragma unroll
-    for (int i = 0; i < KST; ++i) S0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], qf[i], S0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < KST; ++i) read_k(i, KB / 2);
-    const int left = row_lim - from - 4 * h, lo = row_low - from - 4 * h, sk = sinks - from - 4 * h;
-    float mt = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = 8 * (i / 4) + i % 4;
-      if (e < left && (!WIN || e >= lo || e < sk)) mt = fmaxf(mt, S0[i]);
-    }
-    m = fmaxf(m, ceilf(pair_max(mt) * a.c));
-    rise = unif(__any(is_big(m)) ? -1.0f : kRise);
-  }
   auto turn = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0x7 << 4);  // vmcnt(0), lgkmcnt(0): this wave's loads and LDS reads
@@ -391,22 +361,64 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     k0 = k1, k1 = x;
     v0 = v1, v1 = y;
   };
+  int t = 0;
+  if (nt > 0) {
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) load_k(i, k0);
+    next_k();
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) load_k(i, k1);
+    next_k();
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) load_v(i, v0);
+    next_v();
+    __builtin_amdgcn_s_waitcnt(vm(2 * LPW));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (WIN) {  // tiles ahead of this wave's first window (of the first tokens all waves see some)
+      const int skip = ns > 0 ? 0 : min(max(uni(r0 < nr ? low(r0) : 0) / BK - w0 - t0, 0), nw);
+      for (; t < skip; ++t) {
+        turn();
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) load_v(i, v1);
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) load_k(i, k0);
+        rotate();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KST; ++i) read_k(i, WIN ? k0 : 0);
+    S0 = v16f{};
+#pragma unroll
+    for (int i = 0; i < KST; ++i) S0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], qf[i], S0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < KST; ++i) read_k(i, WIN ? k0 + KB / 2 : KB / 2);
+    const int at = WIN ? key_of(t0 + t) : from, left = row_lim - at - 4 * h, lo = row_low - at - 4 * h, sk = sinks - at - 4 * h;
+    float mt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = 8 * (i / 4) + i % 4;
+      if (e < left && (!WIN || e >= lo || e < sk)) mt = fmaxf(mt, S0[i]);
+    }
+    m = fmaxf(m, ceilf(pair_max(mt) * a.c));
+    rise = unif(__any(is_big(m)) ? -1.0f : kRise);
+  }
   auto tile_of = [&](int t, auto maskc) __attribute__((always_inline)) {
     turn();
     if constexpr (decltype(maskc)::value) renew(ofk), renew(ofv);
     const int key = WIN ? key_of(t0 + t) : (t0 + t) * BK;
-    if constexpr (WIN) masked = key + BK > wmin || (key < whigh && key + BK > sinks);
+    if constexpr (WIN) masked = key + 32 > wmin || (key < whigh && key + 32 > sinks);
     stage(S0, S1, k1, v0, key, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_v(i, v1);
     }, maskc);
+    if constexpr (WIN) masked = key + 64 > wmin || (key + 32 < whigh && key + 64 > sinks);
     stage(S1, S0, k1 + KB / 2, v0 + KB / 2, key + 32, [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < LPW; ++i) load_k(i, k0);
     }, maskc);
     rotate();
   };
-  int t = 0;
   if constexpr (WIN) {
     for (; t < nw; ++t) tile_of(t, std::true_type{});
   } else {
