@@ -856,7 +856,7 @@ int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int6
 // a launch holds fewer than 2^32 threads
 bool attn_fits(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t window, int64_t sinks) {
   const int64_t G = Hq / Hkv, few = attn::few_rows(Tq, attn_keys(Tq, Tk, B, window, sinks), B, G, Hkv);
-  if (few && window) return true;  // (as many workgroups as the chip holds)
+  if (few && window) return flat_fits(Tq, B, Hq, Hkv);  // (as many workgroups as the chip holds)
   return (few ? attn::few_slots(Tq, B, G) * 64 * attn::FW : (Tq * G / attn::BM + B) * 64 * attn::NW) * Hkv <= 0xFFFFFFFFLL;
 }
 

@@ -540,7 +540,7 @@ struct Plan {
 };
 inline Plan plan(int64_t Tq, int64_t room, int64_t B, int64_t G, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   const int64_t units = units_of((int)window, (int)sinks, tokens_of((int)G), (int)Tq, (int)std::min<int64_t>(room, 0x7FFFFF00));
-  const int64_t tiles = (Tq * G / FM + B) * Hkv, fits = 4 * (int64_t)num_cus_p();
+  const int64_t tiles = (Tq * G / FM + std::min(B, Tq)) * Hkv, fits = 4 * (int64_t)num_cus_p();
   const bool whole = units <= kMinUnits || (double)tiles * units >= 0x7FFF0000;
   const int64_t wgs = whole ? std::min<int64_t>(tiles, 4 * fits)
                             : std::min<int64_t>(fits, (int64_t)std::min<double>((double)tiles * units / kMinUnits + 1, 1e9));
@@ -568,6 +568,10 @@ template <int DP, int KEYS> hipError_t launch(FlatArgs a, int64_t room, void* ws
 int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   const flat::Plan p = flat::plan(Tq, room, B, Hq / Hkv, Hkv, D, window, sinks);
   return p.whole ? 0 : p.wgs * ((int64_t)sizeof(flat::Record) + 2 * flat::FM * 4 + 2 * p.rows * D * 4);
+}
+
+bool flat_fits(int64_t Tq, int64_t B, int64_t Hq, int64_t Hkv) {
+  return (double)(Tq * (Hq / Hkv) / flat::FM + std::min(B, Tq)) * Hkv < 0x7FFF0000;
 }
 
 hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st) {

@@ -50,9 +50,10 @@ template <> struct Vec<float> {  // 4 floats
   }
 };
 
+// Sum and maximum over the BT threads of a row (16, or whole waves).
 template <int BT> __device__ __forceinline__ double block_sum(double v, double* red) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  for (int o = BT < 64 ? BT / 2 : 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
   if constexpr (BT > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     lds_barrier();
@@ -63,7 +64,8 @@ template <int BT> __device__ __forceinline__ double block_sum(double v, double* 
   return v;
 }
 template <int BT> __device__ __forceinline__ float block_top(float v, float* red) {
-  v = wave_max(v);
+#pragma unroll
+  for (int o = BT < 64 ? BT / 2 : 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
   if constexpr (BT > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     lds_barrier();
@@ -80,11 +82,11 @@ __device__ __forceinline__ float inverse_root(double sum, int64_t K, double eps)
 }
 
 // The lift of a row of codes staged in LDS (zero behind K): whole periods of its byte pattern per thread.
-template <int N, int BT> __device__ __forceinline__ void lift_row(const uint8_t* codes, uint8_t* out, int Kc) {
+template <int N, int BT> __device__ __forceinline__ void lift_row(const uint8_t* codes, uint8_t* out, int Kc, int tid) {
   using LP = LiftPeriod<N>;
   const int nchunk = Kc / 16, nper = (nchunk + LP::PC - 1) / LP::PC;
   const uint32_t* l32 = reinterpret_cast<const uint32_t*>(codes);
-  for (int p = threadIdx.x; p < nper; p += BT) {
+  for (int p = tid; p < nper; p += BT) {
     uint32_t s[LP::SW], o[4 * LP::PC];
 #pragma unroll
     for (int i = 0; i < LP::SW; ++i) s[i] = l32[p * LP::SW + i];
@@ -107,28 +109,32 @@ __host__ __device__ inline int staged_bytes(int n, int Kc) {
     default: return of(LiftPeriod<8>::PC, LiftPeriod<8>::SB);
   }
 }
-template <int BT> __device__ __forceinline__ void lift_any(int n, const uint8_t* codes, uint8_t* out, int Kc) {
+template <int BT> __device__ __forceinline__ void lift_any(int n, const uint8_t* codes, uint8_t* out, int Kc, int tid) {
   switch (n) {
-    case 3: lift_row<3, BT>(codes, out, Kc); break;
-    case 4: lift_row<4, BT>(codes, out, Kc); break;
-    case 5: lift_row<5, BT>(codes, out, Kc); break;
-    case 6: lift_row<6, BT>(codes, out, Kc); break;
-    case 7: lift_row<7, BT>(codes, out, Kc); break;
-    default: lift_row<8, BT>(codes, out, Kc); break;
+    case 3: lift_row<3, BT>(codes, out, Kc, tid); break;
+    case 4: lift_row<4, BT>(codes, out, Kc, tid); break;
+    case 5: lift_row<5, BT>(codes, out, Kc, tid); break;
+    case 6: lift_row<6, BT>(codes, out, Kc, tid); break;
+    case 7: lift_row<7, BT>(codes, out, Kc, tid); break;
+    default: lift_row<8, BT>(codes, out, Kc, tid); break;
   }
 }
 
-// T: the stream's type; TW: the weights'; OUT: 0 int8, 1 fp8, 2 bf16; BT threads of VPT vectors each hold a row.
+// T: the stream's type; TW: the weights'; OUT: 0 int8, 1 fp8, 2 bf16; BT threads of VPT vectors each hold a row, short rows
+// several to a workgroup.
+template <int BT> constexpr int rows_of() { return BT < 256 ? 256 / BT : 1; }
 template <typename T, typename TW, int OUT, int BT, int VPT>
-__global__ __launch_bounds__(BT) void row_kernel(NormArgs a) {
+__global__ __launch_bounds__(BT * rows_of<BT>()) void row_kernel(NormArgs a) {
   using V = Vec<T>;
   constexpr int E = V::E;
   using Qz = Quant<OUT == 1>;
-  extern __shared__ __align__(16) uint8_t codes[];  // of one row, where the lift gathers from LDS
-  __shared__ double red_sum[BT / 64];
-  __shared__ float red_top[BT / 64];
-  const int tid = threadIdx.x, K = (int)a.K;
-  const int64_t row = a.first + blockIdx.x;
+  constexpr int R = rows_of<BT>();
+  extern __shared__ __align__(16) uint8_t all_codes[];  // of each row, where the lift gathers from LDS
+  __shared__ double red_sum[R > 1 ? 1 : BT / 64];
+  __shared__ float red_top[R > 1 ? 1 : BT / 64];
+  const int tid = threadIdx.x % BT, sub = threadIdx.x / BT, K = (int)a.K;
+  const int64_t row = a.first + (int64_t)blockIdx.x * R + sub;
+  if (row >= a.last) return;  // (of a workgroup with several rows, whose only barrier waits for the waves that are left)
   const int nvec = K / E, tail = nvec * E + tid;  // a last part of a vector goes by elements, one a thread
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* res = static_cast<const T*>(a.res) + row * a.ldr;
@@ -230,6 +236,7 @@ __global__ __launch_bounds__(BT) void row_kernel(NormArgs a) {
       }
       for (int c = nvec * 12 + tid; c < Kc; c += BT) q[c] = 0;
     } else {
+      uint8_t* codes = all_codes + sub * ((staged_bytes(n, Kc) + 15) / 16 * 16);
       uint8_t* to = n == 2 ? q : codes;
       const int end = n == 2 ? Kc : staged_bytes(n, Kc);
 #pragma unroll
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(BT) void row_kernel(NormArgs a) {
       for (int c = K + tid; c < end; c += BT) to[c] = 0;
       if (n != 2) {
         __syncthreads();
-        lift_any<BT>(n, codes, q, Kc);
+        lift_any<BT>(n, codes, q, Kc, tid);
       }
     }
   }
@@ -301,18 +308,20 @@ template <typename T, typename TW, int OUT> hipError_t launch(const NormArgs& a,
   const int64_t nvec = (a.K + E - 1) / E;
   const bool gathers = OUT != 2 && nvec <= 4096 && a.n != 2 && !(a.n == 4 && E == 8 && a.K % 8 == 0);
   const int64_t lds = !gathers ? 0 : (staged_bytes(a.n, (int)a.Kc) + 15) / 16 * 16;
-  auto go = [&](auto kern, int threads) -> hipError_t {
-    const hipError_t e = lds_limit((const void*)kern, (int)lds);
+  auto go = [&](auto kern, int threads, int rows = 1) -> hipError_t {
+    const hipError_t e = lds_limit((const void*)kern, (int)(lds * rows));
     if (e != hipSuccess) return e;
     for (int64_t m = 0; m < a.M; m += kSlab) {  // launches of fewer than 2^32 threads
       NormArgs b = a;
       b.first = m;
-      hipLaunchKernelGGL(kern, dim3((unsigned)std::min(kSlab, a.M - m)), dim3(threads), (unsigned)lds, st, b);
+      b.last = std::min(m + kSlab, a.M);
+      hipLaunchKernelGGL(kern, dim3((unsigned)((b.last - m + rows - 1) / rows)), dim3(threads), (unsigned)(lds * rows), st, b);
       if (const hipError_t f = hipGetLastError(); f != hipSuccess) return f;
     }
     return hipSuccess;
   };
-  if (nvec <= 64) return go(row_kernel<T, TW, OUT, 64, 1>, 64);
+  if (nvec <= 16) return go(row_kernel<T, TW, OUT, 16, 1>, 256, 16);
+  if (nvec <= 64) return go(row_kernel<T, TW, OUT, 64, 1>, 256, 4);
   if (nvec <= 256) return go(row_kernel<T, TW, OUT, 256, 1>, 256);
   if (nvec <= 512) return go(row_kernel<T, TW, OUT, 256, 2>, 256);
   if (nvec <= 1024) return go(row_kernel<T, TW, OUT, 256, 4>, 256);

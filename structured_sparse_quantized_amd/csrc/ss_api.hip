@@ -826,7 +826,8 @@ ss_status ss_paged_store(const void* q, int64_t sqt, int64_t sqh, const void* k,
                          void* qo, int64_t sot, int64_t soh, const ss_paged_kv* cache, void* stream) {
   if (T < 0 || B < 0 || Hq < 0 || Hkv < 0 || D < 0) return fail(SS_ERR_SHAPE, "negative size");
   if (layout != SS_ROPE_HALF && layout != SS_ROPE_INTERLEAVED) return fail(SS_ERR_UNSUPPORTED, "unknown layout %d", (int)layout);
-  if (T == 0 || B == 0 || Hkv == 0 || D == 0) return ok();
+  if (T == 0 || B == 0 || (Hkv == 0 && Hq == 0) || D == 0) return ok();
+  if (Hkv == 0) return fail(SS_ERR_SHAPE, "query heads without key heads");
   if (D % 8 != 0) return fail(SS_ERR_UNSUPPORTED, "D=%lld must be a multiple of 8", (long long)D);
   if (rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0)
     return fail(SS_ERR_SHAPE, "rot_dim=%lld must be even and within 0..%lld", (long long)rot_dim, (long long)D);
@@ -886,7 +887,8 @@ ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_
   if (Tq == 0 || B == 0 || Hq == 0) return ok();
   ss_status s;
   if ((s = check_heads(Hq, Hkv, D, scale, causal, &window, &sinks)) != SS_OK) return s;
-  if (Tq > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL) return fail(SS_ERR_SHAPE, "too large");
+  if (Tq > 0x7FFFFFFF || B > 0xFFFFFFF || Hq > 0xFFFF || Tq * (Hq / Hkv) > 0x7FFFFF00LL || !ss::flat_fits(Tq, B, Hq, Hkv))
+    return fail(SS_ERR_SHAPE, "too large");
   if (!cu_q && B != Tq && B != 1) return fail(SS_ERR_NULL, "cu_q is required unless every sequence has one token");
   if (Tq == 1) sqt = sot = D;
   if (Hq == 1) sqh = soh = D;

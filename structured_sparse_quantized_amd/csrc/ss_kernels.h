@@ -138,7 +138,7 @@ struct NormArgs {
   const void *x, *res, *w;  // res, w: or NULL
   void *sum, *y;            // sum: where res is given
   float* sx;
-  int64_t M, first, K, Kc, ldx, ldr, lds, ldy;  // first: of the launch's rows
+  int64_t M, first, last, K, Kc, ldx, ldr, lds, ldy;  // first, last: the launch's rows
   double eps;
   int n;
 };
@@ -189,6 +189,7 @@ struct FlatArgs {
   int whole, tokens;  // (set by the launch)
 };
 int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks);
+bool flat_fits(int64_t Tq, int64_t B, int64_t Hq, int64_t Hkv);  // (tiles within 31 bits)
 hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st);
 
 }  // namespace ss

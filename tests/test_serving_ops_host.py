@@ -87,7 +87,8 @@ def test_paged_attention_refusals(ss):
         (dict(D=136), ss.SS_ERR_UNSUPPORTED), (dict(D=4), ss.SS_ERR_UNSUPPORTED), (dict(scale=NAN), ss.SS_ERR_SHAPE),
         (dict(window=3, causal=0), ss.SS_ERR_UNSUPPORTED), (dict(window=-3), ss.SS_ERR_SHAPE), (dict(Tq=5), ss.SS_ERR_NULL),
         (dict(ws=None), ss.SS_ERR_NULL), (dict(ws=ODD), ss.SS_ERR_ALIGN), (dict(bytes=100), ss.SS_ERR_SHAPE), (dict(bytes=-1), ss.SS_ERR_SHAPE),
-        (dict(k_len=ctypes.c_void_p(2)), ss.SS_ERR_ALIGN), (dict(Tq=0, q=None), ss.SS_OK), (dict(B=0, q=None), ss.SS_OK)])
+        (dict(k_len=ctypes.c_void_p(2)), ss.SS_ERR_ALIGN), (dict(Tq=0, q=None), ss.SS_OK), (dict(B=0, q=None), ss.SS_OK),
+        (dict(Tq=1 << 27, B=1 << 27, Hq=64, Hkv=64, D=8), ss.SS_ERR_SHAPE)])
     for change, status in CACHES:
         assert call(**{**good, "kv": _kv(ss, **change)}) == getattr(ss, status), change
     assert ss.attn_paged_workspace_bytes(3, 96, 3, 4, 2, 128) == 0 and ss.attn_paged_workspace_bytes(3, 9600, 3, 4, 2, 128) > 0
@@ -104,7 +105,7 @@ def test_store_refusals(ss):
         (dict(rot=3), ss.SS_ERR_SHAPE), (dict(rot=130), ss.SS_ERR_SHAPE), (dict(rot=-2), ss.SS_ERR_SHAPE), (dict(rot=0), ss.SS_ERR_UNSUPPORTED),
         (dict(layout=2), ss.SS_ERR_UNSUPPORTED), (dict(mscale=INF), ss.SS_ERR_SHAPE), (dict(B=2), ss.SS_ERR_NULL), (dict(D=20), ss.SS_ERR_UNSUPPORTED),
         (dict(skt=-1), ss.SS_ERR_SHAPE), (dict(soh=64), ss.SS_ERR_SHAPE), (dict(sot=640), ss.SS_ERR_SHAPE), (dict(T=-1), ss.SS_ERR_SHAPE),
-        (dict(T=0, k=None), ss.SS_OK), (dict(Hkv=0, k=None), ss.SS_OK)])
+        (dict(T=0, k=None), ss.SS_OK), (dict(Hkv=0, k=None), ss.SS_ERR_SHAPE), (dict(Hkv=0, Hq=0, k=None), ss.SS_OK)])
     for change, status in CACHES + [(dict(skh=64), "SS_ERR_SHAPE"), (dict(svt=0), "SS_ERR_SHAPE"), (dict(skp=0), "SS_ERR_SHAPE")]:
         assert call(**{**good, "kv": _kv(ss, **change)}) == getattr(ss, status), change
 
