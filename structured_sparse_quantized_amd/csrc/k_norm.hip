@@ -9,7 +9,10 @@
 // bit. It costs two instructions of half rate a value.
 //
 // Bound: HBM. A row stays in registers between its three passes (squares, absmax, codes), so x and the residual are read
-// once, r and the codes written once. A workgroup per row; the row's two sums go through LDS.
+// once, r and the codes written once. A workgroup per row, or 4 or 16 short rows to one (655360 rows of 128 to bf16: 115 us, a
+// workgroup of one wave each 242); a row's two sums go through LDS where it has several waves.
+// Measured: 16384 x 4096 bf16 with residual to FP8 75-80 us, 5.9-6.3 TB/s (a large copy: 5.2); 6:8 INT8 79; 4096 x 14336 70; one row of
+// 3584 3.5, which is a launch and three chains of latencies.
 #include <algorithm>
 
 #include "ss_device.h"
