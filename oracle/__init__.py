@@ -25,7 +25,7 @@ Module map: ``prune`` (magnitude N:M masks, 2:4 compression, energy),
 INT8/FP8, the E4M3FN codec), ``gemm`` (sparse product and rescale epilogue),
 ``paths`` (the five library calls end to end), ``block`` (the block-scaled
 FP8 prep and product), ``accounting`` (bits and closed forms); imported by name: ``rotary``, ``attention``,
-``fused_epilogue`` (what runs between the products of a layer).
+``fused_epilogue``, ``norm``, ``windowed`` (what runs between the products of a layer).
 """
 from .prune import (nm_keep_mask, prune_nm, compress24, decompress24, pack_meta, unpack_meta,
                     paired48_keep_mask, energy_removed)

@@ -13,8 +13,7 @@
 // a run's first tile in one place and its last in another, and join_kernel adds the parts in order.
 //
 // Loads. A unit is loaded to registers while the unit before it is computed, and goes to LDS when that is done (loads to LDS
-// without registers, from addresses of each lane, left a wave's own LDS reads incomplete behind their wait while they were in
-// flight). Each of 32 lanes looks up the page of one key, a unit ahead. A load covers 4 rows of heads of 128, or 8 of 64:
+// without registers, from addresses of each lane, gave wrong parts now and then where a unit in flight was cut). Each of 32 lanes looks up the page of one key, a unit ahead. A load covers 4 rows of heads of 128, or 8 of 64:
 // where page sizes are multiples of that, its address is a scalar, where 32 divides them one for the unit; other sizes take
 // addresses of each lane (16 times 30 instructions a unit more). Values of keys that no row of the tile sees (behind the end, outside the window, of entries that
 // name no page) are replaced by zeros, so whatever they hold stays out of the product.
