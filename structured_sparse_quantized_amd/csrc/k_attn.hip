@@ -257,15 +257,12 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
   auto stage = [&](v16f& cur, v16f& nxt, uint32_t kn, uint32_t vc, int first, auto side, auto maskc) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (decltype(maskc)::value) {
-      const int left = row_lim - first - 4 * h;
+      [[maybe_unused]] const int left = row_lim - first - 4 * h;
       if constexpr (WIN) {
         if (masked) {
-          const int lo = row_low - first - 4 * h, sk = sinks - first - 4 * h;
+          const uint32_t bits = keys_between(row_low - first, row_lim - first, sinks - first) >> (4 * h);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = 8 * (i / 4) + i % 4;
-            if (e >= left || (e < lo && e >= sk)) cur[i] = -INFINITY;
-          }
+          for (int i = 0; i < 16; ++i) cur[i] = where_seen(cur[i], bits, 8 * (i / 4) + i % 4);
         }
       } else {
 #pragma unroll

@@ -323,11 +323,9 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
       const int k0 = base(j);
       const bool seen = uni(there) == -1 && k0 + 32 <= kmin && (k0 >= khigh || k0 + 32 <= sinks);  // by every row, whole
       if (!seen) {
-        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; };
-        const uint32_t bits = (there & below(row_lim - k0) & (~below(row_low - k0) | below(sinks - k0))) >> (4 * h);
+        const uint32_t bits = (there & keys_between(row_low - k0, row_lim - k0, sinks - k0)) >> (4 * h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(bits >> (8 * (i / 4) + i % 4) & 1)) S[i] = -INFINITY;
+        for (int i = 0; i < 16; ++i) S[i] = where_seen(S[i], bits, 8 * (i / 4) + i % 4);
       }
       float mt = S[0];
 #pragma unroll

@@ -102,5 +102,14 @@ template <int DP> __device__ __forceinline__ void add_odd_between(v16f* O, const
       }
 }
 
+// The keys of a unit of 32 that a row sees, a bit each: those below hi that are not below lo, and those below sk; and a score, or
+// -infinity where its key's bit is not set (two instructions: the bit over a word, and a choice of bits).
+__device__ __forceinline__ uint32_t keys_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
+__device__ __forceinline__ uint32_t keys_between(int lo, int hi, int sk) { return keys_below(hi) & (~keys_below(lo) | keys_below(sk)); }
+__device__ __forceinline__ float where_seen(float score, uint32_t bits, int key) {
+  const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)bits, key, 1);
+  return __uint_as_float((m & __float_as_uint(score)) | (~m & 0xFF800000u));
+}
+
 }  // namespace attn
 }  // namespace ss
