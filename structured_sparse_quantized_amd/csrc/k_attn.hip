@@ -127,8 +127,8 @@ constexpr int BK = 64;               // keys per tile
 // list of tiles without the ones between, walked as the whole range is without it. Stages that some row of a wave does not see whole
 // (the diagonal, the windows' lower edges, the end of the first tokens) are masked; the others branch over the masks. (Loops of
 // their own for the two kinds of tiles, in turn, took hundreds of registers to scratch.) Measured: window 1024 and 4 first tokens, 8192
-// tokens, 32 heads of 128 over 8: 165-180 us, 0.72-0.78 PFLOP/s of the seen pairs; window 300, 9 prompts of 8001 tokens, 12 heads of 64:
-// 32 us.
+// tokens, 32 heads of 128 over 8: 165-170 us, 0.76-0.78 PFLOP/s of the seen pairs; window 300, 9 prompts of 8001 tokens, 12 heads of 64: 26
+// us (keys in two parts 36).
 template <int DP, int NS, bool WIN>
 __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int slots) {
   constexpr int CH = DP / 8, KST = DP / 16, DB = DP / 32;  // chunks a row, 16-value steps, 32-value blocks
@@ -392,12 +392,17 @@ __global__ __launch_bounds__(64 * NW * NS, 2) void prompt_kernel(AttnArgs a, int
     for (int i = 0; i < KST; ++i) S0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i], qf[i], S0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < KST; ++i) read_k(i, WIN ? k0 + KB / 2 : KB / 2);
-    const int at = WIN ? key_of(t0 + t) : from, left = row_lim - at - 4 * h, lo = row_low - at - 4 * h, sk = sinks - at - 4 * h;
     float mt = -INFINITY;
+    if constexpr (WIN) {
+      const int at = key_of(t0 + t);
+      const uint32_t bits = keys_between(row_low - at, row_lim - at, sinks - at) >> (4 * h);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = 8 * (i / 4) + i % 4;
-      if (e < left && (!WIN || e >= lo || e < sk)) mt = fmaxf(mt, S0[i]);
+      for (int i = 0; i < 16; ++i) mt = fmaxf(mt, where_seen(S0[i], bits, 8 * (i / 4) + i % 4));
+    } else {
+      const int left = row_lim - from - 4 * h;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * (i / 4) + i % 4 < left) mt = fmaxf(mt, S0[i]);
     }
     m = fmaxf(m, ceilf(pair_max(mt) * a.c));
     rise = unif(__any(is_big(m)) ? -1.0f : kRise);
