@@ -852,7 +852,7 @@ static int64_t attn_keys(int64_t Tq, int64_t Tk, int64_t B, int64_t window, int6
 int64_t attn_workspace_bytes(int64_t Tq, int64_t Tk, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
   const int64_t G = Hq / Hkv;
   if (!attn::few_rows(Tq, attn_keys(Tq, Tk, B, window, sinks), B, G, Hkv)) return 0;
-  if (window) return flat_workspace_bytes(Tq, (Tk + B - 1) / B, B, Hq, Hkv, D, window, sinks);
+  if (window) return flat_workspace_bytes(Tq, (Tk + B - 1) / B, Tk, B, Hq, Hkv, D, window, sinks);
   const int64_t n = attn::splits(Tq, Tk, B, G, Hkv, D);
   return n == 1 ? 0 : n * Tq * Hq * (D + 1) * 4;
 }
@@ -872,7 +872,7 @@ hipError_t launch_attn(const AttnArgs& a, void* ws, hipStream_t st) {
     f.sqt = a.sqt, f.sqh = a.sqh, f.sot = a.sot, f.soh = a.soh, f.skt = (uint32_t)a.skt, f.skh = a.skh, f.svt = (uint32_t)a.svt, f.svh = a.svh;
     f.Tq = a.Tq, f.Tk = a.Tk, f.B = a.B, f.Hkv = a.Hkv, f.G = a.G, f.D = a.D;
     f.c = a.c, f.causal = a.causal, f.window = a.window, f.sinks = a.sinks;
-    return launch_flat(f, (a.Tk + a.B - 1) / a.B, ws, st);
+    return launch_flat(f, (a.Tk + a.B - 1) / a.B, a.Tk, ws, st);
   }
   return a.D <= 64 ? attn::launch_prompt<64>(a, st) : attn::launch_prompt<128>(a, st);
 }

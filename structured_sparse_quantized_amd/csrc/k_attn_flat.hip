@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
 
   // ---- this workgroup's run: 64 sequences at a time, one a lane ---------------------------------------------------
   Seq mine;
-  auto weight = [&](int i) -> int {  // units of sequence i's tiles (the host has seen to it that all fit 31 bits)
+  auto weight = [&](int i) -> int {  // units of sequence i's tiles (plan() leaves tiles whole where all could pass 31 bits)
     mine = Seq{0, 0, 0, 0};
     if (i >= a.B) return 0;
     mine = load_seq<KEYS>(a, i);
@@ -175,8 +175,8 @@ __global__ __launch_bounds__(64 * FW, 2) void flat_kernel(FlatArgs a, Parts ws) 
     before += __builtin_amdgcn_readlane(upto, 63);
   }
   int tiles = tiles_of(s.lq, a.G), un = a.whole ? 1 : units_of(a.window, a.sinks, a.tokens, s.lq, s.lk);
-  int th = (s0 - before) / un;  // tile and key head in the sequence, the head fastest
-  int j0 = (s0 - before) - th * un;
+  int th = (int)((uint32_t)(s0 - before) / (uint32_t)un);  // tile and key head in the sequence, the head fastest
+  int j0 = (int)((uint32_t)(s0 - before) - (uint32_t)th * (uint32_t)un);  // (0 .. un - 1, whatever the bounds hold)
   if ((uint32_t)th >= (uint32_t)(tiles * a.Hkv)) return;  // (bounds that decrease may overlap: more work than the host knows)
 
   SS_LDS uint8_t* ring = (SS_LDS uint8_t*)smem + wave * RING;
@@ -532,23 +532,27 @@ __global__ __launch_bounds__(256) void join_kernel(FlatArgs a, Parts ws) {
 
 // Workgroups of a call, and whether it leaves its tiles whole (then no workspace and one launch): rows over so few keys that
 // a workgroup's least run holds them (or so many rows and keys that their units may pass 31 bits). The lengths are not known
-// here: the rule goes by the room for keys.
+// here: the rules go by the room for keys, the mean of the sequences' (contiguous keys: one of them may have `most` of them, all
+// there are, and all the rows, so the sum is judged by that).
 struct Plan {
   int64_t wgs;
   bool whole;
   int rows;
 };
-inline Plan plan(int64_t Tq, int64_t room, int64_t B, int64_t G, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
-  const int64_t units = units_of((int)window, (int)sinks, tokens_of((int)G), (int)Tq, (int)std::min<int64_t>(room, 0x7FFFFF00));
+inline Plan plan(int64_t Tq, int64_t room, int64_t most, int64_t B, int64_t G, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
+  auto of = [&](int64_t keys) -> int64_t {
+    return units_of((int)window, (int)sinks, tokens_of((int)G), (int)Tq, (int)std::min<int64_t>(keys, 0x7FFFFF00));
+  };
+  const int64_t units = of(room);
   const int64_t tiles = (Tq * G / FM + std::min(B, Tq)) * Hkv, fits = 4 * (int64_t)num_cus_p();
-  const bool whole = units <= kMinUnits || (double)tiles * units >= 0x7FFF0000;
+  const bool whole = units <= kMinUnits || (double)tiles * of(most) >= 0x7FFF0000;
   const int64_t wgs = whole ? std::min<int64_t>(tiles, 4 * fits)
                             : std::min<int64_t>(fits, (int64_t)std::min<double>((double)tiles * units / kMinUnits + 1, 1e9));
   return {std::max<int64_t>(wgs, 1), whole, (int)std::min<int64_t>(FM, Tq * G)};
 }
 
-template <int DP, int KEYS> hipError_t launch(FlatArgs a, int64_t room, void* ws, hipStream_t st) {
-  const Plan p = plan(a.Tq, room, a.B, a.G, a.Hkv, a.D, a.window, a.sinks);
+template <int DP, int KEYS> hipError_t launch(FlatArgs a, int64_t room, int64_t most, void* ws, hipStream_t st) {
+  const Plan p = plan(a.Tq, room, most, a.B, a.G, a.Hkv, a.D, a.window, a.sinks);
   constexpr int lds = lds_bytes(DP);
   const hipError_t e = lds_limit((const void*)flat_kernel<DP, KEYS>, lds);
   if (e != hipSuccess) return e;
@@ -565,8 +569,9 @@ template <int DP, int KEYS> hipError_t launch(FlatArgs a, int64_t room, void* ws
 
 }  // namespace flat
 
-int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks) {
-  const flat::Plan p = flat::plan(Tq, room, B, Hq / Hkv, Hkv, D, window, sinks);
+int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t most, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                             int64_t sinks) {
+  const flat::Plan p = flat::plan(Tq, room, most, B, Hq / Hkv, Hkv, D, window, sinks);
   return p.whole ? 0 : p.wgs * ((int64_t)sizeof(flat::Record) + 2 * flat::FM * 4 + 2 * p.rows * D * 4);
 }
 
@@ -574,13 +579,13 @@ bool flat_fits(int64_t Tq, int64_t B, int64_t Hq, int64_t Hkv) {
   return (double)(Tq * (Hq / Hkv) / flat::FM + std::min(B, Tq)) * Hkv < 0x7FFF0000;
 }
 
-hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st) {
+hipError_t launch_flat(const FlatArgs& a, int64_t room, int64_t most, void* ws, hipStream_t st) {
   auto go = [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
-    if (!a.paged) return flat::launch<DP, flat::kRows>(a, room, ws, st);
-    if (a.page % 32 == 0) return flat::launch<DP, 32>(a, room, ws, st);
-    if (a.page % 16 == 0) return flat::launch<DP, 16>(a, room, ws, st);
-    return a.page % 8 == 0 ? flat::launch<DP, 8>(a, room, ws, st) : flat::launch<DP, flat::kAnyPages>(a, room, ws, st);
+    if (!a.paged) return flat::launch<DP, flat::kRows>(a, room, most, ws, st);
+    if (a.page % 32 == 0) return flat::launch<DP, 32>(a, room, most, ws, st);
+    if (a.page % 16 == 0) return flat::launch<DP, 16>(a, room, most, ws, st);
+    return a.page % 8 == 0 ? flat::launch<DP, 8>(a, room, most, ws, st) : flat::launch<DP, flat::kAnyPages>(a, room, most, ws, st);
   };
   return a.D <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }

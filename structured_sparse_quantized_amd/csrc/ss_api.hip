@@ -876,7 +876,7 @@ int64_t ss_attn_paged_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64
   if (Tq == 0 || B == 0 || Hq == 0 || Hkv == 0 || D == 0) return 0;
   if (Tq > 0x7FFFFFFF || B > 0x7FFFFFFF || Hq > 0xFFFF || D > 128 || Tq * (Hq / Hkv) > 0x7FFFFF00LL) return -1;
   window = window < kMostWindow ? window : kMostWindow;
-  return ss::flat_workspace_bytes(Tq, room, B, Hq, Hkv, D, window, window == 0 ? 0 : sinks < kMostWindow ? sinks : kMostWindow);
+  return ss::flat_workspace_bytes(Tq, room, room, B, Hq, Hkv, D, window, window == 0 ? 0 : sinks < kMostWindow ? sinks : kMostWindow);
 }
 
 ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_kv* cache, void* o, int64_t sot, int64_t soh,
@@ -900,7 +900,7 @@ ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_
   ss_paged_kv c;
   if ((s = check_paged(cache, Hkv, D, B, false, &c)) != SS_OK) return s;
   const int64_t room = c.table_cols * c.page;
-  const int64_t need = ss::flat_workspace_bytes(Tq, room, B, Hq, Hkv, D, window, sinks);
+  const int64_t need = ss::flat_workspace_bytes(Tq, room, room, B, Hq, Hkv, D, window, sinks);
   if ((s = check_workspace(workspace, ws_bytes, need)) != SS_OK) return s;
   ss::FlatArgs a{};
   a.q = static_cast<const uint16_t*>(q);
@@ -919,7 +919,7 @@ ss_status ss_attn_paged(const void* q, int64_t sqt, int64_t sqh, const ss_paged_
   a.window = (int)window;
   a.sinks = (int)sinks;
   a.paged = 1;
-  return hip_status(ss::launch_flat(a, room, need > 0 ? workspace : nullptr, (hipStream_t)stream), "ss_attn_paged launch");
+  return hip_status(ss::launch_flat(a, room, room, need > 0 ? workspace : nullptr, (hipStream_t)stream), "ss_attn_paged launch");
 }
 
 }  // extern "C"

@@ -188,8 +188,10 @@ struct FlatArgs {
   int paged;  // by table, else contiguous keys
   int whole, tokens;  // (set by the launch)
 };
-int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window, int64_t sinks);
+// room: the keys that a sequence has room for, on average; most: that any of them can have
+int64_t flat_workspace_bytes(int64_t Tq, int64_t room, int64_t most, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t window,
+                             int64_t sinks);
 bool flat_fits(int64_t Tq, int64_t B, int64_t Hq, int64_t Hkv);  // (tiles within 31 bits)
-hipError_t launch_flat(const FlatArgs& a, int64_t room, void* ws, hipStream_t st);
+hipError_t launch_flat(const FlatArgs& a, int64_t room, int64_t most, void* ws, hipStream_t st);
 
 }  // namespace ss
