@@ -33,6 +33,7 @@ namespace flat {
 using namespace attn;
 constexpr int FW = 2, FM = 32;          // waves, rows
 constexpr int kMinUnits = 4;            // a workgroup's run, at least
+constexpr int kMostWhole = 128;         // units of a tile that is left whole, at most
 constexpr int kJoin = 8;                // workgroups that share a cut tile's rows (14 rows: 8.1 us; 4: 11.4)
 
 __device__ const uint4 kZeros = {0, 0, 0, 0};
@@ -533,7 +534,10 @@ __global__ __launch_bounds__(256) void join_kernel(FlatArgs a, Parts ws) {
 // Workgroups of a call, and whether it leaves its tiles whole (then no workspace and one launch): rows over so few keys that
 // a workgroup's least run holds them (or so many rows and keys that their units may pass 31 bits). The lengths are not known
 // here: the rules go by the room for keys, the mean of the sequences' (contiguous keys: one of them may have `most` of them, all
-// there are, and all the rows, so the sum is judged by that).
+// there are, and all the rows). By the mean alone one sequence of 100000 keys among 1023 of 8 was walked by a workgroup a
+// tile (32 heads of 128 over 8, one token each: 3360 us, cut 223; one of 8000 among 80: 140 / 27, of 4000 among 40: 72 / 23);
+// cut whenever one could be long, short ones pay for the join (64 of 60 keys 7.4 us whole, 12.0 cut; of 1 to 128 keys 8.6 / 25;
+// 64 of 128 10.1 / 12.9, 256 of 60 28.2 / 22.8). So tiles stay whole while none can have more than kMostWhole units.
 struct Plan {
   int64_t wgs;
   bool whole;
@@ -545,7 +549,7 @@ inline Plan plan(int64_t Tq, int64_t room, int64_t most, int64_t B, int64_t G, i
   };
   const int64_t units = of(room);
   const int64_t tiles = (Tq * G / FM + std::min(B, Tq)) * Hkv, fits = 4 * (int64_t)num_cus_p();
-  const bool whole = units <= kMinUnits || (double)tiles * of(most) >= 0x7FFF0000;
+  const bool whole = (units <= kMinUnits && of(most) <= kMostWhole) || (double)tiles * of(most) >= 0x7FFF0000;
   const int64_t wgs = whole ? std::min<int64_t>(tiles, 4 * fits)
                             : std::min<int64_t>(fits, (int64_t)std::min<double>((double)tiles * units / kMinUnits + 1, 1e9));
   return {std::max<int64_t>(wgs, 1), whole, (int)std::min<int64_t>(FM, Tq * G)};

@@ -40,3 +40,13 @@ def test_sums_within_31_bits_are_cut():
     assert units([(64, 1, 8192)], 32, 8, 4096, 4) < 1 << 31
     assert ss.attn_window_workspace_bytes(64, 64 * 8192, 64, 32, 8, 128, 4096, 4) > 0
     assert ss.attn_window_workspace_bytes(64, 64 * 8192, 64, 32, 8, 128, 1 << 30, 4) > 0
+
+
+def test_short_sequences_are_cut_where_one_of_them_may_be_long():
+    """A tile stays whole, without a workspace, where the mean is at most 128 keys and no sequence can have more than 4096."""
+    import structured_sparse_quantized_amd as ss
+    need = lambda B, Tk, window, sinks=0: ss.attn_window_workspace_bytes(B, Tk, B, 32, 8, 128, window, sinks)  # noqa: E731
+    assert need(1024, 1023 * 8 + 100000, 1 << 20) > 0 and need(81, 80 * 8 + 8000, 9000) > 0
+    assert need(64, 64 * 60, 1 << 20) == 0 and need(1, 128, 4096) == 0 and need(16, 16 * 128, 4096) == 0
+    assert need(1024, 1023 * 8 + 100000, 3000, 4) == 0  # the window keeps tiles short, whatever the lengths
+    assert need(64, 64 * 200, 1 << 20) > 0
