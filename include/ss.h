@@ -510,12 +510,15 @@ ss_status ss_attn_window(const void* q, int64_t sqt, int64_t sqh, const void* k,
 /* ss_rmsnorm_act -- what stands before a layer's products: the residual's addition, the root-mean-square norm, and the
  * preparation of the product's activations, in one pass.
  *   r[m][k] = X[m][k] + residual[m][k], rounded to x_dt and written to sum; without a residual r = X
- *   rs[m] = fl32(1 / sqrt(mean_k r^2 + eps)), the mean and the root in float64
+ *   rs[m] = fl32(1 / sqrt(mean_k r^2 + eps)), the mean and the root in float64; beyond float32 its largest number
  *   z[m][k] = fl32(fl32(r rs) w[k]); w NULL: fl32(r rs)
  * and of the row z: y_dt BF16: Y [M][K], rounded once (n must be 2, sx NULL; ss_prune24_act reads it); I8 or FP8E4M3: codes
  * and scales sx[M] = fl32(a / Q), lifted to Y [M][Kc], Kc = ss_lifted_k(K, n), as ss_quant_lift_act(z, n) gives them but for
  * inv = fl32(fl32(1 / a) Q), which is what a norm and a quantiser of elementwise tensor operations compute: the codes are
  * theirs, and a step from ss_quant_lift_act's where a value lies within 2^-23 of a border. A row of zeros gives zeros.
+ * What is not finite stays so (finite x and residual may add up to it): a NaN of r is a NaN all over its row z, an infinity one
+ * in its place, zeros elsewhere; a row whose z holds a NaN or an infinity has codes of zero and that scale, which make
+ * its products NaN.
  * X, residual, sum [M][K] (F32 or BF16; ldx, ldr, lds elements); sum may be X or residual (the same leading dimension), and is
  * required with a residual; otherwise sum and Y overlap nothing. w [K]: F32 or x_dt. eps finite and >= 0. */
 ss_status ss_rmsnorm_act(const void* X, ss_dtype x_dt, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,

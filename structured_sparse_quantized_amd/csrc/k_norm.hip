@@ -66,23 +66,37 @@ template <int BT> __device__ __forceinline__ double block_sum(double v, double* 
   }
   return v;
 }
+// (the greater one; a NaN where either is one, unlike fmaxf)
+__device__ __forceinline__ float greater(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 template <int BT> __device__ __forceinline__ float block_top(float v, float* red) {
 #pragma unroll
-  for (int o = BT < 64 ? BT / 2 : 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  for (int o = BT < 64 ? BT / 2 : 32; o >= 1; o >>= 1) v = greater(v, __shfl_xor(v, o, 64));
   if constexpr (BT > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     lds_barrier();
     v = red[0];
 #pragma unroll
-    for (int i = 1; i < BT / 64; ++i) v = fmaxf(v, red[i]);
+    for (int i = 1; i < BT / 64; ++i) v = greater(v, red[i]);
   }
   return v;
 }
-// 1 / sqrt(mean + eps), or 0 for a row of zeros without eps (its z are zeros, not 0 * infinity)
+// 1 / sqrt(mean + eps), float32's largest number where it is beyond that, or 0 for a row of zeros without eps (its z are zeros,
+// not 0 * infinity). Of a NaN: NaN; of an infinity: 0, so z is NaN there.
 __device__ __forceinline__ float inverse_root(double sum, int64_t K, double eps) {
-  const double m = sum / (double)K + eps;
-  return m > 0.0 ? (float)fmin(1.0 / sqrt(m), 3.4028234663852886e38) : 0.0f;
+  const double m = sum / (double)K + eps, r = 1.0 / sqrt(m);
+  return m == 0.0 ? 0.0f : r > 3.4028234663852886e38 ? 3.4028234663852886e38f : (float)r;
 }
+// The scale of a row whose largest |z| is `top`, and what z is multiplied with (two roundings: the header). A row with a NaN or an
+// infinity among its z has codes of zero and that scale, so that its products are NaN and not those of an empty row.
+template <typename Qz> struct Scale {
+  bool zero;  // all codes are
+  float inv, sx;
+  __device__ explicit Scale(float top) {
+    zero = !(top > 0.0f && top < INFINITY);
+    inv = zero ? 0.0f : 1.0f / top * Qz::Q;
+    sx = top == 0.0f ? 0.0f : top / Qz::Q;
+  }
+};
 
 // The lift of a row of codes staged in LDS (zero behind K): whole periods of its byte pattern per thread.
 template <int N, int BT> __device__ __forceinline__ void lift_row(const uint8_t* codes, uint8_t* out, int Kc, int tid) {
@@ -217,11 +231,11 @@ __global__ __launch_bounds__(BT * rows_of<BT>()) void row_kernel(NormArgs a) {
   } else {
     float top = fabsf(zt);
 #pragma unroll
-    for (int i = 0; i < VPT * E; ++i) top = fmaxf(top, fabsf(z[i]));
-    top = block_top<BT>(top, red_top);
-    const bool zero = top == 0.0f;
-    const float inv = zero ? 0.0f : 1.0f / top * Qz::Q;  // (two roundings: the header)
-    if (tid == 0) a.sx[row] = zero ? 0.0f : top / Qz::Q;
+    for (int i = 0; i < VPT * E; ++i) top = greater(top, fabsf(z[i]));
+    const Scale<Qz> scale(block_top<BT>(top, red_top));
+    const bool zero = scale.zero;
+    const float inv = scale.inv;
+    if (tid == 0) a.sx[row] = scale.sx;
     auto four = [&](int i) -> uint32_t { return zero ? 0u : Qz::pack4(z[i], z[i + 1], z[i + 2], z[i + 3], inv); };
     uint8_t* q = static_cast<uint8_t*>(a.y) + row * a.ldy;
     const int Kc = (int)a.Kc, n = a.n;
@@ -291,11 +305,11 @@ template <typename T, typename TW, int OUT> __global__ __launch_bounds__(1024) v
     for (int64_t k = tid; k < a.K; k += BT) y[k] = (uint16_t)pack_bf16x2(z(k), 0.0f);
   } else {
     float top = 0.0f;
-    for (int64_t k = tid; k < a.K; k += BT) top = fmaxf(top, fabsf(z(k)));
-    top = block_top<BT>(top, red_top);
-    const bool zero = top == 0.0f;
-    const float inv = zero ? 0.0f : 1.0f / top * Qz::Q;  // (two roundings: the header)
-    if (tid == 0) a.sx[row] = zero ? 0.0f : top / Qz::Q;
+    for (int64_t k = tid; k < a.K; k += BT) top = greater(top, fabsf(z(k)));
+    const Scale<Qz> scale(block_top<BT>(top, red_top));
+    const bool zero = scale.zero;
+    const float inv = scale.inv;
+    if (tid == 0) a.sx[row] = scale.sx;
     uint8_t* q = static_cast<uint8_t*>(a.y) + row * a.ldy;
     const int64_t gb = 4 * (a.n - 1);  // output bytes per group of 2n
     for (int64_t c = tid; c < a.Kc; c += BT) {
