@@ -529,6 +529,9 @@ template <int DP> hipError_t launch_prompt(const AttnArgs& a, hipStream_t st) {
 // maximum, as the scores themselves are) that join_kernel adds in order.
 // Measured: 64 caches of 4096 keys on average (32 heads of 128 over 8): 240 us, 5.0 TB/s, a large copy's rate on this card
 // (4.9); one cache of 4000: 6.5 us here and 3 in the join, both chains of latencies (lengths, keys, LDS, parts).
+// Calls under a window go to flat_kernel (k_attn_flat.hip), whose runs follow the lengths; without one they are quicker here,
+// but for many long caches: one of 4000 keys 9.0 us (there 14.3), 16 of 2000 27.5 (33.1), 256 of 500 on average 105
+// (156), 64 of 4096 217 (209).
 // Short chunks of tokens over a long cache come here too, several tiles of 32 rows to a sequence (few_rows).
 constexpr int FW = 2, FR = 2, FM = 32;  // waves, units in a wave's ring, rows
 constexpr int kMaxParts = 32;           // workgroups that share a tile's keys

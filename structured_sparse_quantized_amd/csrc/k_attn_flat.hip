@@ -3,23 +3,32 @@
 //   key), j <= p and, under a window w with s first tokens, j > p - w or j < s.
 //
 // Mathematics, matrix instructions and LDS tiles are those of the packed attention (k_attn.hip): tiles of 32 rows, the (token,
-// head) pairs of a sequence that share a key head; units of 32 keys; one pass with a running maximum and sum.
+// head) pairs of a sequence that share a key head; units of 32 keys; one pass with a running maximum and sum. Scores, maxima,
+// sums, results and parts are float32; the powers are rounded to bf16, which the second product's matrix instruction takes
+// (their sum is of the unrounded ones): 2^-8 of each at most. A result's error is 0.0021-0.0023 of its size, 0.0016 of which is
+// its own rounding.
 //
 // Split. Such calls read every seen key and value once for a handful of rows (HBM bound), and lengths differ from sequence to
-// sequence. So the work is laid out flat: the units of all tiles one after the other, and each of the launch's workgroups
-// (as many as the chip holds at once) takes an equal run of them, whatever tile that begins and ends in. The lengths are in
-// device memory, so the workgroups find their runs themselves, by a sum over the sequences. A tile that lies whole in a run is
-// finished there; of one that is cut, each workgroup leaves a part (float32, normalised, with its row's log2 of the sum),
-// a run's first tile in one place and its last in another, and join_kernel adds the parts in order.
+// sequence. So the work is laid out flat: the units of all tiles one after the other, and each of the launch's workgroups (as
+// many as the chip holds at once) takes an equal run of them, whatever tile that begins and ends in. The lengths are in device
+// memory, so the workgroups find their runs themselves, by a sum over the sequences, 64 a step (one token each, all but 16 of
+// 1024 empty: 63 us, the 16 alone 33; all but 2 of 2048: 78, alone 17; 1024 of 500 keys on average 439 us, 4.8 TB/s). A tile
+// that lies whole in a run is finished there; of one that is cut, each workgroup leaves a part (float32, normalised, with its
+// row's log2 of the sum), a run's first tile in one place and its last in another, and join_kernel adds the parts in order.
 //
-// Loads. A unit is loaded to registers while the unit before it is computed, and goes to LDS when that is done (loads to LDS
-// without registers, from addresses of each lane, gave wrong parts now and then where a unit in flight was cut). Each of 32 lanes looks up the page of one key, a unit ahead. A load covers 4 rows of heads of 128, or 8 of 64:
-// where page sizes are multiples of that, its address is a scalar, where 32 divides them one for the unit; other sizes take
-// addresses of each lane (16 times 30 instructions a unit more). Values of keys that no row of the tile sees (behind the end, outside the window, of entries that
-// name no page) are replaced by zeros, so whatever they hold stays out of the product.
-// Measured (32 heads of 128 over 8): 64 tokens over 262144 keys in pages of 16, lengths 1 to 8192: 193 us and 9 in the join, 5.3 TB/s; one
-// token over 4000 keys 12 us and 4: the chain lengths, run, table, keys, parts, and instructions fetched cold. 4 units at
-// least to a run (one token 15.9 us a call; 2: 16.8, 8: 17.1), 4 workgroups a CU (64 caches 199 us; 3: 201, 2: 207, 8: 203).
+// Loads. A unit is loaded to registers while the unit before it is computed, and goes to LDS when that is done. (Loads to LDS
+// without registers, from addresses of each lane, gave wrong parts now and then where the unit in flight was cut. Why was not
+// found: the unit that was read had landed by then, for that loop waited for all loads, the table's among them, at its end. The
+// packed attention's loads to LDS, by a resource and scalar places, differ in no call: tests/test_gpu_attn_repeat.py.) Each of
+// 32 lanes looks up the page of one key, a unit ahead. A load covers 4 rows of heads of 128, or 8 of 64: where page sizes are
+// multiples of that, its address is a scalar, where 32 divides them one for the unit; other sizes take addresses of each lane
+// (16 times 30 instructions a unit more). Values of keys that no row of the tile sees (behind the end, outside the window, of
+// entries that name no page) are replaced by zeros, so whatever they hold stays out of the product.
+// Measured (32 heads of 128 over 8): 64 tokens over 262144 keys in pages of 16, lengths 1 to 8192: 193 us and 9 in the join,
+// 5.3 TB/s; one token over 4000 keys 12 us and 4: the chain lengths, run, table, keys, parts, and instructions fetched cold. 4
+// units at least to a run (one token 15.9 us a call; 2: 16.8, 8: 17.1), 4 workgroups a CU (64 caches 199 us; 3: 201, 2: 207, 8:
+// 203; of heads of 64 a CU holds six: 64 of 500 keys 36.5 us in four, 29.8 in six, 1024 of 2000 792 / 774, 2 of 20000 23.5 /
+// 25.0).
 #include <math.h>
 
 #include <algorithm>
